@@ -13,6 +13,9 @@ the computation runs in the library's HIP kernels; there is no fallback.
     ins    = mixer_prep(xq, xk, xv, xb, xw, xa, conv_q, conv_k, conv_v)  # q, k, v, b, w, log_alpha
     y      = mixer_out(o, z, gamma)                            # RMS norm and SiLU output gate
 
+The calls of a state space block beside it (its scan, short convolution and layer norm) are
+listed in ``block``, and imported here.
+
 Layouts: q, k, b, log_alpha [B,T,H,dk]; v, w, o [B,T,H,dv]; state [B,H,dk,dv]
 (packed: [total_T,H,d] with int64 offsets cu_seqlens [N+1] and states [N,H,dk,dv];
 decode: [N,H,d] and the same states).  q, k, v, b, w are bf16 or fp32 (all the same);
@@ -85,6 +88,7 @@ def _load():
         lib.gdn2_mixer_prep.restype = I32
         lib.gdn2_mixer_out.argtypes = [P] * 4 + [I64] * 4 + [ctypes.c_float, I32, I32, P]
         lib.gdn2_mixer_out.restype = I32
+        block._declare(lib)
         lib.gdn2_supported.argtypes = [I32, I64, I64, I32]
         lib.gdn2_supported.restype = I32
         lib.gdn2_status_string.argtypes = [I32]
@@ -99,7 +103,7 @@ def version() -> str:
 
 
 def supported(which: str, dk: int, dv: int, dtype: torch.dtype) -> bool:
-    w = {"chunk_fwd": 0, "decode_step": 1, "chunk_bwd": 2, "mixer": 3}[which]
+    w = {"chunk_fwd": 0, "decode_step": 1, "chunk_bwd": 2, "mixer": 3, "ssm": 5}[which]
     return bool(_load().gdn2_supported(w, dk, dv, _DTYPES[dtype]))
 
 
@@ -441,3 +445,9 @@ def mixer_out(o, z, gamma, eps=1e-6, *, y=None):
     if st != 0:
         raise Gdn2Error("gdn2_mixer_out", st, _load().gdn2_status_string(st).decode())
     return y
+
+
+from . import block  # noqa: E402  (it uses the helpers above)
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__

@@ -11,27 +11,17 @@
 #include <mutex>
 
 #include "../../include/gdn2.h"
+#include "gdn2_check.h"
 #include "gdn2_launch.h"
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using gdn2::mul_ok;
+using gdn2::overlap;
+using gdn2::Range;
+using gdn2::range_of;
 
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void* p, int64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + static_cast<uintptr_t>(bytes)};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > INT64_MAX / a) return false;
-    *out = a * b;
-    return true;
-}
+bool aligned16(const void* p) { return gdn2::aligned_to(p, 16); }
 
 bool chunk_supported(int64_t dk, int64_t dv, gdn2_dtype_t dt) {
     if (dt == GDN2_DTYPE_BF16) return (dk == 128 && dv == 128) || (dk == 64 && dv == 64);
@@ -437,6 +427,7 @@ gdn2_status_t gdn2_mixer_out(const void* o, const void* z, const float* gamma, v
 
 int gdn2_supported(int which, int64_t dk, int64_t dv, gdn2_dtype_t dtype) {
     if (which == 3) return mixer_supported(dk, dv, dtype) ? 1 : 0;
+    if (which == 5) return gdn2::ssm_supported(dk, dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32) ? 1 : 0;
     if (which == 0 || which == 2) return chunk_supported(dk, dv, dtype) ? 1 : 0;
     if (which == 1) return decode_supported(dk, dv, dtype) ? 1 : 0;
     return 0;

@@ -163,6 +163,28 @@ __device__ __forceinline__ Vec<T, N> load_vec(const T* p) {
     return r;
 }
 
+// N consecutive elements at any element address: rows whose length or stride is no whole number of
+// 16-byte units.  Global memory takes vector accesses at element alignment; where the addresses
+// happen to be aligned they cost what load_vec costs.
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> load_vec_any(const T* p) {
+    typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    const V x = *reinterpret_cast<const V*>(p);
+    Vec<T, N> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.v[i] = x[i];
+    return r;
+}
+// N fp32 values stored as T, at any element address
+template <typename T, int N>
+__device__ __forceinline__ void store_vec_any(T* p, const float (&f)[N]) {
+    typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    V x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = from_f32<T>(f[i]);
+    *reinterpret_cast<V*>(p) = x;
+}
+
 // exp(x) for x <= 0 through the hardware base-2 exponential
 __device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 

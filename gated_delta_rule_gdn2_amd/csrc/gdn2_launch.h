@@ -122,6 +122,84 @@ struct MixerOutArgs {
     void* stream;
 };
 
+// The selective state space scan and its single-token step.
+struct SsmArgs {
+    const void* x;          // [tokens, H, dv], token stride x_stride
+    const void* dt;         // [tokens, H], token stride dt_stride
+    const void* b;          // [tokens, G, dk], token stride b_stride
+    const void* c;          // [tokens, G, dk], token stride c_stride
+    const float* A;         // [H]
+    const float* D;         // [H] or nullptr
+    const float* dt_bias;   // [H] or nullptr
+    const float* initial_state;  // [N, H, dk, dv] or nullptr (the step: unused)
+    void* y;                // [tokens, H, dv], contiguous
+    float* final_state;     // [N, H, dk, dv] or nullptr (the step: the state, in place)
+    int64_t N;              // sequences
+    int64_t T;              // tokens of each, or with cu_seqlens the packed total
+    int64_t H, G, dk, dv;
+    int64_t x_stride, dt_stride, b_stride, c_stride;  // elements between tokens
+    bool dtype_bf16, softplus;
+    const int64_t* cu_seqlens;  // N + 1 offsets (device memory), or nullptr
+    void* stream;
+    int cus;
+};
+
+// The causal depthwise convolution of four taps with bias and SiLU.
+struct ConvArgs {
+    const void* x;               // [tokens, C], token stride x_stride
+    const float* taps;           // [C][4]
+    const float* bias;           // [C] or nullptr
+    const void* initial_state;   // [N, 3, C] or nullptr (zeros)
+    void* y;                     // [tokens, C], contiguous
+    void* final_state;           // [N, 3, C] or nullptr; may be initial_state
+    int64_t N, T, C, x_stride;   // T: tokens of each sequence, or with cu_seqlens the packed total
+    bool dtype_bf16;
+    const int64_t* cu_seqlens;
+    void* stream;
+};
+
+struct NormArgs {
+    const void* x;       // [rows, width]
+    const float* gamma;  // [width]
+    const float* beta;   // [width] or nullptr
+    void* y;
+    float* mean;         // [rows] or nullptr (with rstd)
+    float* rstd;
+    int64_t rows, width;
+    bool dtype_bf16;
+    float eps;
+    void* stream;
+};
+
+struct NormBwdArgs {
+    const void* dy;
+    const void* x;
+    const float* gamma;
+    const float* mean;
+    const float* rstd;
+    void* dx;
+    float* dgamma;  // [width]
+    float* dbeta;   // [width] or nullptr
+    float* parts;   // workspace of norm_bwd_workspace_bytes
+    int64_t rows, width;
+    bool dtype_bf16;
+    void* stream;
+};
+
+// head sizes and dtypes that the scan and its step are built for
+inline bool ssm_supported(int64_t dk, int64_t dv, bool bf16, bool f32) {
+    return (bf16 || f32) && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
+}
+// bytes of the workspace with which sequences are walked in segments (0: whole)
+size_t ssm_workspace_bytes(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf16_in, int64_t cus);
+hipError_t launch_ssm_fwd(const SsmArgs& a, void* workspace);
+hipError_t launch_ssm_step(const SsmArgs& a);
+hipError_t launch_short_conv(const ConvArgs& a);
+hipError_t launch_short_conv_step(const ConvArgs& a);
+hipError_t launch_layer_norm(const NormArgs& a);
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t width);
+hipError_t launch_layer_norm_bwd(const NormBwdArgs& a);
+
 // dvs: value columns per workgroup slice (16, 32 or 64)
 hipError_t launch_chunk_fwd(const ChunkArgs& a, int dvs);
 // The forward in two kernels (chunk-local records, then the state pass), bf16 inputs with

@@ -21,7 +21,8 @@
  * gates enter the gradient inner products, so the backward is derived with
  * them), a single-token recurrent decode step (the page's opening section:
  * decoding keeps a constant-size state), and the mixer's fused elementwise
- * passes on either side of the recurrence.
+ * passes on either side of the recurrence.  Beside them stand the calls of a
+ * state space block (its scan, convolution and norm), described with them below.
  *
  * Conventions for every call:
  *   - Tensor pointers are DEVICE pointers (HIP global memory) of the current
@@ -348,9 +349,171 @@ gdn2_status_t gdn2_mixer_out(const void* o, const void* z, const float* gamma, v
                              int64_t T, int64_t H, int64_t dv, float eps, gdn2_dtype_t dtype,
                              gdn2_dtype_t o_dtype, void* stream);
 
+/*
+ * The state space block.  Hybrid stacks put selective state space layers beside
+ * the layers above (page "GDN-2-3B", orcarouter.ai: a listed stack of 52 layers
+ * holds 23 of them).  Such a layer is a layer norm, projections (the caller's),
+ * a short causal convolution with SiLU, the scan, and gdn2_mixer_out on the
+ * scan's output.  These calls follow the conventions at the top; beyond them:
+ *   - x, b, c and dt may have a token stride of their own, so that they can be
+ *     parts of one wider tensor; a token's own elements are contiguous, and so
+ *     is every output.
+ *   - Each is built for dtype BF16 and F32, and its outputs have that dtype; A,
+ *     D, biases, taps, norm weights, statistics and scan states are float32.
+ */
+
+/*
+ * gdn2_ssm_fwd -- the selective state space scan over B sequences of T tokens.
+ * Per sequence and head, with a state S of dk rows and dv columns:
+ *
+ *   dt_t = softplus(raw_t + dt_bias)          (raw_t + dt_bias if softplus = 0)
+ *   S_t  = exp(dt_t A) S_{t-1} + dt_t b_t x_t^T,   y_t = S_t^T c_t + D x_t
+ *
+ *   x             [B, T, H, dv]  dtype    x_stride elements between tokens
+ *   dt            [B, T, H]      dtype    raw time steps, dt_stride
+ *   b, c          [B, T, G, dk]  dtype    shared by the H / G heads of a group:
+ *                                         head h takes group h / (H / G);
+ *                                         b_stride, c_stride
+ *   A             [H]            float32  expected < 0
+ *   D, dt_bias    [H]            float32  each NULL for zeros
+ *   initial_state [B, H, dk, dv] float32  or NULL for zeros
+ *   y             [B, T, H, dv]  dtype    out
+ *   final_state   [B, H, dk, dv] float32  out, or NULL to skip; may be the same
+ *                                         pointer as initial_state
+ *
+ * Token t of sequence n starts at element (n T + t) * stride of its tensor.
+ * Built for dk and dv of 64 or 128 each.  The strides are at least a token's
+ * elements and below 2^22; x_stride, b_stride and c_stride are whole 16-byte
+ * units; H is a multiple of G, and H * dv is below 2^22 (GDN2_ERR_SHAPE, or
+ * GDN2_ERR_MISALIGNED).  dt needs the alignment of its elements only.  Pairs of
+ * tokens are formed in chunks of 64, with zeros for the pairs of a later token:
+ * a NaN or an infinity in x, b, c or dt makes the outputs of its whole chunk
+ * undefined, those of earlier tokens among them.
+ * With workspace = NULL and workspace_bytes = 0 every sequence is walked whole.
+ * With a workspace of gdn2_ssm_fwd_workspace_bytes bytes (256-byte aligned,
+ * overlapping no argument) sequences are cut into segments that are walked in
+ * parallel.  A shorter workspace, or one where that call says 0, returns
+ * GDN2_ERR_WORKSPACE.
+ */
+gdn2_status_t gdn2_ssm_fwd(const void* x, const void* dt, const void* b, const void* c,
+                           const float* A, const float* D, const float* dt_bias,
+                           const float* initial_state, void* y, float* final_state, int64_t B,
+                           int64_t T, int64_t H, int64_t G, int64_t dk, int64_t dv,
+                           int64_t x_stride, int64_t dt_stride, int64_t b_stride, int64_t c_stride,
+                           gdn2_dtype_t dtype, int softplus, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* The workspace with which gdn2_ssm_fwd is fastest for these sizes on the
+ * current device: 0 where the (sequence, head) chains fill it by themselves. */
+size_t gdn2_ssm_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv,
+                                    gdn2_dtype_t dtype);
+
+/*
+ * gdn2_ssm_fwd_varlen -- the scan over N sequences packed along one token axis:
+ * tensors as above with [total_T, ...] for [B, T, ...] and states [N, H, dk, dv];
+ * cu_seqlens as for gdn2_chunk_fwd_varlen (int64 [N + 1] in device memory, each
+ * range clamped into [0, total_T]; tokens of no sequence are left as they were
+ * in y; an empty sequence hands its initial state on).
+ */
+gdn2_status_t gdn2_ssm_fwd_varlen(const void* x, const void* dt, const void* b, const void* c,
+                                  const float* A, const float* D, const float* dt_bias,
+                                  const float* initial_state, void* y, float* final_state,
+                                  const int64_t* cu_seqlens, int64_t N, int64_t total_T, int64_t H,
+                                  int64_t G, int64_t dk, int64_t dv, int64_t x_stride,
+                                  int64_t dt_stride, int64_t b_stride, int64_t c_stride,
+                                  gdn2_dtype_t dtype, int softplus, void* stream);
+
+/* gdn2_ssm_step -- one token for each of N sequences: x [N, H, dv], dt [N, H],
+ * b, c [N, G, dk], y [N, H, dv]; state [N, H, dk, dv] is updated in place. */
+gdn2_status_t gdn2_ssm_step(const void* x, const void* dt, const void* b, const void* c,
+                            const float* A, const float* D, const float* dt_bias, float* state,
+                            void* y, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv,
+                            int64_t x_stride, int64_t dt_stride, int64_t b_stride, int64_t c_stride,
+                            gdn2_dtype_t dtype, int softplus, void* stream);
+
+/*
+ * gdn2_short_conv -- a causal depthwise convolution of four taps, with bias and
+ * SiLU, that keeps its last inputs: gdn2_mixer_prep's convolution for channels
+ * of any split and for sequences that go on.
+ *
+ *   y[t, i] = SiLU(bias[i] + sum_j taps[i, j] x[t - 3 + j, i]),  j = 0 .. 3
+ *
+ *   x             [B, T, C]  dtype    x_stride elements between tokens
+ *   taps          [C, 4]     float32  (three taps: a first tap of zero)
+ *   bias          [C]        float32  or NULL for zeros
+ *   initial_state [B, 3, C]  dtype    the three inputs before the first token,
+ *                                     oldest first; NULL for zeros
+ *   y             [B, T, C]  dtype    out
+ *   final_state   [B, 3, C]  dtype    out: the last three inputs, those of
+ *                                     initial_state among them where T < 3; NULL
+ *                                     to skip; may be the same pointer as
+ *                                     initial_state
+ *
+ * C is a multiple of 8 below 2^22, x_stride at least C and below 2^22.  x and
+ * its tokens need the alignment of their elements only.
+ */
+gdn2_status_t gdn2_short_conv(const void* x, const float* taps, const float* bias,
+                              const void* initial_state, void* y, void* final_state, int64_t B,
+                              int64_t T, int64_t C, int64_t x_stride, gdn2_dtype_t dtype,
+                              void* stream);
+
+/* gdn2_short_conv_varlen -- the same over N packed sequences: x, y [total_T, C],
+ * states [N, 3, C], cu_seqlens as for gdn2_ssm_fwd_varlen (offsets that decrease
+ * leave the tokens between them unspecified). */
+gdn2_status_t gdn2_short_conv_varlen(const void* x, const float* taps, const float* bias,
+                                     const void* initial_state, void* y, void* final_state,
+                                     const int64_t* cu_seqlens, int64_t N, int64_t total_T,
+                                     int64_t C, int64_t x_stride, gdn2_dtype_t dtype, void* stream);
+
+/* gdn2_short_conv_step -- one token for each of N sequences: x, y [N, C]; state
+ * [N, 3, C] is updated in place. */
+gdn2_status_t gdn2_short_conv_step(const void* x, const float* taps, const float* bias, void* state,
+                                   void* y, int64_t N, int64_t C, int64_t x_stride,
+                                   gdn2_dtype_t dtype, void* stream);
+
+/*
+ * gdn2_layer_norm -- y = (x - mean) rstd gamma + beta over rows of `width`, with
+ * rstd = 1 / sqrt(mean((x - mean)^2) + eps).
+ *
+ *   x, y        [rows, width]  dtype    y must not overlap an input
+ *   gamma       [width]        float32
+ *   beta        [width]        float32  or NULL for zeros
+ *   mean, rstd  [rows]         float32  out, for the backward pass; both NULL to
+ *                                       skip
+ *
+ * width may be any value from 1 to 16384, rows any from 0 on.  eps >= 0.
+ */
+gdn2_status_t gdn2_layer_norm(const void* x, const float* gamma, const float* beta, void* y,
+                              float* mean, float* rstd, int64_t rows, int64_t width, float eps,
+                              gdn2_dtype_t dtype, void* stream);
+
+/* Bytes of device workspace that gdn2_layer_norm_bwd needs: partial sums of
+ * dgamma and dbeta.  0 if the sizes are out of range. */
+size_t gdn2_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
+
+/*
+ * gdn2_layer_norm_bwd -- gradients of sum(dy * y) for gdn2_layer_norm.
+ *
+ *   dy, x       [rows, width]  dtype
+ *   gamma       [width]        float32
+ *   mean, rstd  [rows]         float32  as the forward pass gave them
+ *   dx          [rows, width]  dtype    out; may not overlap an input
+ *   dgamma      [width]        float32  out
+ *   dbeta       [width]        float32  out, or NULL to skip
+ *   workspace   16-byte aligned, overlapping no argument
+ *
+ * The sums over rows are formed in a fixed order: equal calls give equal bits.
+ * With rows = 0 dgamma and dbeta are zeros.
+ */
+gdn2_status_t gdn2_layer_norm_bwd(const void* dy, const void* x, const float* gamma,
+                                  const float* mean, const float* rstd, void* dx, float* dgamma,
+                                  float* dbeta, void* workspace, size_t workspace_bytes,
+                                  int64_t rows, int64_t width, gdn2_dtype_t dtype, void* stream);
+
 /* 1 if gdn2_chunk_fwd and gdn2_chunk_fwd_varlen (which = 0), gdn2_decode_step
- * (which = 1), gdn2_chunk_bwd (which = 2) or gdn2_mixer_prep and gdn2_mixer_out
- * (which = 3) support (dk, dv, dtype), else 0. */
+ * (which = 1), gdn2_chunk_bwd (which = 2), gdn2_mixer_prep and gdn2_mixer_out
+ * (which = 3) or gdn2_ssm_fwd, gdn2_ssm_fwd_varlen and gdn2_ssm_step (which = 5)
+ * support (dk, dv, dtype), else 0. */
 int gdn2_supported(int which, int64_t dk, int64_t dv, gdn2_dtype_t dtype);
 
 /* Static, NUL-terminated description of a status code. */
