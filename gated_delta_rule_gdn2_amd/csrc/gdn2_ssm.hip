@@ -1,80 +1,418 @@
 // gdn2_ssm.hip -- the selective state space scan over prompts, and its step for single tokens.
 //
 // Per sequence and head, with a state S of dk rows and dv columns:
-//   dt_t = softplus(raw_t + bias),  S_t = exp(dt_t A) S_{t-1} + dt_t B_t x_t^T,
-//   y_t = S_t^T C_t + D x_t
-// B and C belong to a group of heads.  The columns of S are independent.
+//   dt_t = softplus(raw_t + bias),  S_t = exp(dt_t A) S_{t-1} + dt_t b_t x_t^T,
+//   y_t = S_t^T c_t + D x_t
+// b and c belong to a group of heads; the columns of S are independent.
+//
+// In a chunk of 64 tokens with the state S that enters it and cum_i = sum_{s<=i} dt_s A:
+//   M[i,j] = (c_i . b_j) exp(cum_i - cum_j) dt_j   (j <= i, else 0)
+//   y_i    = exp(cum_i) S^T c_i + sum_j M[i,j] x_j + D x_i
+//   S'     = exp(cum_63) S + sum_j b_j (exp(cum_63 - cum_j) dt_j x_j)^T
+// All four products run on the matrix units.
+#include "gdn2_bf16_ops.h"
 #include "gdn2_device.h"
 #include "gdn2_launch.h"
 
 namespace gdn2 {
 namespace ssm {
 
-// raw + bias, through softplus where asked: max(v, 0) + log(1 + e^-|v|)
+constexpr int Q = 64;   // tokens of a chunk
+constexpr int PS = 64;  // state columns of a workgroup: 16 per wave
+
+typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+
+// raw + bias, through softplus where asked: max(v, 0) + log(1 + e^-|v|).  The library's log1p and
+// exp: once per token and head, and final states keep their fp32 accuracy.
 __device__ __forceinline__ float time_step(float v, bool softplus) {
     return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
 }
 
-// A workgroup walks 64 columns of one (sequence, head) token by token; wave w holds a quarter of
-// the rows, a lane one column of them.
-template <typename T, int DK>
-__global__ __launch_bounds__(256) void walk_kernel(const T* __restrict__ x, const T* __restrict__ dt,
-                                                   const T* __restrict__ bm, const T* __restrict__ cm,
-                                                   const float* __restrict__ A, const float* __restrict__ D,
-                                                   const float* __restrict__ dt_bias, const float* s0,
-                                                   T* __restrict__ y, float* sT, const int64_t* __restrict__ cu,
-                                                   int64_t T_, int H, int G, int dv, int64_t xs, int64_t dts,
-                                                   int64_t bs, int64_t cs, bool softplus) {
-    constexpr int R = DK / 4;
-    __shared__ float part[2][4][64];
-    const int slices = dv / 64, slice = blockIdx.x % slices;
-    const int h = (blockIdx.x / slices) % H, n = blockIdx.x / slices / H;
-    const int g = h / (H / G), w = threadIdx.x >> 6, lane = threadIdx.x & 63, p = slice * 64 + lane;
-    int64_t lo = n * T_, hi = lo + T_;
-    if (cu) {
-        lo = min(max(cu[n], (int64_t)0), T_);
-        hi = min(max(cu[n + 1], lo), T_);
+// ---- LDS tiles ------------------------------------------------------------------------------
+// [64 tokens][W] row-major, in 16-byte units whose place in the row is XORed with a function of
+// the row.  Three patterns read them: 16 rows at one unit (products over W), 8 rows at one pair of
+// units (the transposing read of products over tokens), 16 rows at half a unit; with this
+// function each touches every bank once.
+template <typename T, int W>
+struct Tile {
+    static constexpr int UPR = W * (int)sizeof(T) / 16;  // units per row
+    static constexpr int EPU = 16 / (int)sizeof(T);      // elements per unit
+    __device__ static __forceinline__ int swz(int row) {
+        if constexpr (UPR >= 16) return ((row & 7) << 1) | ((row >> 3) & 1);
+        else return (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
     }
-    float s[R];
-    const int64_t base = (((int64_t)n * H + h) * DK + w * R) * dv + p;
+    __device__ static __forceinline__ int at(int row, int col) {
+        return (row * UPR + ((col / EPU) ^ swz(row))) * EPU + col % EPU;
+    }
+};
+
+// operand of a product over W: row `row`, elements col .. col + 7
+template <int W>
+__device__ __forceinline__ Frag<bf16> rows_contig(const bf16* t, int row, int col) {
+    return load_contig(t + Tile<bf16, W>::at(row, col));
+}
+template <int W>
+__device__ __forceinline__ Frag<float> rows_contig(const float* t, int row, int col) {
+    Frag<float> f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = s0 ? s0[base + (int64_t)r * dv] : 0.f;
-    const float a = A[h], d = D ? D[h] : 0.f, bias = dt_bias ? dt_bias[h] : 0.f;
-    for (int64_t t = lo; t < hi; ++t) {
-        const float step = time_step(to_f32(dt[t * dts + h]) + bias, softplus);
-        const float xv = to_f32(x[t * xs + h * dv + p]), dx = step * xv, decay = expf(step * a);
-        const T* br = bm + t * bs + g * DK + w * R;
-        const T* cr = cm + t * cs + g * DK + w * R;
-        float acc = 0.f;
+    for (int h = 0; h < 2; ++h) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(t + Tile<float, W>::at(row, col + 4 * h));
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            s[r] = s[r] * decay + to_f32(br[r]) * dx;
-            acc += s[r] * to_f32(cr[r]);
+        for (int e = 0; e < 4; ++e) f.v[4 * h + e] = v[e];
+    }
+    return f;
+}
+// the same in the permuted map: elements col .. col + 3 and col + 16 .. col + 19
+template <typename T, int W>
+__device__ __forceinline__ Frag<T> rows_perm(const T* t, int row, int col) {
+    Frag<T> f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const Vec<T, 4> v = load_vec<T, 4>(t + Tile<T, W>::at(row, col + 16 * h));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.v[4 * h + e] = v.v[e];
+    }
+    return f;
+}
+// operand of a product over tokens, in the permuted map: column col + lane % 16, tokens
+// t0 + 4g + e and t0 + 16 + 4g + e.  bf16 through the transposing LDS read: the 16 lanes of a
+// group read four rows of 16 columns, 8 bytes each, and get a column each.
+template <int W>
+__device__ __forceinline__ Frag<bf16> cols_perm(const bf16* t, int t0, int col, int lane) {
+    typedef __attribute__((address_space(3))) s16x4* Lds;
+    Frag<bf16> f;
+    const int r = t0 + (lane >> 4) * 4 + ((lane >> 2) & 3), c = col + (lane & 3) * 4;
+    const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(t + Tile<bf16, W>::at(r, c))));
+    const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(t + Tile<bf16, W>::at(r + 16, c))));
+    f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return f;
+}
+template <int W>
+__device__ __forceinline__ Frag<float> cols_perm(const float* t, int t0, int col, int lane) {
+    Frag<float> f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f.v[e] = t[Tile<float, W>::at(t0 + (e >> 2) * 16 + (lane >> 4) * 4 + (e & 3), col + (lane & 15))];
+    return f;
+}
+
+// ---- weighted x -----------------------------------------------------------------------------
+// The state is fp32 and is returned, so its update keeps 24 bits: in bf16 x and b are exact and
+// the product weight * x is carried as three bf16 planes; in fp32 it is one.
+template <typename T> struct Planes;
+template <> struct Planes<bf16> {
+    static constexpr int N = 3;
+    Frag<bf16> p[3];
+    __device__ __forceinline__ void set(const Frag<bf16>& x, const float (&w)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float v = (float)x.v[e] * w[e];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                p[i].v[e] = (bf16)v;
+                v -= (float)p[i].v[e];
+            }
         }
-        const int k = (int)(t - lo) & 1;  // one barrier a token: the other half is still being read
-        part[k][w][lane] = acc;
-        __syncthreads();
-        if (w == 0)
-            y[(t * H + h) * dv + p] = from_f32<T>(part[k][0][lane] + part[k][1][lane] + part[k][2][lane] + part[k][3][lane] + d * xv);
     }
-    if (sT) {
+};
+template <> struct Planes<float> {
+    static constexpr int N = 1;
+    Frag<float> p[1];
+    __device__ __forceinline__ void set(const Frag<float>& x, const float (&w)[8]) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) sT[base + (int64_t)r * dv] = s[r];
+        for (int e = 0; e < 8; ++e) p[0].v[e] = x.v[e] * w[e];
+    }
+};
+
+// sums of logarithms of decays, in 64 bits; differences of them enter M as T carries it
+template <typename T> struct Cum { typedef float type; };
+template <> struct Cum<float> { typedef double type; };
+
+struct Params {
+    const void* x;
+    const void* dt;
+    const void* b;
+    const void* c;
+    const float* A;
+    const float* D;
+    const float* dt_bias;
+    const float* s0;
+    void* y;
+    float* sT;
+    const int64_t* cu;
+    int64_t T;
+    int N, H, G, dv;
+    int xs, dts, bs, cs;
+    int softplus;
+};
+
+// A workgroup walks 64 columns of one (sequence, head) chunk by chunk.  Wave w holds state columns
+// 16w .. 16w + 15 in accumulators (rows n of all of them), computes its share of M's ten 16 x 16
+// tiles into LDS, and forms y^T (columns by tokens) and the next state for its columns.  The next
+// chunk's inputs are loaded into registers meanwhile.
+template <typename T, int DK>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Params a) {
+    typedef Tile<T, DK> TB;
+    typedef Tile<T, PS> TX;
+    typedef typename Cum<T>::type CumT;
+    constexpr int NB = Q * TB::UPR / 256, NX = Q * TX::UPR / 256;  // 16-byte units per thread
+    constexpr int NT = DK / 16, KS = DK / 32;
+    __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[Q * DK], sX[Q * PS], sM[4 * 2 * 64 * 8];
+    __shared__ CumT sCum[2][Q];
+    __shared__ __attribute__((aligned(16))) float sDt[2][Q], sE[2][Q], sW[2][Q];
+
+    const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
+    const int slices = a.dv / PS, slice = blockIdx.x % slices;
+    const int h = (blockIdx.x / slices) % a.H, n = blockIdx.x / slices / a.H;
+    int64_t lo = n * a.T, hi = lo + a.T;
+    if (a.cu) {
+        lo = min(max(a.cu[n], (int64_t)0), a.T);
+        hi = min(max(a.cu[n + 1], lo), a.T);
+    }
+    const int len = (int)(hi - lo), nc = (len + Q - 1) / Q;
+    const int group = h / (a.H / a.G);
+    const char* gx = (const char*)((const T*)a.x + lo * a.xs + h * a.dv + slice * PS);
+    const char* gb = (const char*)((const T*)a.b + lo * a.bs + group * DK);
+    const char* gc = (const char*)((const T*)a.c + lo * a.cs + group * DK);
+    const T* gt = (const T*)a.dt + lo * a.dts + h;
+    T* gy = (T*)a.y + (lo * a.H + h) * a.dv + slice * PS;
+    const float A = a.A[h], D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+
+    f32x4 S[NT];  // rows 16 nt + 4g + r, column 16 w + lane % 16
+    const int64_t sbase = ((int64_t)(n * a.H + h) * DK + g4) * a.dv + slice * PS + w * 16 + l16;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[nt][r] = a.s0 ? a.s0[sbase + (int64_t)(nt * 16 + r) * a.dv] : 0.f;
+    // halves of M's operands that no tile writes: tiles above the diagonal
+    if (w == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sM[((0 * 2 + 0) * 64 + lane) * 8 + 4 + e] = from_f32<T>(0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sM[((2 * 2 + 1) * 64 + lane) * 8 + 4 + e] = from_f32<T>(0.f);
+    }
+
+    U4 rb[NB], rc[NB], rx[NX];
+    float rdt = 0.f;
+    auto load = [&](int ch) {
+        const int left = len - ch * Q;  // tokens of the chunk; rows behind them are zeros
+        const char* pb = gb + (int64_t)ch * Q * a.bs * (int)sizeof(T);
+        const char* pc = gc + (int64_t)ch * Q * a.cs * (int)sizeof(T);
+        const char* px = gx + (int64_t)ch * Q * a.xs * (int)sizeof(T);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int id = tid + 256 * k, row = id / TB::UPR, u = id % TB::UPR;
+            rb[k] = rc[k] = U4{0, 0, 0, 0};
+            if (row < left) {
+                rb[k] = *reinterpret_cast<const U4*>(pb + (uint32_t)(row * a.bs * (int)sizeof(T) + u * 16));
+                rc[k] = *reinterpret_cast<const U4*>(pc + (uint32_t)(row * a.cs * (int)sizeof(T) + u * 16));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NX; ++k) {
+            const int id = tid + 256 * k, row = id / TX::UPR, u = id % TX::UPR;
+            rx[k] = U4{0, 0, 0, 0};
+            if (row < left) rx[k] = *reinterpret_cast<const U4*>(px + (uint32_t)(row * a.xs * (int)sizeof(T) + u * 16));
+        }
+        if (w == 3) rdt = lane < left ? to_f32(gt[((int64_t)ch * Q + lane) * a.dts]) : 0.f;
+    };
+    auto store = [&]() {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int id = tid + 256 * k, row = id / TB::UPR, u = id % TB::UPR;
+            *reinterpret_cast<U4*>(sB + TB::at(row, u * TB::EPU)) = rb[k];
+            *reinterpret_cast<U4*>(sC + TB::at(row, u * TB::EPU)) = rc[k];
+        }
+#pragma unroll
+        for (int k = 0; k < NX; ++k) {
+            const int id = tid + 256 * k, row = id / TX::UPR, u = id % TX::UPR;
+            *reinterpret_cast<U4*>(sX + TX::at(row, u * TX::EPU)) = rx[k];
+        }
+    };
+    // decays of chunk ch, a token per lane of wave 3: a token behind the end decays and adds nothing
+    auto decays = [&](int ch) {
+        if (w != 3) return;
+        const int k = ch & 1;
+        const float dt = lane < len - ch * Q ? time_step(rdt + bias, a.softplus) : 0.f;
+        double cum = (double)dt * (double)A;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double up = __shfl_up(cum, d);
+            if (lane >= d) cum += up;
+        }
+        const double all = __shfl(cum, 63);
+        sCum[k][lane] = (CumT)cum;
+        sDt[k][lane] = dt;
+        sE[k][lane] = expf((float)cum);
+        sW[k][lane] = expf((float)(all - cum)) * dt;
+    };
+
+    if (nc > 0) {
+        load(0);
+        decays(0);
+        store();
+    }
+    for (int ch = 0; ch < nc; ++ch) {
+        const int k = ch & 1;
+        cb::lds_barrier();  // the chunk is in LDS
+        if (ch + 1 < nc) load(ch + 1);
+        // M's tiles, three for waves 0 and 1, two for 2 and 3
+        auto tile = [&](int it, int jt) {
+            f32x4 acc = zero4();
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                mma(acc, rows_contig<DK>(sB, jt * 16 + l16, s * 32 + 2 * g4), rows_contig<DK>(sC, it * 16 + l16, s * 32 + 2 * g4));
+            const int i = it * 16 + l16;
+            const CumT ci = sCum[k][i];
+            typedef T V __attribute__((ext_vector_type(4)));
+            V m;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = jt * 16 + g4 + r;
+                const float v = acc[r] * expf((float)(ci - sCum[k][j])) * sDt[k][j];
+                m[r] = from_f32<T>(j <= i ? v : 0.f);
+            }
+            *reinterpret_cast<V*>(sM + ((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4) = m;
+        };
+        if (w == 0) { tile(3, 0); tile(3, 1); tile(0, 0); }
+        else if (w == 1) { tile(3, 2); tile(3, 3); tile(1, 0); }
+        else if (w == 2) { tile(2, 0); tile(2, 1); }
+        else { tile(2, 2); tile(1, 1); }
+        // what the entering state gives: y^T[p, i] = exp(cum_i) sum_n S[n, p] c[i, n]
+        f32x4 Y[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) Y[it] = zero4();
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const Frag<T> fs = frag_from_acc<T>(S[2 * s], S[2 * s + 1]);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) mma(Y[it], fs, rows_perm<T, DK>(sC, it * 16 + l16, s * 32 + g4));
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) Y[it] *= sE[k][it * 16 + l16];
+        if (ch + 1 < nc) decays(ch + 1);
+        cb::lds_barrier();  // M is in LDS
+        Frag<T> fx[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) fx[s] = cols_perm<PS>(sX, s * 32, w * 16, lane);
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int s = 0; s <= it / 2; ++s) {
+                Frag<T> fm;
+                const Vec<T, 8> v = load_vec<T, 8>(sM + ((it * 2 + s) * 64 + lane) * 8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) fm.v[e] = v.v[e];
+                mma(Y[it], fx[s], fm);
+            }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int i = it * 16 + l16;
+            const Vec<T, 4> xv = load_vec<T, 4>(sX + TX::at(i, w * 16 + g4));
+            float o[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = Y[it][r] + D * to_f32(xv.v[r]);
+            if (ch * Q + i < len) store_vec_any<T, 4>(gy + (int64_t)(ch * Q + i) * a.H * a.dv + w * 16 + g4, o);
+        }
+        // the next state
+        const float gone = sE[k][Q - 1];
+        Planes<T> wx[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float wt[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wt[e] = sW[k][s * 32 + (e >> 2) * 16 + g4 + (e & 3)];
+            wx[s].set(fx[s], wt);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            S[nt] *= gone;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Frag<T> fb = cols_perm<DK>(sB, s * 32, nt * 16, lane);
+#pragma unroll
+                for (int i = 0; i < Planes<T>::N; ++i) mma(S[nt], fb, wx[s].p[i]);
+            }
+        }
+        cb::lds_barrier();  // the chunk has been read
+        if (ch + 1 < nc) store();
+    }
+    if (a.sT) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a.sT[sbase + (int64_t)(nt * 16 + r) * a.dv] = S[nt][r];
     }
 }
 
+Params params(const SsmArgs& a) {
+    return Params{a.x, a.dt, a.b, a.c, a.A, a.D, a.dt_bias, a.initial_state, a.y, a.final_state, a.cu_seqlens, a.T,
+                  (int)a.N, (int)a.H, (int)a.G, (int)a.dv, (int)a.x_stride, (int)a.dt_stride, (int)a.b_stride,
+                  (int)a.c_stride, a.softplus ? 1 : 0};
+}
+
 template <typename T, int DK>
-hipError_t launch_walk(const SsmArgs& a) {
-    hipLaunchKernelGGL((walk_kernel<T, DK>), dim3((unsigned)(a.N * a.H * (a.dv / 64))), dim3(256), 0,
-                       (hipStream_t)a.stream, (const T*)a.x, (const T*)a.dt, (const T*)a.b, (const T*)a.c, a.A, a.D,
-                       a.dt_bias, a.initial_state, (T*)a.y, a.final_state, a.cu_seqlens, a.T, (int)a.H, (int)a.G,
-                       (int)a.dv, a.x_stride, a.dt_stride, a.b_stride, a.c_stride, a.softplus);
+hipError_t launch_chunks(const SsmArgs& a) {
+    hipLaunchKernelGGL((chunk_kernel<T, DK>), dim3((unsigned)(a.N * a.H * (a.dv / PS))), dim3(256), 0,
+                       (hipStream_t)a.stream, params(a));
     return hipGetLastError();
 }
 
+// ---- single tokens --------------------------------------------------------------------------
+// As the recurrence's decode step: a workgroup owns the state of one (sequence, head), read and
+// written once with 16-byte accesses; a thread holds a column quad of its rows, and y's sums over
+// the rows go through LDS.  Bound by HBM.
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(256) void step_kernel(Params a) {
+    constexpr int NQ = DV / 4, NRG = 256 / NQ, RPG = DK / NRG;
+    static_assert(RPG * NRG == DK && NQ * NRG == 256, "step tiling");
+    __shared__ __attribute__((aligned(16))) float sRed[NRG][DV];
+    __shared__ float sB[DK], sC[DK];
+    const int tid = threadIdx.x, cq = tid % NQ, rg = tid / NQ;
+    const int64_t n = blockIdx.x / a.H;
+    const int h = blockIdx.x % a.H, group = h / (a.H / a.G);
+    float* st = a.sT + ((int64_t)blockIdx.x * DK + rg * RPG) * DV + cq * 4;
+    f32x4 s[RPG];
+#pragma unroll
+    for (int i = 0; i < RPG; ++i) s[i] = *reinterpret_cast<const f32x4*>(st + (int64_t)i * DV);
+    if (tid < DK) {
+        sB[tid] = to_f32(((const T*)a.b)[n * a.bs + group * DK + tid]);
+        sC[tid] = to_f32(((const T*)a.c)[n * a.cs + group * DK + tid]);
+    }
+    const float dt = time_step(to_f32(((const T*)a.dt)[n * a.dts + h]) + (a.dt_bias ? a.dt_bias[h] : 0.f), a.softplus);
+    const float decay = expf(dt * a.A[h]);
+    const Vec<T, 4> xv = load_vec<T, 4>((const T*)a.x + n * a.xs + h * DV + cq * 4);
+    f32x4 dx, acc = zero4();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dx[e] = dt * to_f32(xv.v[e]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RPG; ++i) {
+        const float b = sB[rg * RPG + i], c = sC[rg * RPG + i];
+        s[i] = s[i] * decay + b * dx;
+        acc += s[i] * c;
+        *reinterpret_cast<f32x4*>(st + (int64_t)i * DV) = s[i];
+    }
+    *reinterpret_cast<f32x4*>(&sRed[rg][cq * 4]) = acc;
+    __syncthreads();
+    if (tid < DV) {
+        float o = a.D ? a.D[h] * to_f32(((const T*)a.x)[n * a.xs + h * DV + tid]) : 0.f;
+#pragma unroll
+        for (int r = 0; r < NRG; ++r) o += sRed[r][tid];
+        ((T*)a.y)[(int64_t)blockIdx.x * DV + tid] = from_f32<T>(o);
+    }
+}
+
+template <typename T, int DK, int DV>
+hipError_t launch_step_t(const SsmArgs& a) {
+    hipLaunchKernelGGL((step_kernel<T, DK, DV>), dim3((unsigned)(a.N * a.H)), dim3(256), 0, (hipStream_t)a.stream,
+                       params(a));
+    return hipGetLastError();
+}
 template <typename T>
-hipError_t launch_t(const SsmArgs& a) {
-    return a.dk == 128 ? launch_walk<T, 128>(a) : launch_walk<T, 64>(a);
+hipError_t launch_step(const SsmArgs& a) {
+    if (a.dk == 128) return a.dv == 128 ? launch_step_t<T, 128, 128>(a) : launch_step_t<T, 128, 64>(a);
+    return a.dv == 128 ? launch_step_t<T, 64, 128>(a) : launch_step_t<T, 64, 64>(a);
 }
 
 }  // namespace ssm
@@ -82,10 +420,12 @@ hipError_t launch_t(const SsmArgs& a) {
 size_t ssm_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, bool, int64_t) { return 0; }
 
 hipError_t launch_ssm_fwd(const SsmArgs& a, void*) {
-    return a.dtype_bf16 ? ssm::launch_t<bf16>(a) : ssm::launch_t<float>(a);
+    if (a.dtype_bf16) return a.dk == 128 ? ssm::launch_chunks<bf16, 128>(a) : ssm::launch_chunks<bf16, 64>(a);
+    return a.dk == 128 ? ssm::launch_chunks<float, 128>(a) : ssm::launch_chunks<float, 64>(a);
 }
 
-// a step is sequences of one token, the state first and final
-hipError_t launch_ssm_step(const SsmArgs& a) { return launch_ssm_fwd(a, nullptr); }
+hipError_t launch_ssm_step(const SsmArgs& a) {
+    return a.dtype_bf16 ? ssm::launch_step<bf16>(a) : ssm::launch_step<float>(a);
+}
 
 }  // namespace gdn2
