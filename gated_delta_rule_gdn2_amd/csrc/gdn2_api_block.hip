@@ -117,7 +117,7 @@ size_t gdn2_ssm_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk,
     if (B < 1 || T < 1 || H < 1 || B > INT_MAX || T > INT_MAX || H > INT_MAX || B * H > INT_MAX / 64) return 0;
     if (!gdn2::ssm_supported(dk, dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32)) return 0;
     const int cus = device_cus();
-    return gdn2::ssm_workspace_bytes(B, T, H, dk, dv, dtype == GDN2_DTYPE_BF16, cus > 0 ? cus : 256);
+    return gdn2::ssm_workspace_bytes(B, T, H, dk, dv, cus > 0 ? cus : 256);
 }
 
 gdn2_status_t gdn2_ssm_fwd(const void* x, const void* dt, const void* b, const void* c, const float* A, const float* D,

@@ -144,30 +144,59 @@ struct Params {
     int N, H, G, dv;
     int xs, dts, bs, cs;
     int softplus;
+    // the grid: slots (a sequence, or a segment of one) by parts of their heads and slices
+    int slots, parts, per;
+    // segments of a sequence, chunks of each, and with more than one segment the state that every
+    // segment starts from [N, H, segs, dk, dv] and its whole decay's logarithm [N, H, segs]
+    int segs, seg_chunks;
+    float* starts;
+    double* logs;
 };
+
+// Workgroups go to the eight XCDs in turn, and each XCD has an L2 of its own.  A unit, the heads
+// and slices of one part of a slot, stays on one XCD, whose L2 then holds the b and c that the unit
+// shares.  False: this workgroup has no unit.
+__device__ __forceinline__ bool unit_of(const Params& a, int* slot, int* hs) {
+    const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+    const int unit = (idx / a.per) * 8 + xcd;
+    if (unit >= a.slots * a.parts) return false;
+    *slot = unit / a.parts;
+    *hs = (unit % a.parts) * a.per + idx % a.per;
+    return true;
+}
 
 // A workgroup walks 64 columns of one (sequence, head) chunk by chunk.  Wave w holds state columns
 // 16w .. 16w + 15 in accumulators (rows n of all of them), computes its share of M's ten 16 x 16
 // tiles into LDS, and forms y^T (columns by tokens) and the next state for its columns.  The next
 // chunk's inputs are loaded into registers meanwhile.
-template <typename T, int DK>
+// ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
+// the next segment's place in `starts`, the segment's decay to `logs`.
+template <typename T, int DK, bool ENDS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Params a) {
     typedef Tile<T, DK> TB;
     typedef Tile<T, PS> TX;
     typedef typename Cum<T>::type CumT;
     constexpr int NB = Q * TB::UPR / 256, NX = Q * TX::UPR / 256;  // 16-byte units per thread
     constexpr int NT = DK / 16, KS = DK / 32;
-    __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[Q * DK], sX[Q * PS], sM[4 * 2 * 64 * 8];
+    __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[ENDS ? 8 : Q * DK], sX[Q * PS], sM[ENDS ? 8 : 4 * 2 * 64 * 8];
     __shared__ CumT sCum[2][Q];
     __shared__ __attribute__((aligned(16))) float sDt[2][Q], sE[2][Q], sW[2][Q];
 
     const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
-    const int slices = a.dv / PS, slice = blockIdx.x % slices;
-    const int h = (blockIdx.x / slices) % a.H, n = blockIdx.x / slices / a.H;
+    int slot, hs;
+    if (!unit_of(a, &slot, &hs)) return;
+    const int slices = a.dv / PS, slice = hs % slices, h = hs / slices;
+    const int steps = ENDS ? a.segs - 1 : a.segs;  // slots of a sequence
+    const int n = a.cu ? longest_first(a.cu, a.N, slot, (int)a.T, reinterpret_cast<int*>(sB)) : slot / steps;
+    const int seg = a.cu ? 0 : slot % steps;
+    static_assert(sizeof(sB) >= (kMaxSort + 1) * sizeof(int), "scratch of longest_first");
     int64_t lo = n * a.T, hi = lo + a.T;
     if (a.cu) {
         lo = min(max(a.cu[n], (int64_t)0), a.T);
         hi = min(max(a.cu[n + 1], lo), a.T);
+    } else if (a.segs > 1) {
+        lo += (int64_t)seg * a.seg_chunks * Q;
+        hi = min(hi, lo + (int64_t)a.seg_chunks * Q);
     }
     const int len = (int)(hi - lo), nc = (len + Q - 1) / Q;
     const int group = h / (a.H / a.G);
@@ -180,12 +209,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
 
     f32x4 S[NT];  // rows 16 nt + 4g + r, column 16 w + lane % 16
     const int64_t sbase = ((int64_t)(n * a.H + h) * DK + g4) * a.dv + slice * PS + w * 16 + l16;
+    const int64_t size = (int64_t)DK * a.dv, at0 = sbase - (int64_t)(n * a.H + h) * size;  // place in one state
+    const float* from = a.s0 ? a.s0 + sbase : nullptr;
+    if (a.segs > 1) from = ENDS ? nullptr : a.starts + ((int64_t)(n * a.H + h) * a.segs + seg) * size + at0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[nt][r] = a.s0 ? a.s0[sbase + (int64_t)(nt * 16 + r) * a.dv] : 0.f;
+        for (int r = 0; r < 4; ++r) S[nt][r] = from ? from[(int64_t)(nt * 16 + r) * a.dv] : 0.f;
+    double logs = 0.0;  // ENDS: the logarithm of the segment's decay
     // halves of M's operands that no tile writes: tiles above the diagonal
-    if (w == 0) {
+    if (!ENDS && w == 0) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sM[((0 * 2 + 0) * 64 + lane) * 8 + 4 + e] = from_f32<T>(0.f);
 #pragma unroll
@@ -205,7 +238,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
             rb[k] = rc[k] = U4{0, 0, 0, 0};
             if (row < left) {
                 rb[k] = *reinterpret_cast<const U4*>(pb + (uint32_t)(row * a.bs * (int)sizeof(T) + u * 16));
-                rc[k] = *reinterpret_cast<const U4*>(pc + (uint32_t)(row * a.cs * (int)sizeof(T) + u * 16));
+                if constexpr (!ENDS) rc[k] = *reinterpret_cast<const U4*>(pc + (uint32_t)(row * a.cs * (int)sizeof(T) + u * 16));
             }
         }
 #pragma unroll
@@ -221,7 +254,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
         for (int k = 0; k < NB; ++k) {
             const int id = tid + 256 * k, row = id / TB::UPR, u = id % TB::UPR;
             *reinterpret_cast<U4*>(sB + TB::at(row, u * TB::EPU)) = rb[k];
-            *reinterpret_cast<U4*>(sC + TB::at(row, u * TB::EPU)) = rc[k];
+            if constexpr (!ENDS) *reinterpret_cast<U4*>(sC + TB::at(row, u * TB::EPU)) = rc[k];
         }
 #pragma unroll
         for (int k = 0; k < NX; ++k) {
@@ -241,6 +274,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
             if (lane >= d) cum += up;
         }
         const double all = __shfl(cum, 63);
+        if constexpr (ENDS) logs += all;
         sCum[k][lane] = (CumT)cum;
         sDt[k][lane] = dt;
         sE[k][lane] = expf((float)cum);
@@ -256,6 +290,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
         const int k = ch & 1;
         cb::lds_barrier();  // the chunk is in LDS
         if (ch + 1 < nc) load(ch + 1);
+        f32x4 Y[4];
+        if constexpr (!ENDS) {
         // M's tiles, three for waves 0 and 1, two for 2 and 3
         auto tile = [&](int it, int jt) {
             f32x4 acc = zero4();
@@ -279,7 +315,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
         else if (w == 2) { tile(2, 0); tile(2, 1); }
         else { tile(2, 2); tile(1, 1); }
         // what the entering state gives: y^T[p, i] = exp(cum_i) sum_n S[n, p] c[i, n]
-        f32x4 Y[4];
 #pragma unroll
         for (int it = 0; it < 4; ++it) Y[it] = zero4();
 #pragma unroll
@@ -290,11 +325,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
         }
 #pragma unroll
         for (int it = 0; it < 4; ++it) Y[it] *= sE[k][it * 16 + l16];
+        }
         if (ch + 1 < nc) decays(ch + 1);
-        cb::lds_barrier();  // M is in LDS
+        if constexpr (!ENDS) cb::lds_barrier();  // M is in LDS
         Frag<T> fx[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) fx[s] = cols_perm<PS>(sX, s * 32, w * 16, lane);
+        if constexpr (!ENDS) {
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -313,6 +350,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = Y[it][r] + D * to_f32(xv.v[r]);
             if (ch * Q + i < len) store_vec_any<T, 4>(gy + (int64_t)(ch * Q + i) * a.H * a.dv + w * 16 + g4, o);
+        }
         }
         // the next state
         const float gone = sE[k][Q - 1];
@@ -337,24 +375,98 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
         cb::lds_barrier();  // the chunk has been read
         if (ch + 1 < nc) store();
     }
-    if (a.sT) {
+    float* to = nullptr;
+    if (ENDS) to = a.starts + ((int64_t)(n * a.H + h) * a.segs + seg + 1) * size + at0;
+    else if (a.sT && (a.cu || seg == a.segs - 1)) to = a.sT + sbase;
+    if (to) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) a.sT[sbase + (int64_t)(nt * 16 + r) * a.dv] = S[nt][r];
+            for (int r = 0; r < 4; ++r) to[(int64_t)(nt * 16 + r) * a.dv] = S[nt][r];
+    }
+    if (ENDS && slice == 0 && w == 3 && lane == 0) a.logs[(int64_t)(n * a.H + h) * a.segs + seg] = logs;
+}
+
+// starts[0] = the initial state, starts[s + 1] = exp(logs[s]) starts[s] + the segment's own end,
+// which is in starts[s + 1].  The forward pass reads every segment's start from here, so it may
+// write the final state over the initial one.
+__global__ __launch_bounds__(256) void join_kernel(Params a, int dk) {
+    const int64_t quads = (int64_t)dk * a.dv / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t nh = id / quads;
+    if (nh >= (int64_t)a.N * a.H) return;
+    f32x4* st = reinterpret_cast<f32x4*>(a.starts) + nh * a.segs * quads + id % quads;
+    f32x4 s = a.s0 ? reinterpret_cast<const f32x4*>(a.s0)[id] : zero4();
+    st[0] = s;
+    for (int g = 0; g + 1 < a.segs; ++g) {
+        const f32x4 own = st[(int64_t)(g + 1) * quads];
+        s = s * expf((float)a.logs[nh * a.segs + g]) + own;
+        st[(int64_t)(g + 1) * quads] = s;
     }
 }
 
 Params params(const SsmArgs& a) {
     return Params{a.x, a.dt, a.b, a.c, a.A, a.D, a.dt_bias, a.initial_state, a.y, a.final_state, a.cu_seqlens, a.T,
                   (int)a.N, (int)a.H, (int)a.G, (int)a.dv, (int)a.x_stride, (int)a.dt_stride, (int)a.b_stride,
-                  (int)a.c_stride, a.softplus ? 1 : 0};
+                  (int)a.c_stride, a.softplus ? 1 : 0, 0, 0, 0, 1, 0, nullptr, nullptr};
+}
+
+// Parts of a slot's heads and slices: the fewest that leave the eight XCDs with about as many
+// units each (at most an eighth more than their share).
+void set_grid(Params* p, int slots) {
+    const int hs = p->H * (p->dv / PS);
+    p->slots = slots;
+    p->parts = hs;
+    for (int k = 1; k < hs; ++k) {
+        if (hs % k) continue;
+        const int64_t units = (int64_t)slots * k;
+        if ((units + 7) / 8 * 64 <= units * 9) {
+            p->parts = k;
+            break;
+        }
+    }
+    p->per = hs / p->parts;
+}
+unsigned grid_of(const Params& p) { return (unsigned)(((int64_t)p.slots * p.parts + 7) / 8 * 8 * p.per); }
+
+// Segments of a sequence.  A chain is one (sequence, head, 64 columns); a compute unit runs two
+// workgroups at once.  Chains that do not fill the GPU are cut so that their pieces do, of at least
+// 8 chunks each: a piece but the last is walked twice, once for the state alone.
+int segments(int64_t N, int64_t T, int64_t H, int64_t dv, int64_t cus) {
+    const int64_t chains = N * H * (dv / PS), nc = (T + Q - 1) / Q;
+    int64_t g = 2 * cus / chains;
+    if (g > nc / 8) g = nc / 8;
+    if (g < 2) return 1;
+    const int64_t len = (nc + g - 1) / g;
+    return (int)((nc + len - 1) / len);
+}
+
+struct Layout {
+    int64_t starts, logs, total;  // byte offsets
+};
+Layout layout(int64_t N, int64_t H, int64_t dk, int64_t dv, int64_t segs) {
+    Layout l;
+    l.starts = 0;
+    l.logs = N * H * segs * dk * dv * 4;
+    l.total = l.logs + (N * H * segs * 8 + 255) / 256 * 256;
+    return l;
 }
 
 template <typename T, int DK>
-hipError_t launch_chunks(const SsmArgs& a) {
-    hipLaunchKernelGGL((chunk_kernel<T, DK>), dim3((unsigned)(a.N * a.H * (a.dv / PS))), dim3(256), 0,
-                       (hipStream_t)a.stream, params(a));
+hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
+    Params p = params(a);
+    p.segs = workspace ? segments(a.N, a.T, a.H, a.dv, a.cus) : 1;
+    p.seg_chunks = (int)(((a.T + Q - 1) / Q + p.segs - 1) / p.segs);
+    if (p.segs > 1) {
+        const Layout l = layout(a.N, a.H, a.dk, a.dv, p.segs);
+        p.starts = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.starts);
+        p.logs = reinterpret_cast<double*>(static_cast<char*>(workspace) + l.logs);
+        set_grid(&p, (int)a.N * (p.segs - 1));
+        hipLaunchKernelGGL((chunk_kernel<T, DK, true>), dim3(grid_of(p)), dim3(256), 0, (hipStream_t)a.stream, p);
+        const int64_t quads = a.N * a.H * a.dk * a.dv / 4;
+        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, (hipStream_t)a.stream, p, DK);
+    }
+    set_grid(&p, (int)a.N * p.segs);
+    hipLaunchKernelGGL((chunk_kernel<T, DK, false>), dim3(grid_of(p)), dim3(256), 0, (hipStream_t)a.stream, p);
     return hipGetLastError();
 }
 
@@ -417,11 +529,14 @@ hipError_t launch_step(const SsmArgs& a) {
 
 }  // namespace ssm
 
-size_t ssm_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, bool, int64_t) { return 0; }
+size_t ssm_workspace_bytes(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
+    const int segs = ssm::segments(N, T, H, dv, cus);
+    return segs > 1 ? (size_t)ssm::layout(N, H, dk, dv, segs).total : 0;
+}
 
-hipError_t launch_ssm_fwd(const SsmArgs& a, void*) {
-    if (a.dtype_bf16) return a.dk == 128 ? ssm::launch_chunks<bf16, 128>(a) : ssm::launch_chunks<bf16, 64>(a);
-    return a.dk == 128 ? ssm::launch_chunks<float, 128>(a) : ssm::launch_chunks<float, 64>(a);
+hipError_t launch_ssm_fwd(const SsmArgs& a, void* ws) {
+    if (a.dtype_bf16) return a.dk == 128 ? ssm::launch_chunks<bf16, 128>(a, ws) : ssm::launch_chunks<bf16, 64>(a, ws);
+    return a.dk == 128 ? ssm::launch_chunks<float, 128>(a, ws) : ssm::launch_chunks<float, 64>(a, ws);
 }
 
 hipError_t launch_ssm_step(const SsmArgs& a) {
