@@ -17,8 +17,7 @@
 namespace gdn2 {
 namespace ssm {
 
-constexpr int Q = 64;   // tokens of a chunk
-constexpr int PS = 64;  // state columns of a workgroup: 16 per wave
+constexpr int Q = 64;  // tokens of a chunk
 
 typedef uint32_t U4 __attribute__((ext_vector_type(4)));
 
@@ -30,70 +29,106 @@ __device__ __forceinline__ float time_step(float v, bool softplus) {
 
 // ---- LDS tiles ------------------------------------------------------------------------------
 // [64 tokens][W] row-major, in 16-byte units whose place in the row is XORed with a function of
-// the row.  Three patterns read them: 16 rows at one unit (products over W), 8 rows at one pair of
-// units (the transposing read of products over tokens), 16 rows at half a unit; with this
-// function each touches every bank once.
-template <typename T, int W>
+// the row.  Measured phases of the 64 banks: a 16-byte read takes lanes 0-3, 12-15 and 20-27
+// together (then their like), 8-byte and 4-byte reads 32 lanes in a row.  So a 16-byte read of 16
+// rows (kRows: products over W) wants the rows of a phase at different units, the transposing
+// 8-byte read (kCols: products over tokens; 8 rows, two units of each) different pairs of units
+// over 8 rows.  b is read both ways, c only by rows, x by columns and 8 bytes of 16 rows (kBoth).
+// Without the difference between them a sixth of the chunk kernel's time was LDS conflicts.
+enum Reads { kRows, kCols, kBoth };
+template <typename T, int W, Reads R>
 struct Tile {
     static constexpr int UPR = W * (int)sizeof(T) / 16;  // units per row
     static constexpr int EPU = 16 / (int)sizeof(T);      // elements per unit
     __device__ static __forceinline__ int swz(int row) {
-        if constexpr (UPR >= 16) return ((row & 7) << 1) | ((row >> 3) & 1);
-        else return (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
+        const int r = UPR >= 16 ? row : row >> 1;  // an 8-unit row is half of the banks
+        if constexpr (R == kRows || sizeof(T) == 4) return r & (UPR >= 16 ? 15 : 7);
+        else if constexpr (UPR >= 16) return ((r & 7) << 1) | (R == kBoth ? (r >> 3) & 1 : 0);
+        else return ((r & 3) << 1) | (R == kBoth ? (r >> 2) & 1 : 0);
     }
+    static constexpr int RB = UPR * 16;  // bytes of a row
+    // Byte offset of (row, col).  A row of 16 R + row adds 16 R rows; a column whose bits above a
+    // lane's own are c enters by XOR with its bytes: a pattern's every address is one lane base,
+    // XORed with one constant and offset by another.
     __device__ static __forceinline__ int at(int row, int col) {
-        return (row * UPR + ((col / EPU) ^ swz(row))) * EPU + col % EPU;
+        return row * RB + ((col * (int)sizeof(T)) ^ (swz(row) << 4));
     }
 };
 
-// operand of a product over W: row `row`, elements col .. col + 7
-template <int W>
-__device__ __forceinline__ Frag<bf16> rows_contig(const bf16* t, int row, int col) {
-    return load_contig(t + Tile<bf16, W>::at(row, col));
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> lds_vec(const void* tile, int off) {
+    return load_vec<T, N>(reinterpret_cast<const T*>(static_cast<const char*>(tile) + off));
 }
-template <int W>
-__device__ __forceinline__ Frag<float> rows_contig(const float* t, int row, int col) {
+
+// Operands.  `base` is the pattern's lane base: rows_base, perm_base or cols_base.
+// A product over W: row r0 + lane % 16, elements col + 8g .. col + 8g + 7.
+template <typename TL>
+__device__ __forceinline__ int rows_base(int lane) { return TL::at(lane & 15, (lane >> 4) * 8); }
+template <typename TL>
+__device__ __forceinline__ Frag<bf16> rows_contig(const bf16* t, int base, int r0, int col) {
+    Frag<bf16> f;
+    const Vec<bf16, 8> v = lds_vec<bf16, 8>(t, (base ^ (col * 2)) + r0 * TL::RB);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = v.v[e];
+    return f;
+}
+template <typename TL>
+__device__ __forceinline__ Frag<float> rows_contig(const float* t, int base, int r0, int col) {
     Frag<float> f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(t + Tile<float, W>::at(row, col + 4 * h));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f.v[4 * h + e] = v[e];
-    }
-    return f;
-}
-// the same in the permuted map: elements col .. col + 3 and col + 16 .. col + 19
-template <typename T, int W>
-__device__ __forceinline__ Frag<T> rows_perm(const T* t, int row, int col) {
-    Frag<T> f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const Vec<T, 4> v = load_vec<T, 4>(t + Tile<T, W>::at(row, col + 16 * h));
+        const Vec<float, 4> v = lds_vec<float, 4>(t, (base ^ ((col + 4 * h) * 4)) + r0 * TL::RB);
 #pragma unroll
         for (int e = 0; e < 4; ++e) f.v[4 * h + e] = v.v[e];
     }
     return f;
 }
-// operand of a product over tokens, in the permuted map: column col + lane % 16, tokens
-// t0 + 4g + e and t0 + 16 + 4g + e.  bf16 through the transposing LDS read: the 16 lanes of a
-// group read four rows of 16 columns, 8 bytes each, and get a column each.
-template <int W>
-__device__ __forceinline__ Frag<bf16> cols_perm(const bf16* t, int t0, int col, int lane) {
+// The same in the permuted map: elements col + 4g .. + 3 and col + 16 + 4g .. + 3.
+template <typename TL>
+__device__ __forceinline__ int perm_base(int lane) { return TL::at(lane & 15, (lane >> 4) * 4); }
+template <typename TL, typename T>
+__device__ __forceinline__ Frag<T> rows_perm(const T* t, int base, int r0, int col) {
+    Frag<T> f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const Vec<T, 4> v = lds_vec<T, 4>(t, (base ^ ((col + 16 * h) * (int)sizeof(T))) + r0 * TL::RB);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.v[4 * h + e] = v.v[e];
+    }
+    return f;
+}
+// A product over tokens, in the permuted map: column col + lane % 16, tokens t0 + 4g + e and
+// t0 + 16 + 4g + e.  bf16 through the transposing LDS read: the 16 lanes of a group read four rows
+// of 16 columns, 8 bytes each, and get a column each.
+template <typename TL, typename T>
+__device__ __forceinline__ int cols_base(int lane) {
+    if constexpr (sizeof(T) == 2) return TL::at((lane >> 4) * 4 + ((lane >> 2) & 3), (lane & 3) * 4);
+    else return TL::at((lane >> 4) * 4, lane & 15);
+}
+template <typename TL>
+__device__ __forceinline__ Frag<bf16> cols_perm(const bf16* t, int base, int t0, int col) {
     typedef __attribute__((address_space(3))) s16x4* Lds;
     Frag<bf16> f;
-    const int r = t0 + (lane >> 4) * 4 + ((lane >> 2) & 3), c = col + (lane & 3) * 4;
-    const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(t + Tile<bf16, W>::at(r, c))));
-    const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(t + Tile<bf16, W>::at(r + 16, c))));
+    const char* p = reinterpret_cast<const char*>(t) + (base ^ (col * 2)) + t0 * TL::RB;
+    const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p));
+    const bf16x4 hi = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 16 * TL::RB)));
     f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return f;
 }
-template <int W>
-__device__ __forceinline__ Frag<float> cols_perm(const float* t, int t0, int col, int lane) {
+template <typename TL>
+__device__ __forceinline__ Frag<float> cols_perm(const float* t, int base, int t0, int col) {
     Frag<float> f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        f.v[e] = t[Tile<float, W>::at(t0 + (e >> 2) * 16 + (lane >> 4) * 4 + (e & 3), col + (lane & 15))];
+    for (int e = 0; e < 8; ++e)  // a row of 4g + e: e is in the swizzle's low bits
+        f.v[e] = lds_vec<float, 1>(t, (base ^ (col * 4) ^ ((e & 3) << 4)) + (t0 + (e >> 2) * 16 + (e & 3)) * TL::RB).v[0];
     return f;
+}
+
+// A lane's base that the compiler may not keep derived addresses of: they are one XOR each, and all
+// of them in registers were spilled.
+__device__ __forceinline__ int fresh(int base) {
+    asm volatile("" : "+v"(base));
+    return base;
 }
 
 // ---- weighted x -----------------------------------------------------------------------------
@@ -124,9 +159,20 @@ template <> struct Planes<float> {
     }
 };
 
-// sums of logarithms of decays, in 64 bits; differences of them enter M as T carries it
-template <typename T> struct Cum { typedef float type; };
-template <> struct Cum<float> { typedef double type; };
+// Sums of logarithms of decays are formed in 64 bits.  What a pair of tokens needs, the decay
+// between them, is a difference of two: in bf16 of their fp32 roundings (to base 2, for the
+// hardware's exponential; an error of |cum| 2^-23, far below a bf16 rounding of M where M counts),
+// in fp32 of the 64-bit sums.
+template <typename T> struct Pair {
+    typedef float Cum;
+    __device__ static __forceinline__ Cum cum(double v) { return (float)(v * 1.4426950408889634); }
+    __device__ static __forceinline__ float decay(Cum i, Cum j) { return __builtin_amdgcn_exp2f(i - j); }
+};
+template <> struct Pair<float> {
+    typedef double Cum;
+    __device__ static __forceinline__ Cum cum(double v) { return v; }
+    __device__ static __forceinline__ float decay(Cum i, Cum j) { return expf((float)(i - j)); }
+};
 
 struct Params {
     const void* x;
@@ -144,7 +190,7 @@ struct Params {
     int N, H, G, dv;
     int xs, dts, bs, cs;
     int softplus;
-    // the grid: slots (a sequence, or a segment of one) by parts of their heads and slices
+    // the grid: slots (a sequence, or a segment of one) by parts of their heads
     int slots, parts, per;
     // segments of a sequence, chunks of each, and with more than one segment the state that every
     // segment starts from [N, H, segs, dk, dv] and its whole decay's logarithm [N, H, segs]
@@ -154,42 +200,64 @@ struct Params {
 };
 
 // Workgroups go to the eight XCDs in turn, and each XCD has an L2 of its own.  A unit, the heads
-// and slices of one part of a slot, stays on one XCD, whose L2 then holds the b and c that the unit
+// of one part of a slot, stays on one XCD, whose L2 then holds the b and c that the unit
 // shares.  False: this workgroup has no unit.
-__device__ __forceinline__ bool unit_of(const Params& a, int* slot, int* hs) {
+__device__ __forceinline__ bool unit_of(const Params& a, int* slot, int* head) {
     const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
     const int unit = (idx / a.per) * 8 + xcd;
     if (unit >= a.slots * a.parts) return false;
     *slot = unit / a.parts;
-    *hs = (unit % a.parts) * a.per + idx % a.per;
+    *head = (unit % a.parts) * a.per + idx % a.per;
     return true;
 }
 
-// A workgroup walks 64 columns of one (sequence, head) chunk by chunk.  Wave w holds state columns
-// 16w .. 16w + 15 in accumulators (rows n of all of them), computes its share of M's ten 16 x 16
-// tiles into LDS, and forms y^T (columns by tokens) and the next state for its columns.  The next
-// chunk's inputs are loaded into registers meanwhile.
+__device__ __forceinline__ U4 bload16(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+// four values as T at a byte offset, dropped past the resource's end
+template <typename T>
+__device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const float (&f)[4]) {
+    typedef T V __attribute__((ext_vector_type(4)));
+    V v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = from_f32<T>(f[e]);
+    typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(U2, v), r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(U4, v), r, off, 0, 0);
+}
+
+// waves per SIMD that the register budget is set for
+template <typename T, int NW> constexpr int kWaves = sizeof(T) == 4 ? (NW == 8 ? 2 : 1) : (NW == 8 ? 4 : 3);
+
+// A workgroup of NW waves walks the 16 NW = dv columns of one (sequence, head) chunk by chunk.
+// Wave w holds state columns 16w .. 16w + 15 in accumulators (rows n of all of them), computes its
+// share of M's ten 16 x 16 tiles into LDS, and forms y^T (columns by tokens) and the next state for
+// its columns.  The next chunk's inputs are loaded into registers meanwhile, through buffer
+// resources that end with the sequence: rows behind it read as zeros, and their y is dropped.
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
-template <typename T, int DK, bool ENDS>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Params a) {
-    typedef Tile<T, DK> TB;
-    typedef Tile<T, PS> TX;
-    typedef typename Cum<T>::type CumT;
-    constexpr int NB = Q * TB::UPR / 256, NX = Q * TX::UPR / 256;  // 16-byte units per thread
+template <typename T, int DK, int NW, bool ENDS>
+__global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params a) {
+    constexpr int DV = 16 * NW, NTH = 64 * NW, ES = (int)sizeof(T);
+    typedef Tile<T, DK, kCols> TB;
+    typedef Tile<T, DK, kRows> TC;
+    typedef Tile<T, DV, kBoth> TX;
+    typedef typename Pair<T>::Cum Cum;
+    constexpr int NB = Q * TB::UPR / NTH, NX = Q * TX::UPR / NTH;  // 16-byte units per thread
     constexpr int NT = DK / 16, KS = DK / 32;
-    __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[ENDS ? 8 : Q * DK], sX[Q * PS], sM[ENDS ? 8 : 4 * 2 * 64 * 8];
-    __shared__ CumT sCum[2][Q];
+    __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[ENDS ? 8 : Q * DK], sX[Q * DV], sM[ENDS ? 8 : 4 * 2 * 64 * 8];
+    __shared__ __attribute__((aligned(16))) Cum sCum[2][Q];
     __shared__ __attribute__((aligned(16))) float sDt[2][Q], sE[2][Q], sW[2][Q];
 
-    const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, l16 = lane & 15, g4 = (lane >> 4) * 4;
-    int slot, hs;
-    if (!unit_of(a, &slot, &hs)) return;
-    const int slices = a.dv / PS, slice = hs % slices, h = hs / slices;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, l16 = lane & 15;
+    const int g4 = (lane >> 4) * 4;
+    int slot, h;
+    if (!unit_of(a, &slot, &h)) return;
     const int steps = ENDS ? a.segs - 1 : a.segs;  // slots of a sequence
-    const int n = a.cu ? longest_first(a.cu, a.N, slot, (int)a.T, reinterpret_cast<int*>(sB)) : slot / steps;
-    const int seg = a.cu ? 0 : slot % steps;
     static_assert(sizeof(sB) >= (kMaxSort + 1) * sizeof(int), "scratch of longest_first");
+    const int n = a.cu ? __builtin_amdgcn_readfirstlane(longest_first(a.cu, a.N, slot, (int)a.T, reinterpret_cast<int*>(sB)))
+                       : slot / steps;
+    const int seg = a.cu ? 0 : slot % steps;
     int64_t lo = n * a.T, hi = lo + a.T;
     if (a.cu) {
         lo = min(max(a.cu[n], (int64_t)0), a.T);
@@ -200,22 +268,23 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
     }
     const int len = (int)(hi - lo), nc = (len + Q - 1) / Q;
     const int group = h / (a.H / a.G);
-    const char* gx = (const char*)((const T*)a.x + lo * a.xs + h * a.dv + slice * PS);
-    const char* gb = (const char*)((const T*)a.b + lo * a.bs + group * DK);
-    const char* gc = (const char*)((const T*)a.c + lo * a.cs + group * DK);
+    const T* gx = (const T*)a.x + lo * a.xs + h * DV;
+    const T* gb = (const T*)a.b + lo * a.bs + group * DK;
+    const T* gc = (const T*)a.c + lo * a.cs + group * DK;
     const T* gt = (const T*)a.dt + lo * a.dts + h;
-    T* gy = (T*)a.y + (lo * a.H + h) * a.dv + slice * PS;
+    T* gy = (T*)a.y + (lo * a.H + h) * DV;
+    const int ys = a.H * DV;
     const float A = a.A[h], D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
 
     f32x4 S[NT];  // rows 16 nt + 4g + r, column 16 w + lane % 16
-    const int64_t sbase = ((int64_t)(n * a.H + h) * DK + g4) * a.dv + slice * PS + w * 16 + l16;
-    const int64_t size = (int64_t)DK * a.dv, at0 = sbase - (int64_t)(n * a.H + h) * size;  // place in one state
-    const float* from = a.s0 ? a.s0 + sbase : nullptr;
-    if (a.segs > 1) from = ENDS ? nullptr : a.starts + ((int64_t)(n * a.H + h) * a.segs + seg) * size + at0;
+    const int64_t state = (int64_t)n * a.H + h;
+    const int at0 = g4 * DV + w * 16 + l16;
+    const float* from = a.s0 ? a.s0 + state * (DK * DV) : nullptr;
+    if (a.segs > 1) from = ENDS ? nullptr : a.starts + (state * a.segs + seg) * (DK * DV);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[nt][r] = from ? from[(int64_t)(nt * 16 + r) * a.dv] : 0.f;
+        for (int r = 0; r < 4; ++r) S[nt][r] = from ? from[at0 + (nt * 16 + r) * DV] : 0.f;
     double logs = 0.0;  // ENDS: the logarithm of the segment's decay
     // halves of M's operands that no tile writes: tiles above the diagonal
     if (!ENDS && w == 0) {
@@ -228,43 +297,47 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
     U4 rb[NB], rc[NB], rx[NX];
     float rdt = 0.f;
     auto load = [&](int ch) {
-        const int left = len - ch * Q;  // tokens of the chunk; rows behind them are zeros
-        const char* pb = gb + (int64_t)ch * Q * a.bs * (int)sizeof(T);
-        const char* pc = gc + (int64_t)ch * Q * a.cs * (int)sizeof(T);
-        const char* px = gx + (int64_t)ch * Q * a.xs * (int)sizeof(T);
+        const int64_t t0 = (int64_t)ch * Q;
+        const int rows = min(len - ch * Q, Q);
+        const auto qb = cb::buffer_over(gb + t0 * a.bs, rows * a.bs * ES);
+        const auto qc = cb::buffer_over(gc + t0 * a.cs, rows * a.cs * ES);
+        const auto qx = cb::buffer_over(gx + t0 * a.xs, rows * a.xs * ES);
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int id = tid + 256 * k, row = id / TB::UPR, u = id % TB::UPR;
-            rb[k] = rc[k] = U4{0, 0, 0, 0};
-            if (row < left) {
-                rb[k] = *reinterpret_cast<const U4*>(pb + (uint32_t)(row * a.bs * (int)sizeof(T) + u * 16));
-                if constexpr (!ENDS) rc[k] = *reinterpret_cast<const U4*>(pc + (uint32_t)(row * a.cs * (int)sizeof(T) + u * 16));
-            }
+            const int id = tid + NTH * k, row = id / TB::UPR, u = id % TB::UPR;
+            rb[k] = bload16(qb, row * a.bs * ES + u * 16);
+            if constexpr (!ENDS) rc[k] = bload16(qc, row * a.cs * ES + u * 16);
         }
 #pragma unroll
         for (int k = 0; k < NX; ++k) {
-            const int id = tid + 256 * k, row = id / TX::UPR, u = id % TX::UPR;
-            rx[k] = U4{0, 0, 0, 0};
-            if (row < left) rx[k] = *reinterpret_cast<const U4*>(px + (uint32_t)(row * a.xs * (int)sizeof(T) + u * 16));
+            const int id = tid + NTH * k, row = id / TX::UPR, u = id % TX::UPR;
+            rx[k] = bload16(qx, row * a.xs * ES + u * 16);
         }
-        if (w == 3) rdt = lane < left ? to_f32(gt[((int64_t)ch * Q + lane) * a.dts]) : 0.f;
+        if (w == NW - 1) rdt = lane < rows ? to_f32(gt[(t0 + lane) * a.dts]) : 0.f;
+    };
+    const int stB = TB::at(tid / TB::UPR, tid % TB::UPR * TB::EPU), stC = TC::at(tid / TB::UPR, tid % TB::UPR * TB::EPU);
+    const int stX = TX::at(tid / TX::UPR, tid % TX::UPR * TX::EPU);
+    // a thread's unit k lies k NTH units on: as many rows below, whose swizzle differs by that of
+    // the rows between
+    constexpr int RB = NTH / TB::UPR, RX = NTH / TX::UPR;
+    auto put = [](void* tile, int base, int swz, int k, const U4& v) {
+        *reinterpret_cast<U4*>(static_cast<char*>(tile) + (base ^ (swz << 4)) + k * NTH * 16) = v;
     };
     auto store = [&]() {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int id = tid + 256 * k, row = id / TB::UPR, u = id % TB::UPR;
-            *reinterpret_cast<U4*>(sB + TB::at(row, u * TB::EPU)) = rb[k];
-            if constexpr (!ENDS) *reinterpret_cast<U4*>(sC + TB::at(row, u * TB::EPU)) = rc[k];
+            put(sB, stB, TB::swz(k * RB), k, rb[k]);
+            if constexpr (!ENDS) put(sC, stC, TC::swz(k * RB), k, rc[k]);
         }
 #pragma unroll
-        for (int k = 0; k < NX; ++k) {
-            const int id = tid + 256 * k, row = id / TX::UPR, u = id % TX::UPR;
-            *reinterpret_cast<U4*>(sX + TX::at(row, u * TX::EPU)) = rx[k];
-        }
+        for (int k = 0; k < NX; ++k) put(sX, stX, TX::swz(k * RX), k, rx[k]);
     };
-    // decays of chunk ch, a token per lane of wave 3: a token behind the end decays and adds nothing
+    const int bRowsB = rows_base<TB>(lane), bRowsC = rows_base<TC>(lane), bPermC = perm_base<TC>(lane);
+    const int bColsB = cols_base<TB, T>(lane), bColsX = cols_base<TX, T>(lane), bPermX = perm_base<TX>(lane);
+    // decays of chunk ch, a token per lane of the last wave: a token behind the end decays and
+    // adds nothing
     auto decays = [&](int ch) {
-        if (w != 3) return;
+        if (w != NW - 1) return;
         const int k = ch & 1;
         const float dt = lane < len - ch * Q ? time_step(rdt + bias, a.softplus) : 0.f;
         double cum = (double)dt * (double)A;
@@ -275,7 +348,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
         }
         const double all = __shfl(cum, 63);
         if constexpr (ENDS) logs += all;
-        sCum[k][lane] = (CumT)cum;
+        sCum[k][lane] = Pair<T>::cum(cum);
         sDt[k][lane] = dt;
         sE[k][lane] = expf((float)cum);
         sW[k][lane] = expf((float)(all - cum)) * dt;
@@ -290,101 +363,112 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void chunk_kernel(Para
         const int k = ch & 1;
         cb::lds_barrier();  // the chunk is in LDS
         if (ch + 1 < nc) load(ch + 1);
+        const int rowsB = fresh(bRowsB), rowsC = fresh(bRowsC), permC = fresh(bPermC), colsB = fresh(bColsB);
         f32x4 Y[4];
         if constexpr (!ENDS) {
-        // M's tiles, three for waves 0 and 1, two for 2 and 3
-        auto tile = [&](int it, int jt) {
-            f32x4 acc = zero4();
+            auto tile = [&](int it, int jt) {
+                f32x4 acc = zero4();
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-                mma(acc, rows_contig<DK>(sB, jt * 16 + l16, s * 32 + 2 * g4), rows_contig<DK>(sC, it * 16 + l16, s * 32 + 2 * g4));
-            const int i = it * 16 + l16;
-            const CumT ci = sCum[k][i];
-            typedef T V __attribute__((ext_vector_type(4)));
-            V m;
+                for (int s = 0; s < KS; ++s)
+                    mma(acc, rows_contig<TB>(sB, rowsB, jt * 16, s * 32), rows_contig<TC>(sC, rowsC, it * 16, s * 32));
+                const int i = it * 16 + l16;
+                const Cum ci = sCum[k][i];
+                typedef T V __attribute__((ext_vector_type(4)));
+                V m;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = jt * 16 + g4 + r;
-                const float v = acc[r] * expf((float)(ci - sCum[k][j])) * sDt[k][j];
-                m[r] = from_f32<T>(j <= i ? v : 0.f);
+                for (int r = 0; r < 4; ++r) {
+                    const int j = jt * 16 + g4 + r;
+                    const float v = acc[r] * Pair<T>::decay(ci, sCum[k][j]) * sDt[k][j];
+                    m[r] = from_f32<T>(it > jt || j <= i ? v : 0.f);
+                }
+                *reinterpret_cast<V*>(sM + ((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4) = m;
+            };
+            // the ten tiles; the last wave, which also forms the decays, has the fewest
+            if constexpr (NW == 8) {
+                if (w == 0) { tile(3, 0); tile(0, 0); }
+                else if (w == 1) { tile(3, 1); tile(1, 0); }
+                else if (w == 2) { tile(3, 2); tile(1, 1); }
+                else if (w == 3) tile(3, 3);
+                else if (w == 4) tile(2, 0);
+                else if (w == 5) tile(2, 1);
+                else if (w == 6) tile(2, 2);
+            } else {
+                if (w == 0) { tile(3, 0); tile(3, 1); tile(0, 0); }
+                else if (w == 1) { tile(3, 2); tile(3, 3); tile(1, 0); }
+                else if (w == 2) { tile(2, 0); tile(2, 1); tile(2, 2); }
+                else tile(1, 1);
             }
-            *reinterpret_cast<V*>(sM + ((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4) = m;
-        };
-        if (w == 0) { tile(3, 0); tile(3, 1); tile(0, 0); }
-        else if (w == 1) { tile(3, 2); tile(3, 3); tile(1, 0); }
-        else if (w == 2) { tile(2, 0); tile(2, 1); }
-        else { tile(2, 2); tile(1, 1); }
-        // what the entering state gives: y^T[p, i] = exp(cum_i) sum_n S[n, p] c[i, n]
+            // what the entering state gives: y^T[p, i] = exp(cum_i) sum_n S[n, p] c[i, n]
 #pragma unroll
-        for (int it = 0; it < 4; ++it) Y[it] = zero4();
+            for (int it = 0; it < 4; ++it) Y[it] = zero4();
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const Frag<T> fs = frag_from_acc<T>(S[2 * s], S[2 * s + 1]);
+            for (int s = 0; s < KS; ++s) {
+                const Frag<T> fs = frag_from_acc<T>(S[2 * s], S[2 * s + 1]);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) mma(Y[it], fs, rows_perm<T, DK>(sC, it * 16 + l16, s * 32 + g4));
-        }
+                for (int it = 0; it < 4; ++it) mma(Y[it], fs, rows_perm<TC, T>(sC, permC, it * 16, s * 32));
+            }
 #pragma unroll
-        for (int it = 0; it < 4; ++it) Y[it] *= sE[k][it * 16 + l16];
+            for (int it = 0; it < 4; ++it) Y[it] *= sE[k][it * 16 + l16];
         }
         if (ch + 1 < nc) decays(ch + 1);
         if constexpr (!ENDS) cb::lds_barrier();  // M is in LDS
         Frag<T> fx[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) fx[s] = cols_perm<PS>(sX, s * 32, w * 16, lane);
+        for (int s = 0; s < 2; ++s) fx[s] = cols_perm<TX>(sX, bColsX, s * 32, w * 16);
         if constexpr (!ENDS) {
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
+            for (int it = 0; it < 4; ++it)
 #pragma unroll
-            for (int s = 0; s <= it / 2; ++s) {
-                Frag<T> fm;
-                const Vec<T, 8> v = load_vec<T, 8>(sM + ((it * 2 + s) * 64 + lane) * 8);
+                for (int s = 0; s <= it / 2; ++s) {
+                    Frag<T> fm;
+                    const Vec<T, 8> v = load_vec<T, 8>(sM + ((it * 2 + s) * 64 + lane) * 8);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) fm.v[e] = v.v[e];
-                mma(Y[it], fx[s], fm);
+                    for (int e = 0; e < 8; ++e) fm.v[e] = v.v[e];
+                    mma(Y[it], fx[s], fm);
+                }
+            const int rows = min(len - ch * Q, Q);
+            const auto qy = cb::buffer_over(gy + (int64_t)ch * Q * ys, rows * ys * ES);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int i = it * 16 + l16;
+                const Vec<T, 4> xv = lds_vec<T, 4>(sX, (bPermX ^ (w * 16 * ES)) + it * 16 * TX::RB);
+                float o[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] = Y[it][r] + D * to_f32(xv.v[r]);
+                bstore4<T>(qy, (i * ys + w * 16 + g4) * ES, o);
             }
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int i = it * 16 + l16;
-            const Vec<T, 4> xv = load_vec<T, 4>(sX + TX::at(i, w * 16 + g4));
-            float o[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = Y[it][r] + D * to_f32(xv.v[r]);
-            if (ch * Q + i < len) store_vec_any<T, 4>(gy + (int64_t)(ch * Q + i) * a.H * a.dv + w * 16 + g4, o);
-        }
         }
         // the next state
         const float gone = sE[k][Q - 1];
-        Planes<T> wx[2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[nt] *= gone;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float wt[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) wt[e] = sW[k][s * 32 + (e >> 2) * 16 + g4 + (e & 3)];
-            wx[s].set(fx[s], wt);
-        }
+            Planes<T> wx;
+            wx.set(fx[s], wt);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            S[nt] *= gone;
+            for (int nt = 0; nt < NT; ++nt) {
+                const Frag<T> fb = cols_perm<TB>(sB, colsB, s * 32, nt * 16);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag<T> fb = cols_perm<DK>(sB, s * 32, nt * 16, lane);
-#pragma unroll
-                for (int i = 0; i < Planes<T>::N; ++i) mma(S[nt], fb, wx[s].p[i]);
+                for (int i = 0; i < Planes<T>::N; ++i) mma(S[nt], fb, wx.p[i]);
             }
         }
         cb::lds_barrier();  // the chunk has been read
         if (ch + 1 < nc) store();
     }
     float* to = nullptr;
-    if (ENDS) to = a.starts + ((int64_t)(n * a.H + h) * a.segs + seg + 1) * size + at0;
-    else if (a.sT && (a.cu || seg == a.segs - 1)) to = a.sT + sbase;
+    if (ENDS) to = a.starts + (state * a.segs + seg + 1) * (DK * DV);
+    else if (a.sT && (a.cu || seg == a.segs - 1)) to = a.sT + state * (DK * DV);
     if (to) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) to[(int64_t)(nt * 16 + r) * a.dv] = S[nt][r];
+            for (int r = 0; r < 4; ++r) to[at0 + (nt * 16 + r) * DV] = S[nt][r];
     }
-    if (ENDS && slice == 0 && w == 3 && lane == 0) a.logs[(int64_t)(n * a.H + h) * a.segs + seg] = logs;
+    if (ENDS && tid == NTH - 64) a.logs[state * a.segs + seg] = logs;
 }
 
 // starts[0] = the initial state, starts[s + 1] = exp(logs[s]) starts[s] + the segment's own end,
@@ -410,29 +494,28 @@ Params params(const SsmArgs& a) {
                   (int)a.c_stride, a.softplus ? 1 : 0, 0, 0, 0, 1, 0, nullptr, nullptr};
 }
 
-// Parts of a slot's heads and slices: the fewest that leave the eight XCDs with about as many
-// units each (at most an eighth more than their share).
+// Parts of a slot's heads: the fewest that leave the eight XCDs with about as many units each (at
+// most an eighth more than their share).
 void set_grid(Params* p, int slots) {
-    const int hs = p->H * (p->dv / PS);
     p->slots = slots;
-    p->parts = hs;
-    for (int k = 1; k < hs; ++k) {
-        if (hs % k) continue;
+    p->parts = p->H;
+    for (int k = 1; k < p->H; ++k) {
+        if (p->H % k) continue;
         const int64_t units = (int64_t)slots * k;
         if ((units + 7) / 8 * 64 <= units * 9) {
             p->parts = k;
             break;
         }
     }
-    p->per = hs / p->parts;
+    p->per = p->H / p->parts;
 }
 unsigned grid_of(const Params& p) { return (unsigned)(((int64_t)p.slots * p.parts + 7) / 8 * 8 * p.per); }
 
-// Segments of a sequence.  A chain is one (sequence, head, 64 columns); a compute unit runs two
-// workgroups at once.  Chains that do not fill the GPU are cut so that their pieces do, of at least
-// 8 chunks each: a piece but the last is walked twice, once for the state alone.
+// Segments of a sequence.  A chain is one (sequence, head); a compute unit runs two workgroups at
+// once.  Chains that do not fill the GPU are cut so that their pieces do, of at least 8 chunks
+// each: a piece but the last is walked twice, once for the state alone.
 int segments(int64_t N, int64_t T, int64_t H, int64_t dv, int64_t cus) {
-    const int64_t chains = N * H * (dv / PS), nc = (T + Q - 1) / Q;
+    const int64_t chains = N * H, nc = (T + Q - 1) / Q;
     int64_t g = 2 * cus / chains;
     if (g > nc / 8) g = nc / 8;
     if (g < 2) return 1;
@@ -451,7 +534,7 @@ Layout layout(int64_t N, int64_t H, int64_t dk, int64_t dv, int64_t segs) {
     return l;
 }
 
-template <typename T, int DK>
+template <typename T, int DK, int NW>
 hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
     Params p = params(a);
     p.segs = workspace ? segments(a.N, a.T, a.H, a.dv, a.cus) : 1;
@@ -461,13 +544,19 @@ hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
         p.starts = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.starts);
         p.logs = reinterpret_cast<double*>(static_cast<char*>(workspace) + l.logs);
         set_grid(&p, (int)a.N * (p.segs - 1));
-        hipLaunchKernelGGL((chunk_kernel<T, DK, true>), dim3(grid_of(p)), dim3(256), 0, (hipStream_t)a.stream, p);
+        hipLaunchKernelGGL((chunk_kernel<T, DK, NW, true>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
         const int64_t quads = a.N * a.H * a.dk * a.dv / 4;
         hipLaunchKernelGGL(join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, (hipStream_t)a.stream, p, DK);
     }
     set_grid(&p, (int)a.N * p.segs);
-    hipLaunchKernelGGL((chunk_kernel<T, DK, false>), dim3(grid_of(p)), dim3(256), 0, (hipStream_t)a.stream, p);
+    hipLaunchKernelGGL((chunk_kernel<T, DK, NW, false>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_fwd(const SsmArgs& a, void* ws) {
+    if (a.dk == 128) return a.dv == 128 ? launch_chunks<T, 128, 8>(a, ws) : launch_chunks<T, 128, 4>(a, ws);
+    return a.dv == 128 ? launch_chunks<T, 64, 8>(a, ws) : launch_chunks<T, 64, 4>(a, ws);
 }
 
 // ---- single tokens --------------------------------------------------------------------------
@@ -534,9 +623,8 @@ size_t ssm_workspace_bytes(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t 
     return segs > 1 ? (size_t)ssm::layout(N, H, dk, dv, segs).total : 0;
 }
 
-hipError_t launch_ssm_fwd(const SsmArgs& a, void* ws) {
-    if (a.dtype_bf16) return a.dk == 128 ? ssm::launch_chunks<bf16, 128>(a, ws) : ssm::launch_chunks<bf16, 64>(a, ws);
-    return a.dk == 128 ? ssm::launch_chunks<float, 128>(a, ws) : ssm::launch_chunks<float, 64>(a, ws);
+hipError_t launch_ssm_fwd(const SsmArgs& a, void* workspace) {
+    return a.dtype_bf16 ? ssm::launch_fwd<bf16>(a, workspace) : ssm::launch_fwd<float>(a, workspace);
 }
 
 hipError_t launch_ssm_step(const SsmArgs& a) {
