@@ -83,7 +83,10 @@ __device__ __forceinline__ Frag<float> rows_contig(const float* t, int base, int
     }
     return f;
 }
-// The same in the permuted map: elements col + 4g .. + 3 and col + 16 + 4g .. + 3.
+// The same in the permuted map: elements col + 4g .. + 3 and col + 16 + 4g .. + 3.  The rows too
+// enter by XOR (16 rows are a power of two of bytes): two 8-byte reads that differ by a constant the
+// compiler merges into one, which runs in the phases of a 16-byte read with both of a lane's
+// halves in the same banks.
 template <typename TL>
 __device__ __forceinline__ int perm_base(int lane) { return TL::at(lane & 15, (lane >> 4) * 4); }
 template <typename TL, typename T>
@@ -91,7 +94,7 @@ __device__ __forceinline__ Frag<T> rows_perm(const T* t, int base, int r0, int c
     Frag<T> f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const Vec<T, 4> v = lds_vec<T, 4>(t, (base ^ ((col + 16 * h) * (int)sizeof(T))) + r0 * TL::RB);
+        const Vec<T, 4> v = lds_vec<T, 4>(t, base ^ ((col + 16 * h) * (int)sizeof(T) + r0 * TL::RB));
 #pragma unroll
         for (int e = 0; e < 4; ++e) f.v[4 * h + e] = v.v[e];
     }
@@ -226,33 +229,36 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
     else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(U4, v), r, off, 0, 0);
 }
 
-// waves per SIMD that the register budget is set for
-template <typename T, int NW> constexpr int kWaves = sizeof(T) == 4 ? (NW == 8 ? 2 : 1) : (NW == 8 ? 4 : 3);
-
-// A workgroup of NW waves walks the 16 NW = dv columns of one (sequence, head) chunk by chunk.
-// Wave w holds state columns 16w .. 16w + 15 in accumulators (rows n of all of them), computes its
-// share of M's ten 16 x 16 tiles into LDS, and forms y^T (columns by tokens) and the next state for
-// its columns.  The next chunk's inputs are loaded into registers meanwhile, through buffer
-// resources that end with the sequence: rows behind it read as zeros, and their y is dropped.
+// A workgroup of four waves walks HP heads of one sequence, HP DV = 16 PT columns per wave, chunk by
+// chunk: one head of 128 columns, two of 64 that share b and c (c . b is then formed once for
+// both), or one of 64.  Wave w holds its state columns in accumulators (rows n of all of them),
+// computes its share of M's ten 16 x 16 tiles into LDS, and forms y^T (columns by tokens) and the
+// next state for its columns.  Two tiles of columns a wave halve the LDS reads of b, c and M, which
+// at one tile took as long as the products.  The next chunk's inputs are loaded into registers
+// meanwhile, through buffer resources that end with the sequence: rows behind it read as zeros, and
+// their y is dropped.
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
-template <typename T, int DK, int NW, bool ENDS>
-__global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params a) {
-    constexpr int DV = 16 * NW, NTH = 64 * NW, ES = (int)sizeof(T);
+template <typename T, int DK, int DV, int HP, int NW, bool ENDS>
+__global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void chunk_kernel(Params a) {
+    constexpr int CW = HP * DV, PT = CW / (16 * NW), NTH = 64 * NW, ES = (int)sizeof(T);
     typedef Tile<T, DK, kCols> TB;
     typedef Tile<T, DK, kRows> TC;
-    typedef Tile<T, DV, kBoth> TX;
+    typedef Tile<T, CW, kBoth> TX;
     typedef typename Pair<T>::Cum Cum;
     constexpr int NB = Q * TB::UPR / NTH, NX = Q * TX::UPR / NTH;  // 16-byte units per thread
     constexpr int NT = DK / 16, KS = DK / 32;
-    __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[ENDS ? 8 : Q * DK], sX[Q * DV], sM[ENDS ? 8 : 4 * 2 * 64 * 8];
-    __shared__ __attribute__((aligned(16))) Cum sCum[2][Q];
-    __shared__ __attribute__((aligned(16))) float sDt[2][Q], sE[2][Q], sW[2][Q];
+    __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[ENDS ? 8 : Q * DK], sX[Q * CW];
+    __shared__ __attribute__((aligned(16))) T sM[ENDS ? 1 : HP][ENDS ? 8 : 4 * 2 * 64 * 8];
+    __shared__ __attribute__((aligned(16))) Cum sCum[2][HP][Q];
+    __shared__ __attribute__((aligned(16))) float sDt[2][HP][Q], sE[2][HP][Q], sW[2][HP][Q];
 
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, l16 = lane & 15;
     const int g4 = (lane >> 4) * 4;
-    int slot, h;
-    if (!unit_of(a, &slot, &h)) return;
+    int slot, hb;
+    if (!unit_of(a, &slot, &hb)) return;
+    const int h0 = hb * HP, hw = w * 16 * PT / DV;  // the first head, this wave's among them
+    const int c0 = w * 16 * PT;                     // its first column of the workgroup's
     const int steps = ENDS ? a.segs - 1 : a.segs;  // slots of a sequence
     static_assert(sizeof(sB) >= (kMaxSort + 1) * sizeof(int), "scratch of longest_first");
     const int n = a.cu ? __builtin_amdgcn_readfirstlane(longest_first(a.cu, a.N, slot, (int)a.T, reinterpret_cast<int*>(sB)))
@@ -267,31 +273,35 @@ __global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params 
         hi = min(hi, lo + (int64_t)a.seg_chunks * Q);
     }
     const int len = (int)(hi - lo), nc = (len + Q - 1) / Q;
-    const int group = h / (a.H / a.G);
-    const T* gx = (const T*)a.x + lo * a.xs + h * DV;
+    const int group = h0 / (a.H / a.G);
+    const T* gx = (const T*)a.x + lo * a.xs + h0 * DV;
     const T* gb = (const T*)a.b + lo * a.bs + group * DK;
     const T* gc = (const T*)a.c + lo * a.cs + group * DK;
-    const T* gt = (const T*)a.dt + lo * a.dts + h;
-    T* gy = (T*)a.y + (lo * a.H + h) * DV;
+    const int dh = NW - 1 - w;  // below HP: the wave forms that head's decays
+    const T* gt = (const T*)a.dt + lo * a.dts + h0 + dh;
+    T* gy = (T*)a.y + (lo * a.H + h0) * DV;
     const int ys = a.H * DV;
-    const float A = a.A[h], D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    const float A = dh < HP ? a.A[h0 + dh] : 0.f, bias = dh < HP && a.dt_bias ? a.dt_bias[h0 + dh] : 0.f;
+    const float D = a.D ? a.D[h0 + hw] : 0.f;
 
-    f32x4 S[NT];  // rows 16 nt + 4g + r, column 16 w + lane % 16
-    const int64_t state = (int64_t)n * a.H + h;
-    const int at0 = g4 * DV + w * 16 + l16;
+    f32x4 S[PT][NT];  // rows 16 nt + 4g + r, column c0 + 16 pt + lane % 16
+    const int64_t state = (int64_t)n * a.H + h0 + hw;
+    const int at0 = g4 * DV + c0 % DV + l16;
     const float* from = a.s0 ? a.s0 + state * (DK * DV) : nullptr;
     if (a.segs > 1) from = ENDS ? nullptr : a.starts + (state * a.segs + seg) * (DK * DV);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[nt][r] = from ? from[at0 + (nt * 16 + r) * DV] : 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[pt][nt][r] = from ? from[at0 + pt * 16 + (nt * 16 + r) * DV] : 0.f;
     double logs = 0.0;  // ENDS: the logarithm of the segment's decay
     // halves of M's operands that no tile writes: tiles above the diagonal
-    if (!ENDS && w == 0) {
+    if (!ENDS && w < HP) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sM[((0 * 2 + 0) * 64 + lane) * 8 + 4 + e] = from_f32<T>(0.f);
+        for (int e = 0; e < 4; ++e) sM[w][((0 * 2 + 0) * 64 + lane) * 8 + 4 + e] = from_f32<T>(0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sM[((2 * 2 + 1) * 64 + lane) * 8 + 4 + e] = from_f32<T>(0.f);
+        for (int e = 0; e < 4; ++e) sM[w][((2 * 2 + 1) * 64 + lane) * 8 + 4 + e] = from_f32<T>(0.f);
     }
 
     U4 rb[NB], rc[NB], rx[NX];
@@ -313,7 +323,10 @@ __global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params 
             const int id = tid + NTH * k, row = id / TX::UPR, u = id % TX::UPR;
             rx[k] = bload16(qx, row * a.xs * ES + u * 16);
         }
-        if (w == NW - 1) rdt = lane < rows ? to_f32(gt[(t0 + lane) * a.dts]) : 0.f;
+    };
+    // a head's raw time steps of chunk ch, a token per lane
+    auto load_dt = [&](int ch) {
+        if (dh < HP) rdt = lane < len - ch * Q ? to_f32(gt[((int64_t)ch * Q + lane) * a.dts]) : 0.f;
     };
     const int stB = TB::at(tid / TB::UPR, tid % TB::UPR * TB::EPU), stC = TC::at(tid / TB::UPR, tid % TB::UPR * TB::EPU);
     const int stX = TX::at(tid / TX::UPR, tid % TX::UPR * TX::EPU);
@@ -334,10 +347,10 @@ __global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params 
     };
     const int bRowsB = rows_base<TB>(lane), bRowsC = rows_base<TC>(lane), bPermC = perm_base<TC>(lane);
     const int bColsB = cols_base<TB, T>(lane), bColsX = cols_base<TX, T>(lane), bPermX = perm_base<TX>(lane);
-    // decays of chunk ch, a token per lane of the last wave: a token behind the end decays and
+    // decays of chunk ch, a token per lane of the last waves: a token behind the end decays and
     // adds nothing
     auto decays = [&](int ch) {
-        if (w != NW - 1) return;
+        if (dh >= HP) return;
         const int k = ch & 1;
         const float dt = lane < len - ch * Q ? time_step(rdt + bias, a.softplus) : 0.f;
         double cum = (double)dt * (double)A;
@@ -348,23 +361,25 @@ __global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params 
         }
         const double all = __shfl(cum, 63);
         if constexpr (ENDS) logs += all;
-        sCum[k][lane] = Pair<T>::cum(cum);
-        sDt[k][lane] = dt;
-        sE[k][lane] = expf((float)cum);
-        sW[k][lane] = expf((float)(all - cum)) * dt;
+        sCum[k][dh][lane] = Pair<T>::cum(cum);
+        sDt[k][dh][lane] = dt;
+        sE[k][dh][lane] = expf((float)cum);
+        sW[k][dh][lane] = expf((float)(all - cum)) * dt;
     };
 
     if (nc > 0) {
+        load_dt(0);
         load(0);
         decays(0);
+        load_dt(1);
         store();
     }
     for (int ch = 0; ch < nc; ++ch) {
         const int k = ch & 1;
         cb::lds_barrier();  // the chunk is in LDS
         if (ch + 1 < nc) load(ch + 1);
-        const int rowsB = fresh(bRowsB), rowsC = fresh(bRowsC), permC = fresh(bPermC), colsB = fresh(bColsB);
-        f32x4 Y[4];
+        const int rowsB = fresh(bRowsB), rowsC = fresh(bRowsC), permC = fresh(bPermC), colsB = fresh(bColsB), permX = fresh(bPermX);
+        f32x4 Y[PT][4];
         if constexpr (!ENDS) {
             auto tile = [&](int it, int jt) {
                 f32x4 acc = zero4();
@@ -372,18 +387,21 @@ __global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params 
                 for (int s = 0; s < KS; ++s)
                     mma(acc, rows_contig<TB>(sB, rowsB, jt * 16, s * 32), rows_contig<TC>(sC, rowsC, it * 16, s * 32));
                 const int i = it * 16 + l16;
-                const Cum ci = sCum[k][i];
-                typedef T V __attribute__((ext_vector_type(4)));
-                V m;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = jt * 16 + g4 + r;
-                    const float v = acc[r] * Pair<T>::decay(ci, sCum[k][j]) * sDt[k][j];
-                    m[r] = from_f32<T>(it > jt || j <= i ? v : 0.f);
+                for (int hp = 0; hp < HP; ++hp) {
+                    const Cum ci = sCum[k][hp][i];
+                    typedef T V __attribute__((ext_vector_type(4)));
+                    V m;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = jt * 16 + g4 + r;
+                        const float v = acc[r] * Pair<T>::decay(ci, sCum[k][hp][j]) * sDt[k][hp][j];
+                        m[r] = from_f32<T>(it > jt || j <= i ? v : 0.f);
+                    }
+                    *reinterpret_cast<V*>(&sM[hp][((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4]) = m;
                 }
-                *reinterpret_cast<V*>(sM + ((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4) = m;
             };
-            // the ten tiles; the last wave, which also forms the decays, has the fewest
+            // the ten tiles; a wave that also forms decays has fewer
             if constexpr (NW == 8) {
                 if (w == 0) { tile(3, 0); tile(0, 0); }
                 else if (w == 1) { tile(3, 1); tile(1, 0); }
@@ -392,68 +410,91 @@ __global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params 
                 else if (w == 4) tile(2, 0);
                 else if (w == 5) tile(2, 1);
                 else if (w == 6) tile(2, 2);
-            } else {
-                if (w == 0) { tile(3, 0); tile(3, 1); tile(0, 0); }
-                else if (w == 1) { tile(3, 2); tile(3, 3); tile(1, 0); }
-                else if (w == 2) { tile(2, 0); tile(2, 1); tile(2, 2); }
-                else tile(1, 1);
-            }
+            } else if (w == 0) { tile(3, 0); tile(3, 1); tile(0, 0); }
+            else if (w == 1) { tile(3, 2); tile(3, 3); tile(1, 0); }
+            else if (w == 2) { tile(2, 0); tile(2, 1); if (HP == 1) tile(2, 2); }
+            else { tile(1, 1); if (HP == 2) tile(2, 2); }
             // what the entering state gives: y^T[p, i] = exp(cum_i) sum_n S[n, p] c[i, n]
 #pragma unroll
-            for (int it = 0; it < 4; ++it) Y[it] = zero4();
+            for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+                for (int it = 0; it < 4; ++it) Y[pt][it] = zero4();
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const Frag<T> fs = frag_from_acc<T>(S[2 * s], S[2 * s + 1]);
+                Frag<T> fs[PT];
 #pragma unroll
-                for (int it = 0; it < 4; ++it) mma(Y[it], fs, rows_perm<TC, T>(sC, permC, it * 16, s * 32));
+                for (int pt = 0; pt < PT; ++pt) fs[pt] = frag_from_acc<T>(S[pt][2 * s], S[pt][2 * s + 1]);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const Frag<T> fc = rows_perm<TC, T>(sC, permC, it * 16, s * 32);
+#pragma unroll
+                    for (int pt = 0; pt < PT; ++pt) mma(Y[pt][it], fs[pt], fc);
+                }
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it) Y[it] *= sE[k][it * 16 + l16];
-        }
-        if (ch + 1 < nc) decays(ch + 1);
-        if constexpr (!ENDS) cb::lds_barrier();  // M is in LDS
-        Frag<T> fx[2];
+            for (int it = 0; it < 4; ++it) {
+                const float e = sE[k][hw][it * 16 + l16];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) fx[s] = cols_perm<TX>(sX, bColsX, s * 32, w * 16);
+                for (int pt = 0; pt < PT; ++pt) Y[pt][it] *= e;
+            }
+        }
+        // a chunk's time steps are loaded a chunk ahead of the rest: loads return in order, and a
+        // wait for them here must not be one for the next chunk
+        if (ch + 1 < nc) decays(ch + 1);
+        load_dt(ch + 2);
+        if constexpr (!ENDS) cb::lds_barrier();  // M is in LDS
+        Frag<T> fx[PT][2];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) fx[pt][s] = cols_perm<TX>(sX, bColsX, s * 32, c0 + pt * 16);
         if constexpr (!ENDS) {
 #pragma unroll
             for (int it = 0; it < 4; ++it)
 #pragma unroll
                 for (int s = 0; s <= it / 2; ++s) {
                     Frag<T> fm;
-                    const Vec<T, 8> v = load_vec<T, 8>(sM + ((it * 2 + s) * 64 + lane) * 8);
+                    const Vec<T, 8> v = load_vec<T, 8>(&sM[hw][((it * 2 + s) * 64 + lane) * 8]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) fm.v[e] = v.v[e];
-                    mma(Y[it], fx[s], fm);
+#pragma unroll
+                    for (int pt = 0; pt < PT; ++pt) mma(Y[pt][it], fx[pt][s], fm);
                 }
             const int rows = min(len - ch * Q, Q);
             const auto qy = cb::buffer_over(gy + (int64_t)ch * Q * ys, rows * ys * ES);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const int i = it * 16 + l16;
-                const Vec<T, 4> xv = lds_vec<T, 4>(sX, (bPermX ^ (w * 16 * ES)) + it * 16 * TX::RB);
-                float o[4];
+            for (int it = 0; it < 4; ++it)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] = Y[it][r] + D * to_f32(xv.v[r]);
-                bstore4<T>(qy, (i * ys + w * 16 + g4) * ES, o);
-            }
+                for (int pt = 0; pt < PT; ++pt) {
+                    const int i = it * 16 + l16, c = c0 + pt * 16;
+                    const Vec<T, 4> xv = lds_vec<T, 4>(sX, permX ^ (c * ES + it * 16 * TX::RB));
+                    float o[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[r] = Y[pt][it][r] + D * to_f32(xv.v[r]);
+                    bstore4<T>(qy, (i * ys + c + g4) * ES, o);
+                }
         }
         // the next state
-        const float gone = sE[k][Q - 1];
+        const float gone = sE[k][hw][Q - 1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S[nt] *= gone;
+        for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= gone;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float wt[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wt[e] = sW[k][s * 32 + (e >> 2) * 16 + g4 + (e & 3)];
-            Planes<T> wx;
-            wx.set(fx[s], wt);
+            for (int e = 0; e < 8; ++e) wt[e] = sW[k][hw][s * 32 + (e >> 2) * 16 + g4 + (e & 3)];
+            Planes<T> wx[PT];
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) wx[pt].set(fx[pt][s], wt);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const Frag<T> fb = cols_perm<TB>(sB, colsB, s * 32, nt * 16);
 #pragma unroll
-                for (int i = 0; i < Planes<T>::N; ++i) mma(S[nt], fb, wx.p[i]);
+                for (int i = 0; i < Planes<T>::N; ++i)
+#pragma unroll
+                    for (int pt = 0; pt < PT; ++pt) mma(S[pt][nt], fb, wx[pt].p[i]);
             }
         }
         cb::lds_barrier();  // the chunk has been read
@@ -464,11 +505,13 @@ __global__ __launch_bounds__(64 * NW, (kWaves<T, NW>)) void chunk_kernel(Params 
     else if (a.sT && (a.cu || seg == a.segs - 1)) to = a.sT + state * (DK * DV);
     if (to) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) to[at0 + (nt * 16 + r) * DV] = S[nt][r];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) to[at0 + pt * 16 + (nt * 16 + r) * DV] = S[pt][nt][r];
     }
-    if (ENDS && tid == NTH - 64) a.logs[state * a.segs + seg] = logs;
+    if (ENDS && dh < HP && lane == 0) a.logs[((int64_t)n * a.H + h0 + dh) * a.segs + seg] = logs;
 }
 
 // starts[0] = the initial state, starts[s + 1] = exp(logs[s]) starts[s] + the segment's own end,
@@ -494,28 +537,28 @@ Params params(const SsmArgs& a) {
                   (int)a.c_stride, a.softplus ? 1 : 0, 0, 0, 0, 1, 0, nullptr, nullptr};
 }
 
-// Parts of a slot's heads: the fewest that leave the eight XCDs with about as many units each (at
+// Parts of a slot's `blocks` workgroups: the fewest that leave the eight XCDs with about as many units each (at
 // most an eighth more than their share).
-void set_grid(Params* p, int slots) {
+void set_grid(Params* p, int slots, int blocks) {
     p->slots = slots;
-    p->parts = p->H;
-    for (int k = 1; k < p->H; ++k) {
-        if (p->H % k) continue;
+    p->parts = blocks;
+    for (int k = 1; k < blocks; ++k) {
+        if (blocks % k) continue;
         const int64_t units = (int64_t)slots * k;
         if ((units + 7) / 8 * 64 <= units * 9) {
             p->parts = k;
             break;
         }
     }
-    p->per = p->H / p->parts;
+    p->per = blocks / p->parts;
 }
 unsigned grid_of(const Params& p) { return (unsigned)(((int64_t)p.slots * p.parts + 7) / 8 * 8 * p.per); }
 
-// Segments of a sequence.  A chain is one (sequence, head); a compute unit runs two workgroups at
-// once.  Chains that do not fill the GPU are cut so that their pieces do, of at least 8 chunks
+// Segments of a sequence.  A chain is 128 columns of a sequence's heads; a compute unit runs two
+// workgroups at once.  Chains that do not fill the GPU are cut so that their pieces do, of at least 8 chunks
 // each: a piece but the last is walked twice, once for the state alone.
 int segments(int64_t N, int64_t T, int64_t H, int64_t dv, int64_t cus) {
-    const int64_t chains = N * H, nc = (T + Q - 1) / Q;
+    const int64_t chains = (N * H * dv + 127) / 128, nc = (T + Q - 1) / Q;
     int64_t g = 2 * cus / chains;
     if (g > nc / 8) g = nc / 8;
     if (g < 2) return 1;
@@ -534,7 +577,7 @@ Layout layout(int64_t N, int64_t H, int64_t dk, int64_t dv, int64_t segs) {
     return l;
 }
 
-template <typename T, int DK, int NW>
+template <typename T, int DK, int DV, int HP, int NW>
 hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
     Params p = params(a);
     p.segs = workspace ? segments(a.N, a.T, a.H, a.dv, a.cus) : 1;
@@ -543,20 +586,29 @@ hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
         const Layout l = layout(a.N, a.H, a.dk, a.dv, p.segs);
         p.starts = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.starts);
         p.logs = reinterpret_cast<double*>(static_cast<char*>(workspace) + l.logs);
-        set_grid(&p, (int)a.N * (p.segs - 1));
-        hipLaunchKernelGGL((chunk_kernel<T, DK, NW, true>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
+        set_grid(&p, (int)a.N * (p.segs - 1), (int)a.H / HP);
+        hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, NW, true>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
         const int64_t quads = a.N * a.H * a.dk * a.dv / 4;
         hipLaunchKernelGGL(join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, (hipStream_t)a.stream, p, DK);
     }
-    set_grid(&p, (int)a.N * p.segs);
-    hipLaunchKernelGGL((chunk_kernel<T, DK, NW, false>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
+    set_grid(&p, (int)a.N * p.segs, (int)a.H / HP);
+    hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, NW, false>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
     return hipGetLastError();
 }
 
+#ifndef KNW
+#define KNW 4
+#endif
+constexpr int kNW = KNW;
+template <typename T, int DK>
+hipError_t launch_dk(const SsmArgs& a, void* ws) {
+    if (a.dv == 128) return launch_chunks<T, DK, 128, 1, kNW>(a, ws);
+    // two heads a workgroup where a group has an even number of them
+    return a.H / a.G % 2 == 0 ? launch_chunks<T, DK, 64, 2, kNW>(a, ws) : launch_chunks<T, DK, 64, 1, 4>(a, ws);
+}
 template <typename T>
 hipError_t launch_fwd(const SsmArgs& a, void* ws) {
-    if (a.dk == 128) return a.dv == 128 ? launch_chunks<T, 128, 8>(a, ws) : launch_chunks<T, 128, 4>(a, ws);
-    return a.dv == 128 ? launch_chunks<T, 64, 8>(a, ws) : launch_chunks<T, 64, 4>(a, ws);
+    return a.dk == 128 ? launch_dk<T, 128>(a, ws) : launch_dk<T, 64>(a, ws);
 }
 
 // ---- single tokens --------------------------------------------------------------------------
