@@ -19,13 +19,44 @@ namespace ssm {
 
 constexpr int Q = 64;  // tokens of a chunk
 
+constexpr int AHEAD = 8;  // chunks whose decays are in LDS, formed four at a time
+
 typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // raw + bias, through softplus where asked: max(v, 0) + log(1 + e^-|v|).  The library's log1p and
 // exp: once per token and head, and final states keep their fp32 accuracy.
 __device__ __forceinline__ float time_step(float v, bool softplus) {
     return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
 }
+
+// v of another lane by a DPP control, 0 where there is none (rows: the 16-lane rows that take it)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// inclusive sums over the wave's lanes: shifts within rows of 16, then each row's sum to the rows
+// behind it.  In LDS permutes the same sums kept a wave, and the barrier it reaches last, 3000
+// cycles a chunk.
+__device__ __forceinline__ double scan(double v) {
+    v += dpp<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+    v += dpp<0x112, 0xf>(v);
+    v += dpp<0x114, 0xf>(v);
+    v += dpp<0x118, 0xf>(v);
+    v += dpp<0x142, 0xa>(v);  // row_bcast 15 to rows 1 and 3
+    v += dpp<0x143, 0xc>(v);  // row_bcast 31 to rows 2 and 3
+    return v;
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, 63), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// e^v, rounded to fp32 once before the hardware's base-2 exponential
+__device__ __forceinline__ float exp_of(double v) { return __builtin_amdgcn_exp2f((float)(v * 1.4426950408889634)); }
 
 // ---- LDS tiles ------------------------------------------------------------------------------
 // [64 tokens][W] row-major, in 16-byte units whose place in the row is XORed with a function of
@@ -143,12 +174,16 @@ template <> struct Planes<bf16> {
     Frag<bf16> p[3];
     __device__ __forceinline__ void set(const Frag<bf16>& x, const float (&w)[8]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v = (float)x.v[e] * w[e];
+        for (int e = 0; e < 8; e += 2) {  // pairs: one conversion packs two
+            f32x2 v = {(float)x.v[e] * w[e], (float)x.v[e + 1] * w[e + 1]};
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                p[i].v[e] = (bf16)v;
-                v -= (float)p[i].v[e];
+                const bf16x2 r = __builtin_convertvector(v, bf16x2);
+                p[i].v[e] = r[0];
+                p[i].v[e + 1] = r[1];
+                const uint32_t u = __builtin_bit_cast(uint32_t, r);
+                v[0] -= __uint_as_float(u << 16);
+                v[1] -= __uint_as_float(u & 0xffff0000u);
             }
         }
     }
@@ -170,11 +205,13 @@ template <typename T> struct Pair {
     typedef float Cum;
     __device__ static __forceinline__ Cum cum(double v) { return (float)(v * 1.4426950408889634); }
     __device__ static __forceinline__ float decay(Cum i, Cum j) { return __builtin_amdgcn_exp2f(i - j); }
+    __device__ static __forceinline__ float decay(Cum i) { return __builtin_amdgcn_exp2f(i); }
 };
 template <> struct Pair<float> {
     typedef double Cum;
     __device__ static __forceinline__ Cum cum(double v) { return v; }
-    __device__ static __forceinline__ float decay(Cum i, Cum j) { return expf((float)(i - j)); }
+    __device__ static __forceinline__ float decay(Cum i, Cum j) { return exp_of(i - j); }
+    __device__ static __forceinline__ float decay(Cum i) { return exp_of(i); }
 };
 
 struct Params {
@@ -239,7 +276,8 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
 // their y is dropped.
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
-template <typename T, int DK, int DV, int HP, int NW, bool ENDS>
+constexpr int NW = 4;
+template <typename T, int DK, int DV, int HP, bool ENDS>
 __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void chunk_kernel(Params a) {
     constexpr int CW = HP * DV, PT = CW / (16 * NW), NTH = 64 * NW, ES = (int)sizeof(T);
     typedef Tile<T, DK, kCols> TB;
@@ -250,8 +288,8 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     constexpr int NT = DK / 16, KS = DK / 32;
     __shared__ __attribute__((aligned(16))) T sB[Q * DK], sC[ENDS ? 8 : Q * DK], sX[Q * CW];
     __shared__ __attribute__((aligned(16))) T sM[ENDS ? 1 : HP][ENDS ? 8 : 4 * 2 * 64 * 8];
-    __shared__ __attribute__((aligned(16))) Cum sCum[2][HP][Q];
-    __shared__ __attribute__((aligned(16))) float sDt[2][HP][Q], sE[2][HP][Q], sW[2][HP][Q];
+    __shared__ __attribute__((aligned(16))) Cum sCum[AHEAD][HP][Q];
+    __shared__ __attribute__((aligned(16))) float sDt[AHEAD][HP][Q], sW[AHEAD][HP][Q];
 
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, l16 = lane & 15;
     const int g4 = (lane >> 4) * 4;
@@ -277,11 +315,9 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     const T* gx = (const T*)a.x + lo * a.xs + h0 * DV;
     const T* gb = (const T*)a.b + lo * a.bs + group * DK;
     const T* gc = (const T*)a.c + lo * a.cs + group * DK;
-    const int dh = NW - 1 - w;  // below HP: the wave forms that head's decays
-    const T* gt = (const T*)a.dt + lo * a.dts + h0 + dh;
+    const T* gt = (const T*)a.dt + lo * a.dts + h0;
     T* gy = (T*)a.y + (lo * a.H + h0) * DV;
     const int ys = a.H * DV;
-    const float A = dh < HP ? a.A[h0 + dh] : 0.f, bias = dh < HP && a.dt_bias ? a.dt_bias[h0 + dh] : 0.f;
     const float D = a.D ? a.D[h0 + hw] : 0.f;
 
     f32x4 S[PT][NT];  // rows 16 nt + 4g + r, column c0 + 16 pt + lane % 16
@@ -295,7 +331,6 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[pt][nt][r] = from ? from[at0 + pt * 16 + (nt * 16 + r) * DV] : 0.f;
-    double logs = 0.0;  // ENDS: the logarithm of the segment's decay
     // halves of M's operands that no tile writes: tiles above the diagonal
     if (!ENDS && w < HP) {
 #pragma unroll
@@ -305,7 +340,6 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     }
 
     U4 rb[NB], rc[NB], rx[NX];
-    float rdt = 0.f;
     auto load = [&](int ch) {
         const int64_t t0 = (int64_t)ch * Q;
         const int rows = min(len - ch * Q, Q);
@@ -324,9 +358,28 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
             rx[k] = bload16(qx, row * a.xs * ES + u * 16);
         }
     };
-    // a head's raw time steps of chunk ch, a token per lane
+    // Decays of the four chunks from ch on, a chunk a wave, a token a lane: a token behind the end
+    // decays and adds nothing.  One wave at a time forming the next chunk's kept the others waiting
+    // for 2000 of 14000 cycles.  The raw time steps are loaded a chunk before they are needed.
+    float rdt[HP];
     auto load_dt = [&](int ch) {
-        if (dh < HP) rdt = lane < len - ch * Q ? to_f32(gt[((int64_t)ch * Q + lane) * a.dts]) : 0.f;
+        const int t = (ch + w) * Q + lane;
+#pragma unroll
+        for (int hp = 0; hp < HP; ++hp) rdt[hp] = t < len ? to_f32(gt[(int64_t)t * a.dts + hp]) : 0.f;
+    };
+    double logs[HP] = {};  // ENDS: this wave's part of the logarithms of the segment's decays
+    auto decays = [&](int ch) {
+        const int k = (ch + w) % AHEAD;
+#pragma unroll
+        for (int hp = 0; hp < HP; ++hp) {
+            const float bias = a.dt_bias ? a.dt_bias[h0 + hp] : 0.f;
+            const float dt = (ch + w) * Q + lane < len ? time_step(rdt[hp] + bias, a.softplus) : 0.f;
+            const double cum = scan((double)dt * (double)a.A[h0 + hp]), all = last_lane(cum);
+            if constexpr (ENDS) logs[hp] += all;
+            sCum[k][hp][lane] = Pair<T>::cum(cum);
+            sDt[k][hp][lane] = dt;
+            sW[k][hp][lane] = exp_of(all - cum) * dt;
+        }
     };
     const int stB = TB::at(tid / TB::UPR, tid % TB::UPR * TB::EPU), stC = TC::at(tid / TB::UPR, tid % TB::UPR * TB::EPU);
     const int stX = TX::at(tid / TX::UPR, tid % TX::UPR * TX::EPU);
@@ -347,73 +400,48 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     };
     const int bRowsB = rows_base<TB>(lane), bRowsC = rows_base<TC>(lane), bPermC = perm_base<TC>(lane);
     const int bColsB = cols_base<TB, T>(lane), bColsX = cols_base<TX, T>(lane), bPermX = perm_base<TX>(lane);
-    // decays of chunk ch, a token per lane of the last waves: a token behind the end decays and
-    // adds nothing
-    auto decays = [&](int ch) {
-        if (dh >= HP) return;
-        const int k = ch & 1;
-        const float dt = lane < len - ch * Q ? time_step(rdt + bias, a.softplus) : 0.f;
-        double cum = (double)dt * (double)A;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double up = __shfl_up(cum, d);
-            if (lane >= d) cum += up;
-        }
-        const double all = __shfl(cum, 63);
-        if constexpr (ENDS) logs += all;
-        sCum[k][dh][lane] = Pair<T>::cum(cum);
-        sDt[k][dh][lane] = dt;
-        sE[k][dh][lane] = expf((float)cum);
-        sW[k][dh][lane] = expf((float)(all - cum)) * dt;
-    };
-
     if (nc > 0) {
         load_dt(0);
         load(0);
         decays(0);
-        load_dt(1);
         store();
     }
     for (int ch = 0; ch < nc; ++ch) {
-        const int k = ch & 1;
+        const int k = ch % AHEAD;
         cb::lds_barrier();  // the chunk is in LDS
+        // loads return in order: a wait for the time steps must not be one for the next chunk
+        if (ch % 4 == 2) load_dt(ch + 2);
         if (ch + 1 < nc) load(ch + 1);
         const int rowsB = fresh(bRowsB), rowsC = fresh(bRowsC), permC = fresh(bPermC), colsB = fresh(bColsB), permX = fresh(bPermX);
         f32x4 Y[PT][4];
         if constexpr (!ENDS) {
-            auto tile = [&](int it, int jt) {
+            // M's ten tiles (it, jt), jt <= it, three a wave (two of them twice), with no branch that
+            // would keep them apart from the products below
+            const int its = w == 0 ? 0x033 : w == 1 ? 0x133 : w == 2 ? 0x222 : 0x111;
+            const int jts = w == 0 ? 0x010 : w == 1 ? 0x032 : w == 2 ? 0x210 : 0x111;
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                const int it = its >> (4 * t) & 15, jt = jts >> (4 * t) & 15;
+                const int rb = rowsB + jt * 16 * TB::RB, rcc = rowsC + it * 16 * TC::RB;
                 f32x4 acc = zero4();
 #pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    mma(acc, rows_contig<TB>(sB, rowsB, jt * 16, s * 32), rows_contig<TC>(sC, rowsC, it * 16, s * 32));
-                const int i = it * 16 + l16;
+                for (int s = 0; s < KS; ++s) mma(acc, rows_contig<TB>(sB, rb, 0, s * 32), rows_contig<TC>(sC, rcc, 0, s * 32));
+                const int i = it * 16 + l16, j = jt * 16 + g4;
 #pragma unroll
                 for (int hp = 0; hp < HP; ++hp) {
                     const Cum ci = sCum[k][hp][i];
+                    const Vec<Cum, 4> cj = load_vec<Cum, 4>(&sCum[k][hp][j]);
+                    const Vec<float, 4> dj = load_vec<float, 4>(&sDt[k][hp][j]);
                     typedef T V __attribute__((ext_vector_type(4)));
                     V m;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int j = jt * 16 + g4 + r;
-                        const float v = acc[r] * Pair<T>::decay(ci, sCum[k][hp][j]) * sDt[k][hp][j];
-                        m[r] = from_f32<T>(it > jt || j <= i ? v : 0.f);
+                        const float v = acc[r] * Pair<T>::decay(ci, cj.v[r]) * dj.v[r];
+                        m[r] = from_f32<T>(j + r <= i ? v : 0.f);
                     }
                     *reinterpret_cast<V*>(&sM[hp][((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4]) = m;
                 }
-            };
-            // the ten tiles; a wave that also forms decays has fewer
-            if constexpr (NW == 8) {
-                if (w == 0) { tile(3, 0); tile(0, 0); }
-                else if (w == 1) { tile(3, 1); tile(1, 0); }
-                else if (w == 2) { tile(3, 2); tile(1, 1); }
-                else if (w == 3) tile(3, 3);
-                else if (w == 4) tile(2, 0);
-                else if (w == 5) tile(2, 1);
-                else if (w == 6) tile(2, 2);
-            } else if (w == 0) { tile(3, 0); tile(3, 1); tile(0, 0); }
-            else if (w == 1) { tile(3, 2); tile(3, 3); tile(1, 0); }
-            else if (w == 2) { tile(2, 0); tile(2, 1); if (HP == 1) tile(2, 2); }
-            else { tile(1, 1); if (HP == 2) tile(2, 2); }
+            }
             // what the entering state gives: y^T[p, i] = exp(cum_i) sum_n S[n, p] c[i, n]
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt)
@@ -433,15 +461,11 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
             }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                const float e = sE[k][hw][it * 16 + l16];
+                const float e = Pair<T>::decay(sCum[k][hw][it * 16 + l16]);
 #pragma unroll
                 for (int pt = 0; pt < PT; ++pt) Y[pt][it] *= e;
             }
         }
-        // a chunk's time steps are loaded a chunk ahead of the rest: loads return in order, and a
-        // wait for them here must not be one for the next chunk
-        if (ch + 1 < nc) decays(ch + 1);
-        load_dt(ch + 2);
         if constexpr (!ENDS) cb::lds_barrier();  // M is in LDS
         Frag<T> fx[PT][2];
 #pragma unroll
@@ -475,7 +499,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
                 }
         }
         // the next state
-        const float gone = sE[k][hw][Q - 1];
+        const float gone = Pair<T>::decay(sCum[k][hw][Q - 1]);
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
@@ -484,7 +508,11 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         for (int s = 0; s < 2; ++s) {
             float wt[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wt[e] = sW[k][hw][s * 32 + (e >> 2) * 16 + g4 + (e & 3)];
+            for (int e = 0; e < 8; e += 4) {
+                const Vec<float, 4> v = load_vec<float, 4>(&sW[k][hw][s * 32 + e * 4 + g4]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) wt[e + r] = v.v[r];
+            }
             Planes<T> wx[PT];
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) wx[pt].set(fx[pt][s], wt);
@@ -497,6 +525,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
                     for (int pt = 0; pt < PT; ++pt) mma(S[pt][nt], fb, wx[pt].p[i]);
             }
         }
+        if (ch % 4 == 3) decays(ch + 1);
         cb::lds_barrier();  // the chunk has been read
         if (ch + 1 < nc) store();
     }
@@ -511,7 +540,14 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
 #pragma unroll
                 for (int r = 0; r < 4; ++r) to[at0 + pt * 16 + (nt * 16 + r) * DV] = S[pt][nt][r];
     }
-    if (ENDS && dh < HP && lane == 0) a.logs[((int64_t)n * a.H + h0 + dh) * a.segs + seg] = logs;
+    if constexpr (ENDS) {
+        __shared__ double sLogs[HP][NW];
+#pragma unroll
+        for (int hp = 0; hp < HP; ++hp)
+            if (lane == 0) sLogs[hp][w] = logs[hp];
+        __syncthreads();
+        if (tid < HP) a.logs[((int64_t)n * a.H + h0 + tid) * a.segs + seg] = (sLogs[tid][0] + sLogs[tid][1]) + (sLogs[tid][2] + sLogs[tid][3]);
+    }
 }
 
 // starts[0] = the initial state, starts[s + 1] = exp(logs[s]) starts[s] + the segment's own end,
@@ -577,7 +613,7 @@ Layout layout(int64_t N, int64_t H, int64_t dk, int64_t dv, int64_t segs) {
     return l;
 }
 
-template <typename T, int DK, int DV, int HP, int NW>
+template <typename T, int DK, int DV, int HP>
 hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
     Params p = params(a);
     p.segs = workspace ? segments(a.N, a.T, a.H, a.dv, a.cus) : 1;
@@ -587,24 +623,20 @@ hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
         p.starts = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.starts);
         p.logs = reinterpret_cast<double*>(static_cast<char*>(workspace) + l.logs);
         set_grid(&p, (int)a.N * (p.segs - 1), (int)a.H / HP);
-        hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, NW, true>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
+        hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, true>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
         const int64_t quads = a.N * a.H * a.dk * a.dv / 4;
         hipLaunchKernelGGL(join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, (hipStream_t)a.stream, p, DK);
     }
     set_grid(&p, (int)a.N * p.segs, (int)a.H / HP);
-    hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, NW, false>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
+    hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, false>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
     return hipGetLastError();
 }
 
-#ifndef KNW
-#define KNW 4
-#endif
-constexpr int kNW = KNW;
 template <typename T, int DK>
 hipError_t launch_dk(const SsmArgs& a, void* ws) {
-    if (a.dv == 128) return launch_chunks<T, DK, 128, 1, kNW>(a, ws);
+    if (a.dv == 128) return launch_chunks<T, DK, 128, 1>(a, ws);
     // two heads a workgroup where a group has an even number of them
-    return a.H / a.G % 2 == 0 ? launch_chunks<T, DK, 64, 2, kNW>(a, ws) : launch_chunks<T, DK, 64, 1, 4>(a, ws);
+    return a.H / a.G % 2 == 0 ? launch_chunks<T, DK, 64, 2>(a, ws) : launch_chunks<T, DK, 64, 1>(a, ws);
 }
 template <typename T>
 hipError_t launch_fwd(const SsmArgs& a, void* ws) {
