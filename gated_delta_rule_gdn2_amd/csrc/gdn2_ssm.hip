@@ -172,28 +172,26 @@ template <typename T> struct Planes;
 template <> struct Planes<bf16> {
     static constexpr int N = 3;
     Frag<bf16> p[3];
-    __device__ __forceinline__ void set(const Frag<bf16>& x, const float (&w)[8]) {
+    // elements e and e + 1, e even: one conversion packs two
+    __device__ __forceinline__ void set(const Frag<bf16>& x, int e, float w0, float w1) {
+        f32x2 v = {(float)x.v[e] * w0, (float)x.v[e + 1] * w1};
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {  // pairs: one conversion packs two
-            f32x2 v = {(float)x.v[e] * w[e], (float)x.v[e + 1] * w[e + 1]};
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const bf16x2 r = __builtin_convertvector(v, bf16x2);
-                p[i].v[e] = r[0];
-                p[i].v[e + 1] = r[1];
-                const uint32_t u = __builtin_bit_cast(uint32_t, r);
-                v[0] -= __uint_as_float(u << 16);
-                v[1] -= __uint_as_float(u & 0xffff0000u);
-            }
+        for (int i = 0; i < 3; ++i) {
+            const bf16x2 r = __builtin_convertvector(v, bf16x2);
+            p[i].v[e] = r[0];
+            p[i].v[e + 1] = r[1];
+            const uint32_t u = __builtin_bit_cast(uint32_t, r);
+            v[0] -= __uint_as_float(u << 16);
+            v[1] -= __uint_as_float(u & 0xffff0000u);
         }
     }
 };
 template <> struct Planes<float> {
     static constexpr int N = 1;
     Frag<float> p[1];
-    __device__ __forceinline__ void set(const Frag<float>& x, const float (&w)[8]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[0].v[e] = x.v[e] * w[e];
+    __device__ __forceinline__ void set(const Frag<float>& x, int e, float w0, float w1) {
+        p[0].v[e] = x.v[e] * w0;
+        p[0].v[e + 1] = x.v[e + 1] * w1;
     }
 };
 
@@ -414,33 +412,42 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         if (ch + 1 < nc) load(ch + 1);
         const int rowsB = fresh(bRowsB), rowsC = fresh(bRowsC), permC = fresh(bPermC), colsB = fresh(bColsB), permX = fresh(bPermX);
         f32x4 Y[PT][4];
+        // Every stage reads the next one's operands before its own products, and carries as much
+        // vector work of another stage as its products leave issue slots for; the fences keep the
+        // compiler from gathering either.
         if constexpr (!ENDS) {
-            // M's ten tiles (it, jt), jt <= it, three a wave (two of them twice), with no branch that
-            // would keep them apart from the products below
+            // M's ten tiles (it, jt), jt <= it, three a wave (two of them twice)
             const int its = w == 0 ? 0x033 : w == 1 ? 0x133 : w == 2 ? 0x222 : 0x111;
             const int jts = w == 0 ? 0x010 : w == 1 ? 0x032 : w == 2 ? 0x210 : 0x111;
+            int ob[3], oc[3];
 #pragma unroll
             for (int t = 0; t < 3; ++t) {
-                const int it = its >> (4 * t) & 15, jt = jts >> (4 * t) & 15;
-                const int rb = rowsB + jt * 16 * TB::RB, rcc = rowsC + it * 16 * TC::RB;
-                f32x4 acc = zero4();
+                ob[t] = rowsB + (jts >> (4 * t) & 15) * 16 * TB::RB;
+                oc[t] = rowsC + (its >> (4 * t) & 15) * 16 * TC::RB;
+            }
+            f32x4 G[3] = {zero4(), zero4(), zero4()};
+            Frag<T> gb_[2][3], gc_[2][3], fc[2][4];
+            auto read_g = [&](int s) {
 #pragma unroll
-                for (int s = 0; s < KS; ++s) mma(acc, rows_contig<TB>(sB, rb, 0, s * 32), rows_contig<TC>(sC, rcc, 0, s * 32));
-                const int i = it * 16 + l16, j = jt * 16 + g4;
-#pragma unroll
-                for (int hp = 0; hp < HP; ++hp) {
-                    const Cum ci = sCum[k][hp][i];
-                    const Vec<Cum, 4> cj = load_vec<Cum, 4>(&sCum[k][hp][j]);
-                    const Vec<float, 4> dj = load_vec<float, 4>(&sDt[k][hp][j]);
-                    typedef T V __attribute__((ext_vector_type(4)));
-                    V m;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float v = acc[r] * Pair<T>::decay(ci, cj.v[r]) * dj.v[r];
-                        m[r] = from_f32<T>(j + r <= i ? v : 0.f);
-                    }
-                    *reinterpret_cast<V*>(&sM[hp][((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4]) = m;
+                for (int t = 0; t < 3; ++t) {
+                    gb_[s & 1][t] = rows_contig<TB>(sB, ob[t], 0, s * 32);
+                    gc_[s & 1][t] = rows_contig<TC>(sC, oc[t], 0, s * 32);
                 }
+            };
+            auto read_c = [&](int s) {
+#pragma unroll
+                for (int it = 0; it < 4; ++it) fc[s & 1][it] = rows_perm<TC, T>(sC, permC, it * 16, s * 32);
+            };
+            read_g(0);
+            cb::sched_fence();
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                if (s + 1 < KS) read_g(s + 1);
+                else read_c(0);
+                cb::sched_fence();
+#pragma unroll
+                for (int t = 0; t < 3; ++t) mma(G[t], gb_[s & 1][t], gc_[s & 1][t]);
+                cb::sched_fence();
             }
             // what the entering state gives: y^T[p, i] = exp(cum_i) sum_n S[n, p] c[i, n]
 #pragma unroll
@@ -449,15 +456,35 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
                 for (int it = 0; it < 4; ++it) Y[pt][it] = zero4();
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
+                if (s + 1 < KS) read_c(s + 1);
                 Frag<T> fs[PT];
 #pragma unroll
                 for (int pt = 0; pt < PT; ++pt) fs[pt] = frag_from_acc<T>(S[pt][2 * s], S[pt][2 * s + 1]);
+                cb::sched_fence();
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const Frag<T> fc = rows_perm<TC, T>(sC, permC, it * 16, s * 32);
+                for (int it = 0; it < 4; ++it)
 #pragma unroll
-                    for (int pt = 0; pt < PT; ++pt) mma(Y[pt][it], fs[pt], fc);
+                    for (int pt = 0; pt < PT; ++pt) mma(Y[pt][it], fs[pt], fc[s & 1][it]);
+                // a tile of M beside them
+#pragma unroll
+                for (int t = s * 3 / KS; t < (s + 1) * 3 / KS; ++t) {
+                    const int it = its >> (4 * t) & 15, jt = jts >> (4 * t) & 15, i = it * 16 + l16, j = jt * 16 + g4;
+#pragma unroll
+                    for (int hp = 0; hp < HP; ++hp) {
+                        const Cum ci = sCum[k][hp][i];
+                        const Vec<Cum, 4> cj = load_vec<Cum, 4>(&sCum[k][hp][j]);
+                        const Vec<float, 4> dj = load_vec<float, 4>(&sDt[k][hp][j]);
+                        typedef T V __attribute__((ext_vector_type(4)));
+                        V m;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float v = G[t][r] * Pair<T>::decay(ci, cj.v[r]) * dj.v[r];
+                            m[r] = from_f32<T>(j + r <= i ? v : 0.f);
+                        }
+                        *reinterpret_cast<V*>(&sM[hp][((it * 2 + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4]) = m;
+                    }
                 }
+                cb::sched_fence();
             }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
@@ -465,65 +492,103 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
 #pragma unroll
                 for (int pt = 0; pt < PT; ++pt) Y[pt][it] *= e;
             }
+            cb::lds_barrier();  // M is in LDS
         }
-        if constexpr (!ENDS) cb::lds_barrier();  // M is in LDS
-        Frag<T> fx[PT][2];
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) fx[pt][s] = cols_perm<TX>(sX, bColsX, s * 32, c0 + pt * 16);
-        if constexpr (!ENDS) {
-#pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int s = 0; s <= it / 2; ++s) {
-                    Frag<T> fm;
-                    const Vec<T, 8> v = load_vec<T, 8>(&sM[hw][((it * 2 + s) * 64 + lane) * 8]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) fm.v[e] = v.v[e];
-#pragma unroll
-                    for (int pt = 0; pt < PT; ++pt) mma(Y[pt][it], fx[pt][s], fm);
-                }
-            const int rows = min(len - ch * Q, Q);
-            const auto qy = cb::buffer_over(gy + (int64_t)ch * Q * ys, rows * ys * ES);
-#pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int pt = 0; pt < PT; ++pt) {
-                    const int i = it * 16 + l16, c = c0 + pt * 16;
-                    const Vec<T, 4> xv = lds_vec<T, 4>(sX, permX ^ (c * ES + it * 16 * TX::RB));
-                    float o[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = Y[pt][it][r] + D * to_f32(xv.v[r]);
-                    bstore4<T>(qy, (i * ys + c + g4) * ES, o);
-                }
-        }
-        // the next state
-        const float gone = Pair<T>::decay(sCum[k][hw][Q - 1]);
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= gone;
+        Frag<T> fx[PT][2], fb[3];
+        float wt[2][8];
+        Planes<T> wx[2][PT];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            float wt[8];
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) fx[pt][s] = cols_perm<TX>(sX, bColsX, s * 32, c0 + pt * 16);
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
                 const Vec<float, 4> v = load_vec<float, 4>(&sW[k][hw][s * 32 + e * 4 + g4]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) wt[e + r] = v.v[r];
+                for (int r = 0; r < 4; ++r) wt[s][e + r] = v.v[r];
             }
-            Planes<T> wx[PT];
+        }
+        // pair u of the 4 PT pairs of weighted x that tokens 32 s on need
+        auto plane = [&](int s, int u) { wx[s][u / 4].set(fx[u / 4][s], u % 4 * 2, wt[s][u % 4 * 2], wt[s][u % 4 * 2 + 1]); };
+        const int rows = min(len - ch * Q, Q);
+        const auto qy = cb::buffer_over(gy + (int64_t)ch * Q * ys, rows * ys * ES);
+        Vec<T, 4> xq[2];
+        auto read_x = [&](int u) { xq[u & 1] = lds_vec<T, 4>(sX, permX ^ ((c0 + u % PT * 16) * ES + u / PT * 16 * TX::RB)); };
+        auto put_y = [&](int u) {
+            const int it = u / PT, pt = u % PT;
+            float o[4];
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) wx[pt].set(fx[pt][s], wt);
+            for (int r = 0; r < 4; ++r) o[r] = Y[pt][it][r] + D * to_f32(xq[u & 1].v[r]);
+            bstore4<T>(qy, ((it * 16 + l16) * ys + c0 + pt * 16 + g4) * ES, o);
+        };
+        if constexpr (!ENDS) {
+            // the chunk's own part: six pieces of M, with the first half's planes beside them
+            Frag<T> fm[2];
+            auto read_m = [&](int u) {
+                const int it = u < 2 ? u : u < 4 ? 2 : 3, s = u < 2 ? 0 : u & 1;
+                const Vec<T, 8> v = load_vec<T, 8>(&sM[hw][((it * 2 + s) * 64 + lane) * 8]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const Frag<T> fb = cols_perm<TB>(sB, colsB, s * 32, nt * 16);
+                for (int e = 0; e < 8; ++e) fm[u & 1].v[e] = v.v[e];
+            };
+            read_m(0);
+            read_x(0);
+            read_x(1);
+            cb::sched_fence();
 #pragma unroll
-                for (int i = 0; i < Planes<T>::N; ++i)
+            for (int u = 0; u < 6; ++u) {
+                const int it = u < 2 ? u : u < 4 ? 2 : 3, s = u < 2 ? 0 : u & 1;
+                if (u < 5) read_m(u + 1);
+                cb::sched_fence();
 #pragma unroll
-                    for (int pt = 0; pt < PT; ++pt) mma(S[pt][nt], fb, wx[pt].p[i]);
+                for (int pt = 0; pt < PT; ++pt) mma(Y[pt][it], fx[pt][s], fm[u & 1]);
+#pragma unroll
+                for (int v = u * 4 * PT / 6; v < (u + 1) * 4 * PT / 6; ++v) plane(0, v);
+                cb::sched_fence();
+                // y of the 16 tokens whose last piece was the one before
+                const int done = u == 1 ? 0 : u == 2 ? 1 : u == 4 ? 2 : -1;
+                if (done >= 0) {
+#pragma unroll
+                    for (int v = done * PT; v < done * PT + PT; ++v) {
+                        put_y(v);
+                        if (v + 2 < 4 * PT) read_x(v + 2);
+                    }
+                }
             }
+#pragma unroll
+            for (int v = 3 * PT; v < 4 * PT; ++v) {
+                put_y(v);
+                if (v + 2 < 4 * PT) read_x(v + 2);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4 * PT; ++v) plane(0, v);
+        }
+        // the next state, a tile of rows at a time
+        const float gone = Pair<T>::decay(sCum[k][hw][Q - 1]);
+        auto read_b = [&](int u) { fb[u % 3] = cols_perm<TB>(sB, colsB, u / NT * 32, u % NT * 16); };
+        auto scale = [&](int nt) {
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) S[pt][nt] *= gone;
+        };
+        read_b(0);
+        read_b(1);
+        scale(0);
+        cb::sched_fence();
+#pragma unroll
+        for (int u = 0; u < 2 * NT; ++u) {
+            const int s = u / NT, nt = u % NT;
+            if (u + 2 < 2 * NT) read_b(u + 2);
+            cb::sched_fence();
+#pragma unroll
+            for (int i = 0; i < Planes<T>::N; ++i)
+#pragma unroll
+                for (int pt = 0; pt < PT; ++pt) mma(S[pt][nt], fb[u % 3], wx[s][pt].p[i]);
+            if (s == 0) {
+                if (nt + 1 < NT) scale(nt + 1);
+#pragma unroll
+                for (int v = nt * 4 * PT / NT; v < (nt + 1) * 4 * PT / NT; ++v) plane(1, v);
+            }
+            cb::sched_fence();
         }
         if (ch % 4 == 3) decays(ch + 1);
         cb::lds_barrier();  // the chunk has been read
