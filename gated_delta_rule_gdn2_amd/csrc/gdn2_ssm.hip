@@ -358,12 +358,13 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     };
     // Decays of the four chunks from ch on, a chunk a wave, a token a lane: a token behind the end
     // decays and adds nothing.  One wave at a time forming the next chunk's kept the others waiting
-    // for 2000 of 14000 cycles.  The raw time steps are loaded a chunk before they are needed.
-    float rdt[HP];
+    // for 2000 of 14000 cycles.  The raw time steps are loaded a chunk
+    // before they are needed, and carried as they are: widening them would wait for them.
+    T rdt[HP];
     auto load_dt = [&](int ch) {
-        const int t = (ch + w) * Q + lane;
+        const int t = min((ch + w) * Q + lane, len - 1);
 #pragma unroll
-        for (int hp = 0; hp < HP; ++hp) rdt[hp] = t < len ? to_f32(gt[(int64_t)t * a.dts + hp]) : 0.f;
+        for (int hp = 0; hp < HP; ++hp) rdt[hp] = gt[(int64_t)t * a.dts + hp];
     };
     double logs[HP] = {};  // ENDS: this wave's part of the logarithms of the segment's decays
     auto decays = [&](int ch) {
@@ -371,7 +372,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
 #pragma unroll
         for (int hp = 0; hp < HP; ++hp) {
             const float bias = a.dt_bias ? a.dt_bias[h0 + hp] : 0.f;
-            const float dt = (ch + w) * Q + lane < len ? time_step(rdt[hp] + bias, a.softplus) : 0.f;
+            const float dt = (ch + w) * Q + lane < len ? time_step(to_f32(rdt[hp]) + bias, a.softplus) : 0.f;
             const double cum = scan((double)dt * (double)a.A[h0 + hp]), all = last_lane(cum);
             if constexpr (ENDS) logs[hp] += all;
             sCum[k][hp][lane] = Pair<T>::cum(cum);
