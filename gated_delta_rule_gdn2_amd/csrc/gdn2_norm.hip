@@ -6,23 +6,25 @@
 //   dx = rstd (v - mean(v) - u mean(u v)),  dgamma = sum over rows of dy u,  dbeta = sum of dy.
 //
 // Both passes read each row once, into registers: the variance is a second pass over registers, not
-// a difference of sums, so a row far from zero keeps its accuracy.  LANES lanes share a row, a
-// wave up to 2048 columns (8 to 32 elements a lane; no LDS, no barrier), a workgroup of 256 to 1024
-// threads above (16 elements a lane: the backward pass holds five values an element in registers).  Workgroups stay for many rows, with gamma (and in the backward pass the sums
-// over rows) of a lane's columns in registers.  Statistics and sums are fp32; y and dx are rounded
-// once, on the store.  Bound by HBM.
+// a difference of sums, so a row far from zero keeps its accuracy.  8 elements a lane (16 above 8192
+// columns): a row takes 16 lanes (up to 128 columns) to a wave (512; no barrier), or a workgroup of
+// 128 to 1024 threads.  Workgroups stay for many rows, with gamma (and in the backward pass the sums over rows)
+// of a lane's columns in registers.  Statistics and sums are fp32; y and dx are rounded once, on the
+// store.  Bound by HBM, so what counts is rows in flight: 32768 rows of 2048 in bf16 took 98 us
+// forward and 118 us backward at 32 elements a lane, a wave a row, against 61 and 83 us
+// (4.4 and 4.8 TB/s, the rate of a large copy) at 8.
 #include "gdn2_device.h"
 #include "gdn2_launch.h"
 
 namespace gdn2 {
 namespace norm {
 
-// The sum of one value per lane, over the wave and in every lane of it: shifts within rows of 16
-// lanes, then each row's sum to the rows behind it.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
 }
+// The sum of one value per lane, over the wave and in every lane of it: shifts within rows of 16
+// lanes, then each row's sum to the rows behind it.
 __device__ __forceinline__ float wave_sum(float v) {
     v += dpp<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
     v += dpp<0x112, 0xf>(v);
@@ -33,10 +35,18 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// the same over the LANES lanes of a row; sums alternate between two slots of scratch, so that one
-// barrier a sum is enough
+// The same over the LANES lanes of a row.  Sums alternate between two slots of scratch, so that one
+// barrier a sum is enough.
 template <int LANES>
-__device__ __forceinline__ float row_sum(float v, float (*scratch)[LANES / 64], int slot) {
+__device__ __forceinline__ float row_sum(float v, float (*scratch)[LANES > 64 ? LANES / 64 : 1], int slot) {
+    if constexpr (LANES < 64) {
+        v += dpp<0x128, 0xf>(v);  // row_ror 8, 4, 2, 1
+        v += dpp<0x124, 0xf>(v);
+        v += dpp<0x122, 0xf>(v);
+        v += dpp<0x121, 0xf>(v);
+        if constexpr (LANES == 32) v += __shfl_xor(v, 16);
+        return v;
+    }
     v = wave_sum(v);
     if constexpr (LANES > 64) {
         if ((threadIdx.x & 63) == 0) scratch[slot][threadIdx.x >> 6] = v;
@@ -95,7 +105,7 @@ __device__ __forceinline__ void load_columns(float (&g)[NV * V], const float* p,
     }
 }
 
-template <int LANES> constexpr int kThreads = LANES < 256 ? 256 : LANES;
+template <int LANES> constexpr int kThreads = LANES <= 64 ? 256 : LANES;  // whole rows a workgroup
 
 template <typename T, int LANES, int NV>
 __global__ __launch_bounds__(kThreads<LANES>) void fwd_kernel(const T* __restrict__ x, const float* __restrict__ gamma,
@@ -104,7 +114,7 @@ __global__ __launch_bounds__(kThreads<LANES>) void fwd_kernel(const T* __restric
                                                               int64_t rows, int width, float eps) {
     typedef Row<T, LANES, NV> R;
     constexpr int E = NV * R::V, RPB = kThreads<LANES> / LANES;  // elements a lane, rows a workgroup
-    __shared__ float scratch[2][LANES / 64];
+    __shared__ float scratch[2][LANES > 64 ? LANES / 64 : 1];
     const int lane = threadIdx.x % LANES;
     const float inv = 1.f / (float)width;
     float g[E], b[E];
@@ -146,7 +156,7 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(const T* __restric
                                                               float* __restrict__ parts, int64_t rows, int width) {
     typedef Row<T, LANES, NV> R;
     constexpr int E = NV * R::V, RPB = kThreads<LANES> / LANES;
-    __shared__ float scratch[2][LANES / 64];
+    __shared__ float scratch[2][LANES > 64 ? LANES / 64 : 1];
     __shared__ float join[RPB > 1 ? 2 * LANES * E : 1];
     const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv = 1.f / (float)width;
@@ -236,23 +246,34 @@ __global__ __launch_bounds__(kJoinCols* kJoinRows) void join_kernel(const float*
     }
 }
 
-int rows_per_block(int64_t width) { return width <= 2048 ? 4 : 1; }
-// workgroups that stay: enough to fill the GPU, few enough that the parts' sums are a small share
-constexpr int64_t kFwdBlocks = 2048, kParts = 512;
+// lanes of a row and threads of a workgroup, by the row's width (as by_width)
+int lanes_of(int64_t width) {
+    int lanes = 16;
+    while (lanes < 1024 && width > lanes * 8) lanes *= 2;
+    return lanes;
+}
+int threads_of(int64_t width) { return lanes_of(width) <= 64 ? 256 : lanes_of(width); }
+// Workgroups that stay: those that fit the GPU at once by the registers they take, 8 waves a SIMD
+// forward and 6 backward (of which workgroups of 16 waves do not fill the last third: two rounds of
+// them).  Twice as many lost up to a third (the last ones start late), half as many up to a half.
+template <int LANES> constexpr int64_t kFwdBlocks = (1 << 19) / kThreads<LANES>;
+int64_t parts_limit(int64_t width) { return threads_of(width) == 1024 ? 512 : 3 * (1 << 17) / threads_of(width); }
 int parts_of(int64_t rows, int64_t width) {
-    const int64_t rpb = rows_per_block(width), b = (rows + rpb - 1) / rpb;
-    return (int)(b < kParts ? b : kParts);
+    const int64_t rpb = threads_of(width) / lanes_of(width), b = (rows + rpb - 1) / rpb, most = parts_limit(width);
+    return (int)(b < most ? b : most);
 }
 
 // f<LANES, NV> for a row's width
 template <typename T, typename F>
 hipError_t by_width(int64_t width, F f) {
     constexpr int V = 16 / (int)sizeof(T);
+    if (width <= 16 * 8) return f.template run<16, 8 / V>();
+    if (width <= 32 * 8) return f.template run<32, 8 / V>();
     if (width <= 64 * 8) return f.template run<64, 8 / V>();
-    if (width <= 64 * 16) return f.template run<64, 16 / V>();
-    if (width <= 64 * 32) return f.template run<64, 32 / V>();
-    if (width <= 256 * 16) return f.template run<256, 16 / V>();
-    if (width <= 512 * 16) return f.template run<512, 16 / V>();
+    if (width <= 128 * 8) return f.template run<128, 8 / V>();
+    if (width <= 256 * 8) return f.template run<256, 8 / V>();
+    if (width <= 512 * 8) return f.template run<512, 8 / V>();
+    if (width <= 1024 * 8) return f.template run<1024, 8 / V>();
     return f.template run<1024, 16 / V>();
 }
 
@@ -262,7 +283,7 @@ struct Fwd {
     template <int LANES, int NV>
     hipError_t run() const {
         constexpr int RPB = kThreads<LANES> / LANES;
-        const int64_t want = (a.rows + RPB - 1) / RPB, blocks = want < kFwdBlocks ? want : kFwdBlocks;
+        const int64_t want = (a.rows + RPB - 1) / RPB, blocks = want < kFwdBlocks<LANES> ? want : kFwdBlocks<LANES>;
         hipLaunchKernelGGL((fwd_kernel<T, LANES, NV>), dim3((unsigned)blocks), dim3(kThreads<LANES>), 0,
                            (hipStream_t)a.stream, (const T*)a.x, a.gamma, a.beta, (T*)a.y, a.mean, a.rstd, a.rows,
                            (int)a.width, a.eps);
