@@ -712,8 +712,11 @@ hipError_t launch_fwd(const SsmArgs& a, void* ws) {
 // ---- single tokens --------------------------------------------------------------------------
 // As the recurrence's decode step: a workgroup owns the state of one (sequence, head), read and
 // written once with 16-byte accesses; a thread holds a column quad of its rows, and y's sums over
-// the rows go through LDS.  Bound by HBM.
-template <typename T, int DK, int DV>
+// the rows go through LDS.  Bound by HBM.  STREAM: past the caches, for states of which two do not
+// fit them together.  Such a state is not there any more when its layer's next token comes: three
+// of 268 MB in turn take 96 us a step instead of 105 (one alone, which no stack of layers has, would
+// take 95 instead of 80).
+template <typename T, int DK, int DV, bool STREAM>
 __global__ __launch_bounds__(256) void step_kernel(Params a) {
     constexpr int NQ = DV / 4, NRG = 256 / NQ, RPG = DK / NRG;
     static_assert(RPG * NRG == DK && NQ * NRG == 256, "step tiling");
@@ -725,7 +728,11 @@ __global__ __launch_bounds__(256) void step_kernel(Params a) {
     float* st = a.sT + ((int64_t)blockIdx.x * DK + rg * RPG) * DV + cq * 4;
     f32x4 s[RPG];
 #pragma unroll
-    for (int i = 0; i < RPG; ++i) s[i] = *reinterpret_cast<const f32x4*>(st + (int64_t)i * DV);
+    for (int i = 0; i < RPG; ++i) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(st + (int64_t)i * DV);
+        if constexpr (STREAM) s[i] = __builtin_nontemporal_load(p);
+        else s[i] = *p;
+    }
     if (tid < DK) {
         sB[tid] = to_f32(((const T*)a.b)[n * a.bs + group * DK + tid]);
         sC[tid] = to_f32(((const T*)a.c)[n * a.cs + group * DK + tid]);
@@ -742,7 +749,9 @@ __global__ __launch_bounds__(256) void step_kernel(Params a) {
         const float b = sB[rg * RPG + i], c = sC[rg * RPG + i];
         s[i] = s[i] * decay + b * dx;
         acc += s[i] * c;
-        *reinterpret_cast<f32x4*>(st + (int64_t)i * DV) = s[i];
+        f32x4* p = reinterpret_cast<f32x4*>(st + (int64_t)i * DV);
+        if constexpr (STREAM) __builtin_nontemporal_store(s[i], p);
+        else *p = s[i];
     }
     *reinterpret_cast<f32x4*>(&sRed[rg][cq * 4]) = acc;
     __syncthreads();
@@ -756,8 +765,9 @@ __global__ __launch_bounds__(256) void step_kernel(Params a) {
 
 template <typename T, int DK, int DV>
 hipError_t launch_step_t(const SsmArgs& a) {
-    hipLaunchKernelGGL((step_kernel<T, DK, DV>), dim3((unsigned)(a.N * a.H)), dim3(256), 0, (hipStream_t)a.stream,
-                       params(a));
+    const bool stream = a.N * a.H * DK * DV * 4 > (int64_t)128 << 20;  // the last cache holds 256 MB
+    auto kernel = stream ? step_kernel<T, DK, DV, true> : step_kernel<T, DK, DV, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(a.N * a.H)), dim3(256), 0, (hipStream_t)a.stream, params(a));
     return hipGetLastError();
 }
 template <typename T>
