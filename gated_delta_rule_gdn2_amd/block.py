@@ -24,7 +24,8 @@ import torch
 
 from . import _DTYPES, Gdn2Error, _check, _load, _ptr
 
-__all__ = ["ssm_fwd", "ssm_fwd_varlen", "ssm_fwd_workspace_bytes", "ssm_step", "short_conv", "short_conv_varlen",
+__all__ = ["ssm_fwd", "ssm_fwd_varlen", "ssm_fwd_workspace_bytes", "ssm_fwd_varlen_workspace_bytes",
+           "ssm_step", "short_conv", "short_conv_varlen",
            "short_conv_step", "layer_norm", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes"]
 
 _F32 = torch.float32
@@ -35,7 +36,8 @@ def _declare(lib):
     for name, args, res in (
             ("ssm_fwd", [P] * 10 + [I64] * 10 + [I32, I32, P, SZ, P], I32),
             ("ssm_fwd_workspace_bytes", [I64] * 5 + [I32], SZ),
-            ("ssm_fwd_varlen", [P] * 11 + [I64] * 10 + [I32, I32, P], I32),
+            ("ssm_fwd_varlen", [P] * 11 + [I64] * 10 + [I32, I32, P, SZ, P], I32),
+            ("ssm_fwd_varlen_workspace_bytes", [I64] * 5 + [I32], SZ),
             ("ssm_step", [P] * 9 + [I64] * 9 + [I32, I32, P], I32),
             ("short_conv", [P] * 6 + [I64] * 4 + [I32, P], I32),
             ("short_conv_varlen", [P] * 7 + [I64] * 4 + [I32, P], I32),
@@ -194,8 +196,13 @@ def ssm_fwd_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16) -> int:
     return int(_load().gdn2_ssm_fwd_workspace_bytes(B, T, H, dk, dv, _DTYPES[dtype]))
 
 
+def ssm_fwd_varlen_workspace_bytes(N, total_T, H, dk, dv, dtype=torch.bfloat16) -> int:
+    """Device workspace (bytes) with which ssm_fwd_varlen is fastest for these sizes (0: it takes none)."""
+    return int(_load().gdn2_ssm_fwd_varlen_workspace_bytes(N, total_T, H, dk, dv, _DTYPES[dtype]))
+
+
 def ssm_fwd_varlen(x, dt, B, C, A, cu_seqlens, D=None, dt_bias=None, initial_state=None, *, y=None, final_state=None,
-                   output_final_state=True, softplus=True):
+                   output_final_state=True, softplus=True, workspace=None):
     """ssm_fwd over N sequences packed along the token axis: x [total_T,H,dv], dt [total_T,H],
     B, C [total_T,G,dk], cu_seqlens int64 [N+1] on the device, states [N,H,dk,dv], which
     ssm_step continues from."""
@@ -208,8 +215,10 @@ def ssm_fwd_varlen(x, dt, B, C, A, cu_seqlens, D=None, dt_bias=None, initial_sta
     y = _out("y", y, lead + (H, dv), x.dtype, dev)
     if final_state is not None or output_final_state:
         final_state = _out("final_state", final_state, sshape, _F32, dev)
+    need = _load().gdn2_ssm_fwd_varlen_workspace_bytes(n, lead[0], H, dk, dv, code)
+    ws, ws_bytes, keep = _workspace(workspace, need, 256, dev) if need else (None, 0, None)
     _launch("gdn2_ssm_fwd_varlen", dev, *ptrs, s0, y.data_ptr(), _ptr(final_state), cu_seqlens.data_ptr(), n, lead[0],
-            H, G, dk, dv, *strides, code, int(softplus))
+            H, G, dk, dv, *strides, code, int(softplus), ws, ws_bytes)
     return y, final_state
 
 

@@ -81,6 +81,37 @@ gdn2_status_t check_ssm(const gdn2::SsmArgs& a, gdn2_dtype_t dtype, int64_t toke
     return GDN2_OK;
 }
 
+size_t ssm_workspace(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, gdn2_dtype_t dtype) {
+    if (N < 1 || T < 1 || H < 1 || N > INT_MAX || T > INT_MAX || H > INT_MAX || N * H > INT_MAX / 64) return 0;
+    if (!gdn2::ssm_supported(dk, dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32)) return 0;
+    const int cus = device_cus();
+    return gdn2::ssm_workspace_bytes(packed, N, T, H, dk, dv, cus > 0 ? cus : 256);
+}
+
+// the scan of whole or packed prompts, with `tokens` rows in all
+gdn2_status_t ssm_fwd(gdn2::SsmArgs a, gdn2_dtype_t dtype, int64_t tokens, void* workspace, size_t workspace_bytes) {
+    const gdn2_status_t st = check_ssm(a, dtype, tokens, false);
+    if (st != GDN2_OK) return st;
+    if (workspace || workspace_bytes) {
+        const size_t need = ssm_workspace(a.cu_seqlens != nullptr, a.N, a.T, a.H, a.dk, a.dv, dtype);
+        if (need == 0 || !workspace || workspace_bytes < need) return GDN2_ERR_WORKSPACE;
+        if (!aligned_to(workspace, 256)) return GDN2_ERR_MISALIGNED;
+        const int64_t es = elem(dtype), nt = tokens - 1, ns = a.N * a.H * a.dk * a.dv * 4;
+        const Range rw = range_of(workspace, (int64_t)need);
+        for (const Range& r :
+             {range_of(a.x, (nt * a.x_stride + a.H * a.dv) * es), range_of(a.dt, (nt * a.dt_stride + a.H) * es),
+              range_of(a.b, (nt * a.b_stride + a.G * a.dk) * es), range_of(a.c, (nt * a.c_stride + a.G * a.dk) * es),
+              range_of(a.A, a.H * 4), range_of(a.D, a.D ? a.H * 4 : 0), range_of(a.dt_bias, a.dt_bias ? a.H * 4 : 0),
+              range_of(a.initial_state, a.initial_state ? ns : 0), range_of(a.final_state, a.final_state ? ns : 0),
+              range_of(a.y, tokens * a.H * a.dv * es), range_of(a.cu_seqlens, a.cu_seqlens ? (a.N + 1) * 8 : 0)})
+            if (overlap(rw, r)) return GDN2_ERR_ALIAS;
+    }
+    if (tokens == 0 && !a.final_state) return GDN2_OK;  // nothing to write
+    a.cus = device_cus();
+    if (a.cus <= 0) return GDN2_ERR_HIP;
+    return gdn2::launch_ssm_fwd(a, workspace) == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
 gdn2_status_t check_conv(const gdn2::ConvArgs& a, gdn2_dtype_t dtype, int64_t tokens, bool in_place) {
     if (!known(dtype)) return GDN2_ERR_UNSUPPORTED;
     if (a.N < 1 || a.T < 0 || tokens < 0 || a.C < 1 || a.C % 8) return GDN2_ERR_SHAPE;
@@ -114,10 +145,12 @@ bool norm_sizes_ok(int64_t rows, int64_t width) { return rows >= 0 && rows <= IN
 extern "C" {
 
 size_t gdn2_ssm_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdn2_dtype_t dtype) {
-    if (B < 1 || T < 1 || H < 1 || B > INT_MAX || T > INT_MAX || H > INT_MAX || B * H > INT_MAX / 64) return 0;
-    if (!gdn2::ssm_supported(dk, dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32)) return 0;
-    const int cus = device_cus();
-    return gdn2::ssm_workspace_bytes(B, T, H, dk, dv, cus > 0 ? cus : 256);
+    return ssm_workspace(false, B, T, H, dk, dv, dtype);
+}
+
+size_t gdn2_ssm_fwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t H, int64_t dk, int64_t dv,
+                                           gdn2_dtype_t dtype) {
+    return ssm_workspace(true, N, total_T, H, dk, dv, dtype);
 }
 
 gdn2_status_t gdn2_ssm_fwd(const void* x, const void* dt, const void* b, const void* c, const float* A, const float* D,
@@ -127,44 +160,22 @@ gdn2_status_t gdn2_ssm_fwd(const void* x, const void* dt, const void* b, const v
                            size_t workspace_bytes, void* stream) {
     int64_t tokens;
     if (B < 1 || T < 1 || !mul_ok(B, T, &tokens)) return GDN2_ERR_SHAPE;
-    gdn2::SsmArgs a{x, dt, b, c, A, D, dt_bias, initial_state, y, final_state, B, T, H, G, dk, dv, x_stride, dt_stride,
-                    b_stride, c_stride, dtype == GDN2_DTYPE_BF16, softplus != 0, nullptr, stream, 0};
-    const gdn2_status_t st = check_ssm(a, dtype, tokens, false);
-    if (st != GDN2_OK) return st;
-    if (workspace || workspace_bytes) {
-        const size_t need = gdn2_ssm_fwd_workspace_bytes(B, T, H, dk, dv, dtype);
-        if (need == 0 || !workspace || workspace_bytes < need) return GDN2_ERR_WORKSPACE;
-        if (!aligned_to(workspace, 256)) return GDN2_ERR_MISALIGNED;
-        const int64_t es = elem(dtype), nt = tokens - 1, ns = B * H * dk * dv * 4;
-        const Range rw = range_of(workspace, (int64_t)need);
-        for (const Range& r :
-             {range_of(x, (nt * x_stride + H * dv) * es), range_of(dt, (nt * dt_stride + H) * es),
-              range_of(b, (nt * b_stride + G * dk) * es), range_of(c, (nt * c_stride + G * dk) * es),
-              range_of(A, H * 4), range_of(D, D ? H * 4 : 0), range_of(dt_bias, dt_bias ? H * 4 : 0),
-              range_of(initial_state, initial_state ? ns : 0), range_of(final_state, final_state ? ns : 0),
-              range_of(y, tokens * H * dv * es)})
-            if (overlap(rw, r)) return GDN2_ERR_ALIAS;
-    }
-    a.cus = device_cus();
-    if (a.cus <= 0) return GDN2_ERR_HIP;
-    return gdn2::launch_ssm_fwd(a, workspace) == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+    const gdn2::SsmArgs a{x, dt, b, c, A, D, dt_bias, initial_state, y, final_state, B, T, H, G, dk, dv, x_stride,
+                          dt_stride, b_stride, c_stride, dtype == GDN2_DTYPE_BF16, softplus != 0, nullptr, stream, 0};
+    return ssm_fwd(a, dtype, tokens, workspace, workspace_bytes);
 }
 
 gdn2_status_t gdn2_ssm_fwd_varlen(const void* x, const void* dt, const void* b, const void* c, const float* A,
                                   const float* D, const float* dt_bias, const float* initial_state, void* y,
                                   float* final_state, const int64_t* cu_seqlens, int64_t N, int64_t total_T, int64_t H,
                                   int64_t G, int64_t dk, int64_t dv, int64_t x_stride, int64_t dt_stride,
-                                  int64_t b_stride, int64_t c_stride, gdn2_dtype_t dtype, int softplus, void* stream) {
+                                  int64_t b_stride, int64_t c_stride, gdn2_dtype_t dtype, int softplus, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
     if (!cu_seqlens) return GDN2_ERR_NULL;
     if (!aligned_to(cu_seqlens, 8)) return GDN2_ERR_MISALIGNED;
-    gdn2::SsmArgs a{x, dt, b, c, A, D, dt_bias, initial_state, y, final_state, N, total_T, H, G, dk, dv, x_stride,
-                    dt_stride, b_stride, c_stride, dtype == GDN2_DTYPE_BF16, softplus != 0, cu_seqlens, stream, 0};
-    const gdn2_status_t st = check_ssm(a, dtype, total_T, false);
-    if (st != GDN2_OK) return st;
-    if (total_T == 0 && !final_state) return GDN2_OK;  // nothing to write
-    a.cus = device_cus();
-    if (a.cus <= 0) return GDN2_ERR_HIP;
-    return gdn2::launch_ssm_fwd(a, nullptr) == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+    const gdn2::SsmArgs a{x, dt, b, c, A, D, dt_bias, initial_state, y, final_state, N, total_T, H, G, dk, dv, x_stride,
+                          dt_stride, b_stride, c_stride, dtype == GDN2_DTYPE_BF16, softplus != 0, cu_seqlens, stream, 0};
+    return ssm_fwd(a, dtype, total_T, workspace, workspace_bytes);
 }
 
 gdn2_status_t gdn2_ssm_step(const void* x, const void* dt, const void* b, const void* c, const float* A, const float* D,

@@ -230,11 +230,26 @@ struct Params {
     int softplus;
     // the grid: slots (a sequence, or a segment of one) by parts of their heads
     int slots, parts, per;
-    // segments of a sequence, chunks of each, and with more than one segment the state that every
-    // segment starts from [N, H, segs, dk, dv] and its whole decay's logarithm [N, H, segs]
+    // segments of a sequence (of one length; 1: whole) and chunks of each; by an index that a
+    // segment of a cut sequence has, the state that it starts from [.., H, dk, dv] and the
+    // logarithm of its whole decay [.., H]
     int segs, seg_chunks;
     float* starts;
     double* logs;
+    // packed sequences that are cut: what split_kernel found
+    const struct Split* split;
+};
+
+// Packed sequences cut into segments of seg_chunks chunks: the pieces in the order in which they
+// are walked, longest first; those of them whose end state the next segment needs; and the cut
+// sequences.  The arrays follow one another behind this header.
+struct Piece {
+    int n, seg, index, count;  // sequence, segment, index of its state (-1: uncut); a cut sequence's segments
+};
+struct Split {
+    int pieces, ends, cuts, pad;
+    int64_t ends_at, cuts_at;  // places among the Piece records behind the header
+    __device__ const Piece* list(int64_t at) const { return reinterpret_cast<const Piece*>(this + 1) + at; }
 };
 
 // Workgroups go to the eight XCDs in turn, and each XCD has an L2 of its own.  A unit, the heads
@@ -295,16 +310,30 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     if (!unit_of(a, &slot, &hb)) return;
     const int h0 = hb * HP, hw = w * 16 * PT / DV;  // the first head, this wave's among them
     const int c0 = w * 16 * PT;                     // its first column of the workgroup's
-    const int steps = ENDS ? a.segs - 1 : a.segs;  // slots of a sequence
     static_assert(sizeof(sB) >= (kMaxSort + 1) * sizeof(int), "scratch of longest_first");
-    const int n = a.cu ? __builtin_amdgcn_readfirstlane(longest_first(a.cu, a.N, slot, (int)a.T, reinterpret_cast<int*>(sB)))
-                       : slot / steps;
-    const int seg = a.cu ? 0 : slot % steps;
+    int n, seg = 0, index = -1;  // index: of this segment's state, where its sequence is cut
+    if (a.split) {
+        if (slot >= (ENDS ? a.split->ends : a.split->pieces)) return;
+        const Piece piece = a.split->list(ENDS ? a.split->ends_at : 0)[slot];
+        if (piece.n < 0) return;
+        n = piece.n;
+        seg = piece.seg;
+        index = piece.index;
+    } else if (a.cu) {
+        n = __builtin_amdgcn_readfirstlane(longest_first(a.cu, a.N, slot, (int)a.T, reinterpret_cast<int*>(sB)));
+    } else {
+        const int steps = ENDS ? a.segs - 1 : a.segs;  // slots of a sequence
+        n = slot / steps;
+        seg = slot % steps;
+        if (a.segs > 1) index = n * a.segs + seg;
+    }
     int64_t lo = n * a.T, hi = lo + a.T;
     if (a.cu) {
         lo = min(max(a.cu[n], (int64_t)0), a.T);
         hi = min(max(a.cu[n + 1], lo), a.T);
-    } else if (a.segs > 1) {
+    }
+    const int64_t end = hi;  // of the sequence
+    if (index >= 0) {
         lo += (int64_t)seg * a.seg_chunks * Q;
         hi = min(hi, lo + (int64_t)a.seg_chunks * Q);
     }
@@ -322,7 +351,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     const int64_t state = (int64_t)n * a.H + h0 + hw;
     const int at0 = g4 * DV + c0 % DV + l16;
     const float* from = a.s0 ? a.s0 + state * (DK * DV) : nullptr;
-    if (a.segs > 1) from = ENDS ? nullptr : a.starts + (state * a.segs + seg) * (DK * DV);
+    if (index >= 0) from = ENDS ? nullptr : a.starts + ((int64_t)index * a.H + h0 + hw) * (DK * DV);
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
@@ -596,8 +625,8 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         if (ch + 1 < nc) store();
     }
     float* to = nullptr;
-    if (ENDS) to = a.starts + (state * a.segs + seg + 1) * (DK * DV);
-    else if (a.sT && (a.cu || seg == a.segs - 1)) to = a.sT + state * (DK * DV);
+    if (ENDS) to = a.starts + ((int64_t)(index + 1) * a.H + h0 + hw) * (DK * DV);
+    else if (a.sT && hi == end) to = a.sT + state * (DK * DV);
     if (to) {
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt)
@@ -612,31 +641,124 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         for (int hp = 0; hp < HP; ++hp)
             if (lane == 0) sLogs[hp][w] = logs[hp];
         __syncthreads();
-        if (tid < HP) a.logs[((int64_t)n * a.H + h0 + tid) * a.segs + seg] = (sLogs[tid][0] + sLogs[tid][1]) + (sLogs[tid][2] + sLogs[tid][3]);
+        if (tid < HP) a.logs[(int64_t)index * a.H + h0 + tid] = (sLogs[tid][0] + sLogs[tid][1]) + (sLogs[tid][2] + sLogs[tid][3]);
     }
 }
 
-// starts[0] = the initial state, starts[s + 1] = exp(logs[s]) starts[s] + the segment's own end,
-// which is in starts[s + 1].  The forward pass reads every segment's start from here, so it may
-// write the final state over the initial one.
+// For a cut sequence's segments: starts[0] = the initial state, starts[s + 1] = exp(logs[s])
+// starts[s] + the segment's own end, which is in starts[s + 1].  The forward pass reads every
+// segment's start from here, so it may write the final state over the initial one.
 __global__ __launch_bounds__(256) void join_kernel(Params a, int dk) {
     const int64_t quads = (int64_t)dk * a.dv / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t nh = id / quads;
-    if (nh >= (int64_t)a.N * a.H) return;
-    f32x4* st = reinterpret_cast<f32x4*>(a.starts) + nh * a.segs * quads + id % quads;
-    f32x4 s = a.s0 ? reinterpret_cast<const f32x4*>(a.s0)[id] : zero4();
-    st[0] = s;
-    for (int g = 0; g + 1 < a.segs; ++g) {
-        const f32x4 own = st[(int64_t)(g + 1) * quads];
-        s = s * expf((float)a.logs[nh * a.segs + g]) + own;
-        st[(int64_t)(g + 1) * quads] = s;
+    const int64_t row = quads * a.H, j = id / row, r = id % row;  // r: place in a sequence's states
+    int n = (int)j, base = n * a.segs, segs = a.segs;
+    if (a.split) {
+        if (j >= a.split->cuts) return;
+        const Piece cut = a.split->list(a.split->cuts_at)[j];
+        n = cut.n;
+        base = cut.index;
+        segs = cut.count;
+    } else if (j >= a.N) {
+        return;
     }
+    f32x4* st = reinterpret_cast<f32x4*>(a.starts) + base * row + r;
+    const double* lg = a.logs + (int64_t)base * a.H + r / quads;
+    f32x4 s = a.s0 ? reinterpret_cast<const f32x4*>(a.s0)[n * row + r] : zero4();
+    st[0] = s;
+    constexpr int AT = 4;  // segments whose ends are loaded together
+    for (int g = 0; g + 1 < segs; g += AT) {
+        f32x4 own[AT];
+        double l[AT];
+#pragma unroll
+        for (int k = 0; k < AT; ++k) {
+            const int at = min(g + k, segs - 2);
+            own[k] = st[(int64_t)(at + 1) * row];
+            l[k] = lg[(int64_t)at * a.H];
+        }
+#pragma unroll
+        for (int k = 0; k < AT; ++k) {
+            if (g + k + 1 >= segs) break;
+            s = s * exp_of(l[k]) + own[k];
+            st[(int64_t)(g + k + 1) * row] = s;
+        }
+    }
+}
+
+// The pieces of packed sequences, sorted by their chunks through a histogram; one workgroup.  The
+// lists hold max_ends ends of segments, more than sequences side by side in the token axis can have;
+// where offsets overlap, sequences past them are left whole.  index_of [N] holds a cut sequence's
+// first state, -1 for the others.
+constexpr int kBins = 2048;  // more than a segment's chunks
+__global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__ cu, int N, int64_t total, int seg_chunks,
+                                                     Split* split, int max_ends, int64_t ends_at, int64_t cuts_at,
+                                                     int* index_of) {
+    __shared__ int at[kBins];  // first pieces of a size: a count, then the place of the next one
+    __shared__ int sums[1024];
+    __shared__ int ends, cuts, states;
+    const int tid = threadIdx.x;
+    Piece* list = reinterpret_cast<Piece*>(split + 1);
+    at[tid] = at[tid + 1024] = 0;
+    if (tid == 0) ends = cuts = states = 0;
+    __syncthreads();
+    auto chunks = [&](int n) {
+        const int64_t lo = min(max(cu[n], (int64_t)0), total), hi = min(max(cu[n + 1], lo), total);
+        return (int)((hi - lo + Q - 1) / Q);
+    };
+    auto bin = [](int c) { return min(c, kBins - 1); };
+    // a sequence: `full` whole segments and a piece of the rest, or one piece
+    for (int n = tid; n < N; n += 1024) {
+        const int c = chunks(n), full = c / seg_chunks, rest = c - full * seg_chunks, segs = full + (rest ? 1 : 0);
+        int index = -1;
+        if (segs > 1) {
+            const int e = atomicAdd(&ends, segs - 1);
+            if (e + segs - 1 <= max_ends) {
+                index = atomicAdd(&states, segs);
+                for (int k = 0; k + 1 < segs; ++k) list[ends_at + e + k] = Piece{n, k, index + k, segs};
+                list[cuts_at + atomicAdd(&cuts, 1)] = Piece{n, 0, index, segs};
+                atomicAdd(&at[seg_chunks], full);
+                if (rest) atomicAdd(&at[rest], 1);
+            } else {  // given back as ends of nothing
+                for (int k = 0; k + 1 < segs; ++k)
+                    if (e + k < max_ends) list[ends_at + e + k] = Piece{-1, 0, 0, 0};
+            }
+        }
+        if (index < 0) atomicAdd(&at[bin(c)], 1);
+        index_of[n] = index;
+    }
+    __syncthreads();
+    // sizes from the largest down: thread t has the bin kBins - 1 - 2t and the one below
+    const int hi = kBins - 1 - 2 * tid, a = at[hi], b = at[hi - 1];
+    sums[tid] = a + b;
+    __syncthreads();
+    for (int d = 1; d < 1024; d <<= 1) {
+        const int v = tid >= d ? sums[tid - d] : 0;
+        __syncthreads();
+        sums[tid] += v;
+        __syncthreads();
+    }
+    const int before = sums[tid] - a - b;
+    at[hi] = before;
+    at[hi - 1] = before + a;
+    const int pieces = sums[1023];
+    __syncthreads();
+    for (int n = tid; n < N; n += 1024) {
+        const int c = chunks(n), index = index_of[n];
+        if (index < 0) {
+            list[atomicAdd(&at[bin(c)], 1)] = Piece{n, 0, -1, 1};
+            continue;
+        }
+        const int full = c / seg_chunks, rest = c - full * seg_chunks, segs = full + (rest ? 1 : 0);
+        const int p = atomicAdd(&at[seg_chunks], full);
+        for (int k = 0; k < full; ++k) list[p + k] = Piece{n, k, index + k, segs};
+        if (rest) list[atomicAdd(&at[rest], 1)] = Piece{n, full, index + full, segs};
+    }
+    if (tid == 0) *split = Split{pieces, min(ends, max_ends), cuts, 0, ends_at, cuts_at};
 }
 
 Params params(const SsmArgs& a) {
     return Params{a.x, a.dt, a.b, a.c, a.A, a.D, a.dt_bias, a.initial_state, a.y, a.final_state, a.cu_seqlens, a.T,
                   (int)a.N, (int)a.H, (int)a.G, (int)a.dv, (int)a.x_stride, (int)a.dt_stride, (int)a.b_stride,
-                  (int)a.c_stride, a.softplus ? 1 : 0, 0, 0, 0, 1, 0, nullptr, nullptr};
+                  (int)a.c_stride, a.softplus ? 1 : 0, 0, 0, 0, 1, 0, nullptr, nullptr, nullptr};
 }
 
 // Parts of a slot's `blocks` workgroups: the fewest that leave the eight XCDs with about as many units each (at
@@ -656,57 +778,120 @@ void set_grid(Params* p, int slots, int blocks) {
 }
 unsigned grid_of(const Params& p) { return (unsigned)(((int64_t)p.slots * p.parts + 7) / 8 * 8 * p.per); }
 
-// Segments of a sequence.  A chain is 128 columns of a sequence's heads; a compute unit runs two
-// workgroups at once.  Chains that do not fill the GPU are cut so that their pieces do, of at least 8 chunks
-// each: a piece but the last is walked twice, once for the state alone.
-int segments(int64_t N, int64_t T, int64_t H, int64_t dv, int64_t cus) {
-    const int64_t chains = (N * H * dv + 127) / 128, nc = (T + Q - 1) / Q;
-    int64_t g = 2 * cus / chains;
-    if (g > nc / 8) g = nc / 8;
-    if (g < 2) return 1;
-    const int64_t len = (nc + g - 1) / g;
-    return (int)((nc + len - 1) / len);
+// How a call is cut, and its workspace.
+struct Plan {
+    int segs, seg_chunks;                 // as Params; packed: segs 0, cut by split_kernel
+    int64_t indexes, pieces, ends, cuts;  // at most: states of segments; packed: pieces and lists
+    int64_t starts, logs, split, index_of, total;  // byte offsets of the workspace, its size (0: none)
+};
+
+// Sequences of one length.  A chunk's time is the unit.  A compute unit runs two workgroups (of 128
+// state columns) at once, each then 1.36 times as long as one alone; the pass for the segments' ends
+// takes half a chunk's time a chunk; its launch, the join's and the states' way through HBM are the
+// rest.  Fitted to 128 sequence-heads of 64 chunks (whole 64, in 2 / 3 / 4 / 8 segments 52 / 48 / 42 /
+// 47, of 4.4 us) and 16 of 512 (in 8 / 16 / 32 segments 97 / 53 / 43).
+Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
+    Plan p{};
+    const int64_t nc = (T + Q - 1) / Q, heads = N * H;
+    // workgroups of a segment: pairs of heads of 64 columns only where there are enough of them
+    const int64_t chains = dv == 128 || heads <= cus ? heads : (heads + 1) / 2;
+    auto rounds = [&](int64_t w) { return w <= cus ? 1.0 : 1.36 * (double)((w + 2 * cus - 1) / (2 * cus)); };
+    double best = rounds(chains) * (double)nc;
+    p.segs = 1;
+    for (int64_t g = 2; g <= nc && g <= 128 && chains * g <= 8 * cus; ++g) {
+        const int64_t len = (nc + g - 1) / g;
+        if ((nc + len - 1) / len != g) continue;
+        const double cost = rounds(chains * g) * (double)len + 0.5 * rounds(chains * (g - 1)) * (double)len + 3.0 +
+                            0.009 * (double)(chains * g);
+        if (cost < best) {
+            best = cost;
+            p.segs = (int)g;
+        }
+    }
+    p.seg_chunks = (int)((nc + p.segs - 1) / p.segs);
+    if (p.segs > 1) {
+        p.indexes = N * p.segs;
+        p.logs = p.indexes * H * dk * dv * 4;
+        p.total = p.logs + (p.indexes * H * 8 + 255) / 256 * 256;
+    }
+    return p;
 }
 
-struct Layout {
-    int64_t starts, logs, total;  // byte offsets
-};
-Layout layout(int64_t N, int64_t H, int64_t dk, int64_t dv, int64_t segs) {
-    Layout l;
-    l.starts = 0;
-    l.logs = N * H * segs * dk * dv * 4;
-    l.total = l.logs + (N * H * segs * 8 + 255) / 256 * 256;
-    return l;
+// Packed sequences, whose lengths the host does not know: segments of as many chunks as a workgroup
+// slot of the GPU has of all, or half as many where there are sequences enough to fill the slots (then
+// only the longest are cut, and the launch does not wait for their chains alone).
+Plan plan_packed(int64_t N, int64_t total, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
+    Plan p{};
+    p.segs = 1;
+    const int64_t nc = total / Q + N, wide = H * dv < 128 ? 1 : H * dv / 128, slots = N * wide < cus ? 2 * cus : 4 * cus;
+    int64_t len = (nc * wide + slots - 1) / slots;
+    if (len < 4) len = 4;
+    if (len > kBins - 1) len = kBins - 1;
+    if (total <= len * Q) return p;  // no sequence can be longer than a segment
+    p.segs = 0;
+    p.seg_chunks = (int)len;
+    // a cut sequence of k segments has more than (k - 1) len chunks' tokens
+    p.ends = total / (len * Q);
+    p.cuts = p.ends;
+    p.pieces = p.ends + N;
+    p.indexes = 2 * p.ends;
+    p.logs = p.indexes * H * dk * dv * 4;
+    p.split = p.logs + (p.indexes * H * 8 + 255) / 256 * 256;
+    p.index_of = p.split + (int64_t)sizeof(Split) + (p.pieces + p.ends + p.cuts) * (int64_t)sizeof(Piece);
+    p.total = (p.index_of + N * 4 + 255) / 256 * 256;
+    return p;
 }
 
 template <typename T, int DK, int DV, int HP>
-hipError_t launch_chunks(const SsmArgs& a, void* workspace) {
+hipError_t launch_chunks(const SsmArgs& a, const Plan& plan, void* workspace) {
     Params p = params(a);
-    p.segs = workspace ? segments(a.N, a.T, a.H, a.dv, a.cus) : 1;
-    p.seg_chunks = (int)(((a.T + Q - 1) / Q + p.segs - 1) / p.segs);
-    if (p.segs > 1) {
-        const Layout l = layout(a.N, a.H, a.dk, a.dv, p.segs);
-        p.starts = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.starts);
-        p.logs = reinterpret_cast<double*>(static_cast<char*>(workspace) + l.logs);
-        set_grid(&p, (int)a.N * (p.segs - 1), (int)a.H / HP);
-        hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, true>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
-        const int64_t quads = a.N * a.H * a.dk * a.dv / 4;
-        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, (hipStream_t)a.stream, p, DK);
+    const hipStream_t stream = (hipStream_t)a.stream;
+    const int blocks = (int)a.H / HP;
+    char* ws = static_cast<char*>(workspace);
+    int64_t ends = 0, cuts = 0, slots = a.N;
+    if (plan.total) {
+        p.segs = plan.segs;
+        p.seg_chunks = plan.seg_chunks;
+        p.starts = reinterpret_cast<float*>(ws + plan.starts);
+        p.logs = reinterpret_cast<double*>(ws + plan.logs);
+        if (a.cu_seqlens) {
+            Split* split = reinterpret_cast<Split*>(ws + plan.split);
+            p.split = split;
+            hipLaunchKernelGGL(split_kernel, dim3(1), dim3(1024), 0, stream, a.cu_seqlens, (int)a.N, a.T, plan.seg_chunks,
+                               split, (int)plan.ends, plan.pieces, plan.pieces + plan.ends,
+                               reinterpret_cast<int*>(ws + plan.index_of));
+            ends = plan.ends;
+            cuts = plan.cuts;
+            slots = plan.pieces;
+        } else {
+            ends = a.N * (plan.segs - 1);
+            cuts = a.N;
+            slots = a.N * plan.segs;
+        }
+        set_grid(&p, (int)ends, blocks);
+        hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, true>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);
+        const int64_t quads = cuts * a.H * DK * DV / 4;
+        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, p, DK);
     }
-    set_grid(&p, (int)a.N * p.segs, (int)a.H / HP);
-    hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, false>), dim3(grid_of(p)), dim3(64 * NW), 0, (hipStream_t)a.stream, p);
+    set_grid(&p, (int)slots, blocks);
+    hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, false>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);
     return hipGetLastError();
 }
 
 template <typename T, int DK>
-hipError_t launch_dk(const SsmArgs& a, void* ws) {
-    if (a.dv == 128) return launch_chunks<T, DK, 128, 1>(a, ws);
-    // two heads a workgroup where a group has an even number of them
-    return a.H / a.G % 2 == 0 ? launch_chunks<T, DK, 64, 2>(a, ws) : launch_chunks<T, DK, 64, 1>(a, ws);
+hipError_t launch_dk(const SsmArgs& a, const Plan& plan, void* ws) {
+    if (a.dv == 128) return launch_chunks<T, DK, 128, 1>(a, plan, ws);
+    // Two heads a workgroup where a group has an even number of them and pairs still fill the GPU:
+    // c . b and the staging of b and c are shared, but few workgroups take longer.
+    const int64_t pairs = (plan.pieces ? plan.pieces : a.N * (plan.total ? plan.segs : 1)) * a.H / 2;
+    return a.H / a.G % 2 == 0 && pairs >= a.cus ? launch_chunks<T, DK, 64, 2>(a, plan, ws)
+                                                 : launch_chunks<T, DK, 64, 1>(a, plan, ws);
 }
 template <typename T>
 hipError_t launch_fwd(const SsmArgs& a, void* ws) {
-    return a.dk == 128 ? launch_dk<T, 128>(a, ws) : launch_dk<T, 64>(a, ws);
+    Plan plan{};
+    if (ws) plan = a.cu_seqlens ? plan_packed(a.N, a.T, a.H, a.dk, a.dv, a.cus) : plan_fixed(a.N, a.T, a.H, a.dk, a.dv, a.cus);
+    return a.dk == 128 ? launch_dk<T, 128>(a, plan, ws) : launch_dk<T, 64>(a, plan, ws);
 }
 
 // ---- single tokens --------------------------------------------------------------------------
@@ -778,9 +963,8 @@ hipError_t launch_step(const SsmArgs& a) {
 
 }  // namespace ssm
 
-size_t ssm_workspace_bytes(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
-    const int segs = ssm::segments(N, T, H, dv, cus);
-    return segs > 1 ? (size_t)ssm::layout(N, H, dk, dv, segs).total : 0;
+size_t ssm_workspace_bytes(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
+    return (size_t)(packed ? ssm::plan_packed(N, T, H, dk, dv, cus) : ssm::plan_fixed(N, T, H, dk, dv, cus)).total;
 }
 
 hipError_t launch_ssm_fwd(const SsmArgs& a, void* workspace) {

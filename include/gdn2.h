@@ -413,7 +413,9 @@ size_t gdn2_ssm_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk,
  * tensors as above with [total_T, ...] for [B, T, ...] and states [N, H, dk, dv];
  * cu_seqlens as for gdn2_chunk_fwd_varlen (int64 [N + 1] in device memory, each
  * range clamped into [0, total_T]; tokens of no sequence are left as they were
- * in y; an empty sequence hands its initial state on).
+ * in y; an empty sequence hands its initial state on).  The workspace works as
+ * for gdn2_ssm_fwd: without one every sequence is walked whole, with one of
+ * gdn2_ssm_fwd_varlen_workspace_bytes bytes the long ones are cut.
  */
 gdn2_status_t gdn2_ssm_fwd_varlen(const void* x, const void* dt, const void* b, const void* c,
                                   const float* A, const float* D, const float* dt_bias,
@@ -421,7 +423,13 @@ gdn2_status_t gdn2_ssm_fwd_varlen(const void* x, const void* dt, const void* b, 
                                   const int64_t* cu_seqlens, int64_t N, int64_t total_T, int64_t H,
                                   int64_t G, int64_t dk, int64_t dv, int64_t x_stride,
                                   int64_t dt_stride, int64_t b_stride, int64_t c_stride,
-                                  gdn2_dtype_t dtype, int softplus, void* stream);
+                                  gdn2_dtype_t dtype, int softplus, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* The workspace with which gdn2_ssm_fwd_varlen is fastest for these sizes on the
+ * current device (0 where no sequence of total_T tokens would be cut). */
+size_t gdn2_ssm_fwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t H, int64_t dk,
+                                           int64_t dv, gdn2_dtype_t dtype);
 
 /* gdn2_ssm_step -- one token for each of N sequences: x [N, H, dv], dt [N, H],
  * b, c [N, G, dk], y [N, H, dv]; state [N, H, dk, dv] is updated in place. */

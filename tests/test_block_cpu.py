@@ -24,10 +24,10 @@ def ssm(lib, f, B=1, T=64, H=2, G=1, dk=64, dv=64, xs=None, ts=None, bs=None, cs
                             G * dk if bs is None else bs, G * dk if cs is None else cs, dtype, 1, ws, wb, None)
 
 
-def packed(lib, f, N=2, total=64, H=2, G=1, dk=64, dv=64, dtype=BF16, **over):
+def packed(lib, f, N=2, total=64, H=2, G=1, dk=64, dv=64, dtype=BF16, ws=None, wb=0, **over):
     a = {n: f.p(i) for i, n in enumerate("x dt b c A D bias s0 y sT cu".split())}
     a.update(over)
-    return lib.gdn2_ssm_fwd_varlen(*a.values(), N, total, H, G, dk, dv, H * dv, H, G * dk, G * dk, dtype, 1, None)
+    return lib.gdn2_ssm_fwd_varlen(*a.values(), N, total, H, G, dk, dv, H * dv, H, G * dk, G * dk, dtype, 1, ws, wb, None)
 
 
 def step(lib, f, N=3, H=2, G=1, dk=64, dv=64, dtype=BF16, **over):
@@ -61,6 +61,21 @@ def test_scan_workspace_refusals(lib):
     assert lib.gdn2_ssm_fwd_workspace_bytes(1, 64, 2, 64, 64, BF16) == 0  # one chunk: nothing to cut
     assert ssm(lib, f, ws=f.p(10), wb=1 << 20) == ERR_WORKSPACE
     assert ssm(lib, f, wb=1) == ERR_WORKSPACE
+    # packed: a workspace where total_T is more than a segment
+    assert lib.gdn2_ssm_fwd_varlen_workspace_bytes(2, 64, 2, 64, 64, BF16) == 0
+    assert packed(lib, f, ws=f.p(11), wb=1 << 20) == ERR_WORKSPACE
+    need = lib.gdn2_ssm_fwd_varlen_workspace_bytes(2, 4096, 2, 64, 64, BF16)
+    assert need > 0 and need == gdn2.ssm_fwd_varlen_workspace_bytes(2, 4096, 2, 64, 64)
+    a256 = lambda slot: f.p(slot, -f.p(slot).value % 256)
+    assert packed(lib, f, total=4096, ws=a256(11), wb=need - 1) == ERR_WORKSPACE
+    assert packed(lib, f, total=4096, ws=None, wb=need) == ERR_WORKSPACE
+    assert packed(lib, f, total=4096, ws=ctypes.c_void_p(a256(11).value + 16), wb=need) == ERR_MISALIGNED
+    for slot in (0, 1, 2, 3, 7, 8, 9):
+        assert packed(lib, f, total=4096, ws=a256(slot), wb=need) == ERR_ALIAS, slot
+    need = lib.gdn2_ssm_fwd_workspace_bytes(1, 8192, 2, 64, 64, BF16)
+    assert need > 0
+    assert ssm(lib, f, T=8192, ws=a256(8), wb=need) == ERR_ALIAS
+    assert ssm(lib, f, T=8192, ws=a256(10), wb=need - 1) == ERR_WORKSPACE
 
 
 def test_packed_and_step_refusals(lib):

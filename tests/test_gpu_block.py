@@ -180,6 +180,51 @@ def test_packed_scan_matches_oracle(dtype, dk, dv):
         check_scan(one, y[None, lo:lo + n], s[i:i + 1], oracle_scan(one), (n + 63) // 64)
 
 
+@pytest.mark.parametrize("dtype,H,G,dk,dv,in_place", [(BF16, 2, 1, 128, 128, True), (BF16, 4, 2, 64, 64, False),
+                                                      (F32, 1, 1, 64, 64, True)])
+def test_packed_scan_cut_into_segments(dtype, H, G, dk, dv, in_place):
+    """Sequences around one and several segments, an empty one among them; the same call without a
+    workspace walks them whole and agrees within both bars."""
+    lengths = [0, 256, 257, 1, 1500, 700, 512, 0, 3]
+    k, cu = packed_case(dtype, lengths, H, G, dk, dv, 17, lead=1, behind=2)
+    assert gdn2.ssm_fwd_varlen_workspace_bytes(len(lengths), sum(lengths) + 3, H, dk, dv, dtype) > 0
+    d = dev(k)
+    state = d["s0"].clone()
+    y, s = gdn2.ssm_fwd_varlen(d["x"], d["dt"], d["B"], d["C"], d["A"], cu.cuda(), d["D"], d["dt_bias"], state,
+                               final_state=state if in_place else None)
+    again, s2 = gdn2.ssm_fwd_varlen(d["x"], d["dt"], d["B"], d["C"], d["A"], cu.cuda(), d["D"], d["dt_bias"], d["s0"])
+    inside = slice(1, int(cu[-1]))
+    assert torch.equal(y[inside], again[inside]) and torch.equal(s, s2)
+    for i, n in enumerate(lengths):
+        if n == 0:
+            assert torch.equal(s[i].cpu(), k["s0"][i])
+            continue
+        lo = int(cu[i])
+        one = {m: (v[None, lo:lo + n] if m in ("x", "dt", "B", "C") else v) for m, v in k.items()}
+        one["s0"] = k["s0"][i:i + 1]
+        check_scan(one, y[None, lo:lo + n], s[i:i + 1], oracle_scan(one), (n + 63) // 64)
+
+
+@pytest.mark.parametrize("N", [600, 2500])
+def test_packed_scan_of_many_sequences(N):
+    """More sequences than the order by length is kept for, and more than a workgroup's threads; a few
+    long ones are cut."""
+    g = torch.Generator("cpu").manual_seed(N)
+    lengths = torch.randint(0, 9, (N,), generator=g).tolist()
+    lengths[7], lengths[N - 1] = 1100, 400
+    k, cu = packed_case(BF16, lengths, 1, 1, 64, 64, 18)
+    d = dev(k)
+    y, s = gdn2.ssm_fwd_varlen(d["x"], d["dt"], d["B"], d["C"], d["A"], cu.cuda(), d["D"], d["dt_bias"], d["s0"])
+    for i in [0, 7, 8, 511, 512, N - 2, N - 1]:
+        lo, n = int(cu[i]), lengths[i]
+        if n == 0:
+            assert torch.equal(s[i].cpu(), k["s0"][i])
+            continue
+        one = {m: (v[None, lo:lo + n] if m in ("x", "dt", "B", "C") else v) for m, v in k.items()}
+        one["s0"] = k["s0"][i:i + 1]
+        check_scan(one, y[None, lo:lo + n], s[i:i + 1], oracle_scan(one), (n + 63) // 64)
+
+
 def test_packed_scan_of_equal_lengths_is_the_scan():
     k = scan_case(BF16, (3, 130), 2, 1, 128, 128, 8, 3)
     d = dev(k)
