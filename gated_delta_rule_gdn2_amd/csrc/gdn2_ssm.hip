@@ -352,12 +352,16 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     const int at0 = g4 * DV + c0 % DV + l16;
     const float* from = a.s0 ? a.s0 + state * (DK * DV) : nullptr;
     if (index >= 0) from = ENDS ? nullptr : a.starts + ((int64_t)index * a.H + h0 + hw) * (DK * DV);
+    // through a resource, the rows as scalar offsets: with an address a row the registers spilled
+    const auto qs = cb::buffer_over(from, DK * DV * 4);
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[pt][nt][r] = from ? from[at0 + pt * 16 + (nt * 16 + r) * DV] : 0.f;
+            for (int r = 0; r < 4; ++r)
+                S[pt][nt][r] = from ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                          qs, (at0 + pt * 16) * 4, (nt * 16 + r) * DV * 4, 0)) : 0.f;
     // halves of M's operands that no tile writes: tiles above the diagonal
     if (!ENDS && w < HP) {
 #pragma unroll
@@ -628,12 +632,15 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     if (ENDS) to = a.starts + ((int64_t)(index + 1) * a.H + h0 + hw) * (DK * DV);
     else if (a.sT && hi == end) to = a.sT + state * (DK * DV);
     if (to) {
+        const auto qt = cb::buffer_over(to, DK * DV * 4);
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) to[at0 + pt * 16 + (nt * 16 + r) * DV] = S[pt][nt][r];
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (float)S[pt][nt][r]), qt,
+                                                          (at0 + pt * 16) * 4, (nt * 16 + r) * DV * 4, 0);
     }
     if constexpr (ENDS) {
         __shared__ double sLogs[HP][NW];
