@@ -19,7 +19,7 @@ namespace ssm {
 
 constexpr int Q = 64;  // tokens of a chunk
 
-constexpr int AHEAD = 8;  // chunks whose decays are in LDS, formed four at a time
+constexpr int AHEAD = 4;  // chunks whose decays are formed together
 
 typedef uint32_t U4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -624,8 +624,8 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
             }
             cb::sched_fence();
         }
-        if (ch % 4 == 3) decays(ch + 1);
         cb::lds_barrier();  // the chunk has been read
+        if (ch % 4 == 3) decays(ch + 1);
         if (ch + 1 < nc) store();
     }
     float* to = nullptr;
