@@ -127,9 +127,11 @@ def _opt(name, t, shape, dtype, dev):
     return None if t is None else _in(name, t, shape, dtype, dev)
 
 
-def _out(name, t, shape, dtype, dev):
+def _out(name, t, shape, dtype, dev, like=None):
+    """The caller's output after its checks, or a new one; `like`: a contiguous tensor of its shape
+    and dtype, if there is one (a quicker way to a new one)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like)
     _check(name, t, shape, dtype, dev)
     return t
 
@@ -183,7 +185,7 @@ def ssm_fwd(x, dt, B, C, A, D=None, dt_bias=None, initial_state=None, *, y=None,
     s0 = _opt("initial_state", initial_state, sshape, _F32, dev)
     y = _out("y", y, lead + (H, dv), x.dtype, dev)
     if final_state is not None or output_final_state:
-        final_state = _out("final_state", final_state, sshape, _F32, dev)
+        final_state = _out("final_state", final_state, sshape, _F32, dev, initial_state)
     need = _load().gdn2_ssm_fwd_workspace_bytes(n, T, H, dk, dv, code)
     ws, ws_bytes, keep = _workspace(workspace, need, 256, dev) if need else (None, 0, None)
     _launch("gdn2_ssm_fwd", dev, *ptrs, s0, y.data_ptr(), _ptr(final_state), n, T, H, G, dk, dv, *strides, code,
@@ -214,7 +216,7 @@ def ssm_fwd_varlen(x, dt, B, C, A, cu_seqlens, D=None, dt_bias=None, initial_sta
     s0 = _opt("initial_state", initial_state, sshape, _F32, dev)
     y = _out("y", y, lead + (H, dv), x.dtype, dev)
     if final_state is not None or output_final_state:
-        final_state = _out("final_state", final_state, sshape, _F32, dev)
+        final_state = _out("final_state", final_state, sshape, _F32, dev, initial_state)
     need = _load().gdn2_ssm_fwd_varlen_workspace_bytes(n, lead[0], H, dk, dv, code)
     ws, ws_bytes, keep = _workspace(workspace, need, 256, dev) if need else (None, 0, None)
     _launch("gdn2_ssm_fwd_varlen", dev, *ptrs, s0, y.data_ptr(), _ptr(final_state), cu_seqlens.data_ptr(), n, lead[0],
@@ -266,9 +268,9 @@ def _conv_args(x, taps, bias, initial_state, y, final_state, output_final_state,
     pt = _in("taps", taps, (ch, 4), _F32, dev)
     b = _opt("bias", bias, (ch,), _F32, dev)
     s0 = _opt("initial_state", initial_state, (n, 3, ch), x.dtype, dev)
-    y = _out("y", y, x.shape, x.dtype, dev)
+    y = _out("y", y, tuple(x.shape), x.dtype, dev)
     if final_state is not None or output_final_state:
-        final_state = _out("final_state", final_state, (n, 3, ch), x.dtype, dev)
+        final_state = _out("final_state", final_state, (n, 3, ch), x.dtype, dev, initial_state)
     return y, (x.data_ptr(), pt, b, s0, y.data_ptr(), _ptr(final_state)), final_state
 
 
@@ -298,11 +300,11 @@ def layer_norm(x, gamma, beta=None, eps=1e-5, *, y=None, stats=True):
     px = _in("x", x, shape, x.dtype, dev)
     pg = _in("gamma", gamma, (width,), _F32, dev)
     b = _opt("beta", beta, (width,), _F32, dev)
-    y = _out("y", y, shape, x.dtype, dev)
+    y = _out("y", y, shape, x.dtype, dev, x)
     mean = rstd = None
     if stats:
-        mean = torch.empty(shape[:-1], dtype=_F32, device=dev)
-        rstd = torch.empty(shape[:-1], dtype=_F32, device=dev)
+        mean = torch.empty(tuple(shape[:-1]), dtype=_F32, device=dev)
+        rstd = torch.empty_like(mean)
     _launch("gdn2_layer_norm", dev, px, pg, b, y.data_ptr(), _ptr(mean), _ptr(rstd),
             x.numel() // max(width, 1), width, float(eps), code)
     return y, mean, rstd
@@ -324,13 +326,14 @@ def layer_norm_bwd(dy, x, gamma, mean, rstd, *, grads=None, want_beta_grad=True,
     shape = x.shape
     width = shape[-1]
     rows = x.numel() // max(width, 1)
+    lead = tuple(shape[:-1])
     ptrs = (_in("dy", dy, shape, x.dtype, dev), _in("x", x, shape, x.dtype, dev),
-            _in("gamma", gamma, (width,), _F32, dev), _in("mean", mean, shape[:-1], _F32, dev),
-            _in("rstd", rstd, shape[:-1], _F32, dev))
+            _in("gamma", gamma, (width,), _F32, dev), _in("mean", mean, lead, _F32, dev),
+            _in("rstd", rstd, lead, _F32, dev))
     out = {} if grads is None else dict(grads)
-    out["dx"] = _out("dx", out.get("dx"), shape, x.dtype, dev)
-    out["dgamma"] = _out("dgamma", out.get("dgamma"), (width,), _F32, dev)
-    out["dbeta"] = _out("dbeta", out.get("dbeta"), (width,), _F32, dev) if want_beta_grad else None
+    out["dx"] = _out("dx", out.get("dx"), shape, x.dtype, dev, x)
+    out["dgamma"] = _out("dgamma", out.get("dgamma"), (width,), _F32, dev, gamma)
+    out["dbeta"] = _out("dbeta", out.get("dbeta"), (width,), _F32, dev, gamma) if want_beta_grad else None
     need = layer_norm_bwd_workspace_bytes(rows, width)
     ws, ws_bytes, keep = _workspace(workspace, need, 16, dev) if need else (None, 0, None)
     _launch("gdn2_layer_norm_bwd", dev, *ptrs, out["dx"].data_ptr(), out["dgamma"].data_ptr(), _ptr(out["dbeta"]), ws, ws_bytes, rows,

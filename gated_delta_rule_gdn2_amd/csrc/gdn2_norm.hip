@@ -153,7 +153,8 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(const T* __restric
                                                               const float* __restrict__ gamma,
                                                               const float* __restrict__ mean,
                                                               const float* __restrict__ rstd, T* __restrict__ dx,
-                                                              float* __restrict__ parts, int64_t rows, int width) {
+                                                              float* __restrict__ parts, float* __restrict__ dgamma,
+                                                              float* __restrict__ dbeta, int64_t rows, int width) {
     typedef Row<T, LANES, NV> R;
     constexpr int E = NV * R::V, RPB = kThreads<LANES> / LANES;
     __shared__ float scratch[2][LANES > 64 ? LANES / 64 : 1];
@@ -208,9 +209,11 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(const T* __restric
         }
     }
     if (sub == 0) {
-        float* p = parts + (int64_t)blockIdx.x * 2 * width;
-        store_row<float, LANES, NV, R::V>(p, lane, width, [&](int i) { return dg[i]; });
-        store_row<float, LANES, NV, R::V>(p + width, lane, width, [&](int i) { return db[i]; });
+        // one workgroup: its part is the whole
+        float* pg = gridDim.x == 1 ? dgamma : parts + (int64_t)blockIdx.x * 2 * width;
+        float* pb = gridDim.x == 1 ? dbeta : parts + ((int64_t)blockIdx.x * 2 + 1) * width;
+        store_row<float, LANES, NV, R::V>(pg, lane, width, [&](int i) { return dg[i]; });
+        if (pb) store_row<float, LANES, NV, R::V>(pb, lane, width, [&](int i) { return db[i]; });
     }
 }
 
@@ -258,8 +261,11 @@ int threads_of(int64_t width) { return lanes_of(width) <= 64 ? 256 : lanes_of(wi
 // them).  Twice as many lost up to a third (the last ones start late), half as many up to a half.
 template <int LANES> constexpr int64_t kFwdBlocks = (1 << 19) / kThreads<LANES>;
 int64_t parts_limit(int64_t width) { return threads_of(width) == 1024 ? 512 : 3 * (1 << 17) / threads_of(width); }
+// Few rows, up to 8 for each row that a workgroup takes at once, go to one workgroup: its time stays
+// below that of a second launch, and there are no parts to join.
 int parts_of(int64_t rows, int64_t width) {
     const int64_t rpb = threads_of(width) / lanes_of(width), b = (rows + rpb - 1) / rpb, most = parts_limit(width);
+    if (b <= 8) return rows > 0 ? 1 : 0;
     return (int)(b < most ? b : most);
 }
 
@@ -299,7 +305,8 @@ struct Bwd {
         if (np > 0)
             hipLaunchKernelGGL((bwd_kernel<T, LANES, NV>), dim3((unsigned)np), dim3(kThreads<LANES>), 0,
                                (hipStream_t)a.stream, (const T*)a.dy, (const T*)a.x, a.gamma, a.mean, a.rstd,
-                               (T*)a.dx, a.parts, a.rows, (int)a.width);
+                               (T*)a.dx, a.parts, a.dgamma, a.dbeta, a.rows, (int)a.width);
+        if (np == 1) return hipGetLastError();
         hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.width + kJoinCols - 1) / kJoinCols)),
                            dim3(kJoinCols * kJoinRows), 0, (hipStream_t)a.stream, a.parts, a.dgamma, a.dbeta,
                            (int)a.width, np);
@@ -313,7 +320,10 @@ hipError_t launch_layer_norm(const NormArgs& a) {
     return a.dtype_bf16 ? norm::by_width<bf16>(a.width, norm::Fwd<bf16>{a}) : norm::by_width<float>(a.width, norm::Fwd<float>{a});
 }
 
-size_t norm_bwd_workspace_bytes(int64_t rows, int64_t width) { return (size_t)norm::parts_of(rows, width) * 2 * width * 4; }
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t width) {
+    const int64_t np = norm::parts_of(rows, width);
+    return np > 1 ? (size_t)(np * 2 * width * 4) : 0;
+}
 
 hipError_t launch_layer_norm_bwd(const NormBwdArgs& a) {
     return a.dtype_bf16 ? norm::by_width<bf16>(a.width, norm::Bwd<bf16>{a}) : norm::by_width<float>(a.width, norm::Bwd<float>{a});

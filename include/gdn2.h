@@ -496,7 +496,7 @@ gdn2_status_t gdn2_layer_norm(const void* x, const float* gamma, const float* be
                               gdn2_dtype_t dtype, void* stream);
 
 /* Bytes of device workspace that gdn2_layer_norm_bwd needs: partial sums of
- * dgamma and dbeta.  0 if the sizes are out of range. */
+ * dgamma and dbeta.  0 for few rows, and if the sizes are out of range. */
 size_t gdn2_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
 
 /*

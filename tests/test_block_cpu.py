@@ -127,7 +127,7 @@ def norm(lib, f, rows=4, width=100, eps=1e-5, dtype=F32, **over):
     return lib.gdn2_layer_norm(*a.values(), rows, width, eps, dtype, None)
 
 
-def norm_bwd(lib, f, rows=4, width=100, dtype=F32, wb=None, **over):
+def norm_bwd(lib, f, rows=400, width=100, dtype=F32, wb=None, **over):
     a = {n: f.p(i) for i, n in enumerate("dy x gamma mean rstd dx dgamma dbeta ws".split())}
     a.update(over)
     if wb is None:
@@ -151,11 +151,12 @@ def test_norm_refusals(lib):
         assert norm_bwd(lib, f, **{n: None}) == ERR_NULL, n
     assert norm_bwd(lib, f, rows=-1) == ERR_SHAPE and norm_bwd(lib, f, width=20000) == ERR_SHAPE
     assert norm_bwd(lib, f, ws=None) == ERR_WORKSPACE
-    assert norm_bwd(lib, f, wb=lib.gdn2_layer_norm_bwd_workspace_bytes(4, 100) - 1) == ERR_WORKSPACE
+    assert norm_bwd(lib, f, wb=lib.gdn2_layer_norm_bwd_workspace_bytes(400, 100) - 1) == ERR_WORKSPACE
     assert norm_bwd(lib, f, ws=f.p(8, 8)) == ERR_MISALIGNED and norm_bwd(lib, f, dx=f.p(5, 4)) == ERR_MISALIGNED
     for kw in (dict(dx=f.p(0)), dict(dgamma=f.p(2)), dict(dbeta=f.p(6)), dict(ws=f.p(1)), dict(ws=f.p(7))):
         assert norm_bwd(lib, f, **kw) == ERR_ALIAS, kw
     assert lib.gdn2_layer_norm_bwd_workspace_bytes(4, 20000) == 0
+    assert lib.gdn2_layer_norm_bwd_workspace_bytes(4, 100) == 0 < lib.gdn2_layer_norm_bwd_workspace_bytes(400, 100)
 
 
 def test_binding_refuses_cpu_tensors_and_odd_layouts():
