@@ -70,6 +70,15 @@ def _launch(name, dev, *args):
         raise Gdn2Error(name, st, lib.gdn2_status_string(st).decode())
 
 
+def _bytes(name, dev, *args):
+    """A workspace's size as the library states it for dev."""
+    f = getattr(_load(), name)
+    if dev.index == torch.cuda.current_device():
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
 def _on_gpu(fn, t, ndim, layout):
     """The dtype code and device of a call's first tensor, after its checks."""
     if not isinstance(t, torch.Tensor):
@@ -186,7 +195,7 @@ def ssm_fwd(x, dt, B, C, A, D=None, dt_bias=None, initial_state=None, *, y=None,
     y = _out("y", y, lead + (H, dv), x.dtype, dev)
     if final_state is not None or output_final_state:
         final_state = _out("final_state", final_state, sshape, _F32, dev, initial_state)
-    need = _load().gdn2_ssm_fwd_workspace_bytes(n, T, H, dk, dv, code)
+    need = _bytes("gdn2_ssm_fwd_workspace_bytes", dev, n, T, H, dk, dv, code)
     ws, ws_bytes, keep = _workspace(workspace, need, 256, dev) if need else (None, 0, None)
     _launch("gdn2_ssm_fwd", dev, *ptrs, s0, y.data_ptr(), _ptr(final_state), n, T, H, G, dk, dv, *strides, code,
             int(softplus), ws, ws_bytes)
@@ -217,7 +226,7 @@ def ssm_fwd_varlen(x, dt, B, C, A, cu_seqlens, D=None, dt_bias=None, initial_sta
     y = _out("y", y, lead + (H, dv), x.dtype, dev)
     if final_state is not None or output_final_state:
         final_state = _out("final_state", final_state, sshape, _F32, dev, initial_state)
-    need = _load().gdn2_ssm_fwd_varlen_workspace_bytes(n, lead[0], H, dk, dv, code)
+    need = _bytes("gdn2_ssm_fwd_varlen_workspace_bytes", dev, n, lead[0], H, dk, dv, code)
     ws, ws_bytes, keep = _workspace(workspace, need, 256, dev) if need else (None, 0, None)
     _launch("gdn2_ssm_fwd_varlen", dev, *ptrs, s0, y.data_ptr(), _ptr(final_state), cu_seqlens.data_ptr(), n, lead[0],
             H, G, dk, dv, *strides, code, int(softplus), ws, ws_bytes)
