@@ -195,6 +195,15 @@ template <> struct Planes<float> {
     }
 };
 
+// A token's logarithm of decay, no less than 160 factors of two: an fp32 decay is 0 from 150 on, so
+// no result differs, and a token that clears the state leaves the sums of those behind it exact
+// enough.  (At -1e7 the difference of two such sums in fp32 was off by e; -inf gave NaN.)  NaN stays.
+__device__ __forceinline__ double log_decay(float dt, float A) {
+    constexpr double least = -110.9035488896;  // 160 ln 2
+    const double v = (double)dt * (double)A;
+    return v < least ? least : v;
+}
+
 // Sums of logarithms of decays are formed in 64 bits.  What a pair of tokens needs, the decay
 // between them, is a difference of two: in bf16 of their fp32 roundings (to base 2, for the
 // hardware's exponential; an error of |cum| 2^-23, far below a bf16 rounding of M where M counts),
@@ -391,8 +400,8 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     };
     // Decays of the four chunks from ch on, a chunk a wave, a token a lane: a token behind the end
     // decays and adds nothing.  One wave at a time forming the next chunk's kept the others waiting
-    // for 2000 of 14000 cycles.  The raw time steps are loaded a chunk
-    // before they are needed, and carried as they are: widening them would wait for them.
+    // for 2000 of 14000 cycles.  The raw time steps are loaded a chunk before they are needed, and
+    // carried as they are: widening them would wait for them.
     T rdt[HP];
     auto load_dt = [&](int ch) {
         const int t = min((ch + w) * Q + lane, len - 1);
@@ -406,7 +415,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         for (int hp = 0; hp < HP; ++hp) {
             const float bias = a.dt_bias ? a.dt_bias[h0 + hp] : 0.f;
             const float dt = (ch + w) * Q + lane < len ? time_step(to_f32(rdt[hp]) + bias, a.softplus) : 0.f;
-            const double cum = scan((double)dt * (double)a.A[h0 + hp]), all = last_lane(cum);
+            const double cum = scan(log_decay(dt, a.A[h0 + hp])), all = last_lane(cum);
             if constexpr (ENDS) logs[hp] += all;
             sCum[k][hp][lane] = Pair<T>::cum(cum);
             sDt[k][hp][lane] = dt;

@@ -374,7 +374,7 @@ gdn2_status_t gdn2_mixer_out(const void* o, const void* z, const float* gamma, v
  *   b, c          [B, T, G, dk]  dtype    shared by the H / G heads of a group:
  *                                         head h takes group h / (H / G);
  *                                         b_stride, c_stride
- *   A             [H]            float32  expected < 0
+ *   A             [H]            float32  expected < 0; a decay below 2^-149 is 0
  *   D, dt_bias    [H]            float32  each NULL for zeros
  *   initial_state [B, H, dk, dv] float32  or NULL for zeros
  *   y             [B, T, H, dv]  dtype    out

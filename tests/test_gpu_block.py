@@ -128,6 +128,20 @@ def test_scan_without_the_optional_inputs(dtype):
     assert none is None and torch.equal(y, y2)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scan_after_tokens_that_clear_the_state(dtype):
+    """A few tokens whose decay is e^-1e7 (documents joined in one sequence are set apart so): what
+    follows them in the same chunk keeps its own decays, of a tenth a token."""
+    k = scan_case(dtype, (1, 150), 2, 1, 64, 64, 23, 1)
+    k.update(A=torch.full((2,), -1e5), dt_bias=None, dt=torch.full((1, 150, 2), 1e-6).to(dtype))
+    for t in (5, 6, 70, 149):
+        k["dt"][:, t] = 100.0
+    k["x"] = (k["x"] * 1e3).to(dtype)
+    d = dev(k)
+    y, s = gdn2.ssm_fwd(d["x"], d["dt"], d["B"], d["C"], d["A"], d["D"], None, d["s0"], softplus=False)
+    check_scan(k, y, s, oracle_scan(k, softplus=False), 3)
+
+
 @pytest.mark.parametrize("dtype,T", [(BF16, 130), (F32, 130), (BF16, 2200)])
 def test_scan_reads_parts_of_one_tensor(dtype, T):
     """x, B, C and dt as parts of wider tensors give the bits of their copies; caller outputs are
