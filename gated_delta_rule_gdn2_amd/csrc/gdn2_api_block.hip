@@ -20,6 +20,11 @@ using gdn2::range_of;
 
 constexpr int64_t kMaxStride = int64_t(1) << 22;  // elements between tokens: 64 of them stay below 2^30 bytes
 constexpr int64_t kMaxWidth = 16384;
+// Tokens of a sequence, or of all packed ones: indexes a few chunks behind the last stay 32-bit.
+constexpr int64_t kMaxTokens = INT_MAX - 1024;
+// Sequence-heads: workgroups of 256 threads, of which a launch may have less than 2^32; packed
+// sequences that are cut have more pieces than there are sequences.
+constexpr int64_t kMaxHeads = INT_MAX / 256;
 
 int64_t elem(gdn2_dtype_t t) { return t == GDN2_DTYPE_BF16 ? 2 : 4; }
 bool known(gdn2_dtype_t t) { return t == GDN2_DTYPE_BF16 || t == GDN2_DTYPE_F32; }
@@ -50,7 +55,7 @@ gdn2_status_t check_ssm(const gdn2::SsmArgs& a, gdn2_dtype_t dtype, int64_t toke
     if (tokens > 0 && (!a.x || !a.dt || !a.b || !a.c || !a.y)) return GDN2_ERR_NULL;
     if (!a.A || (in_place && !a.final_state)) return GDN2_ERR_NULL;
     if (!gdn2::ssm_supported(a.dk, a.dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32)) return GDN2_ERR_UNSUPPORTED;
-    if (a.N > INT_MAX || a.T > INT_MAX || a.H >= kMaxStride || a.H % a.G) return GDN2_ERR_SHAPE;
+    if (a.N > INT_MAX || a.T > kMaxTokens || a.H >= kMaxStride || a.H % a.G) return GDN2_ERR_SHAPE;
     if (a.H * a.dv >= kMaxStride || a.G * a.dk >= kMaxStride) return GDN2_ERR_SHAPE;
     if (a.x_stride < a.H * a.dv || a.dt_stride < a.H || a.b_stride < a.G * a.dk || a.c_stride < a.G * a.dk)
         return GDN2_ERR_SHAPE;
@@ -58,7 +63,7 @@ gdn2_status_t check_ssm(const gdn2::SsmArgs& a, gdn2_dtype_t dtype, int64_t toke
         return GDN2_ERR_SHAPE;
     const int64_t es = elem(dtype);
     int64_t nh, ns, nx, nt, nb, nc, ny;
-    if (!mul_ok(a.N, a.H, &nh) || nh > INT_MAX / 64 || !mul_ok(nh, a.dk * a.dv * 4, &ns)) return GDN2_ERR_SHAPE;
+    if (!mul_ok(a.N, a.H, &nh) || nh > kMaxHeads || !mul_ok(nh, a.dk * a.dv * 4, &ns)) return GDN2_ERR_SHAPE;
     if (!span(tokens, a.x_stride, a.H * a.dv, es, &nx) || !span(tokens, a.dt_stride, a.H, es, &nt) ||
         !span(tokens, a.b_stride, a.G * a.dk, es, &nb) || !span(tokens, a.c_stride, a.G * a.dk, es, &nc) ||
         !span(tokens, a.H * a.dv, a.H * a.dv, es, &ny))
@@ -82,7 +87,7 @@ gdn2_status_t check_ssm(const gdn2::SsmArgs& a, gdn2_dtype_t dtype, int64_t toke
 }
 
 size_t ssm_workspace(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, gdn2_dtype_t dtype) {
-    if (N < 1 || T < 1 || H < 1 || N > INT_MAX || T > INT_MAX || H > INT_MAX || N * H > INT_MAX / 64) return 0;
+    if (N < 1 || T < 1 || H < 1 || N > INT_MAX || T > kMaxTokens || H > INT_MAX || N * H > kMaxHeads) return 0;
     if (!gdn2::ssm_supported(dk, dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32)) return 0;
     const int cus = device_cus();
     return gdn2::ssm_workspace_bytes(packed, N, T, H, dk, dv, cus > 0 ? cus : 256);
@@ -123,8 +128,12 @@ gdn2_status_t check_conv(const gdn2::ConvArgs& a, gdn2_dtype_t dtype, int64_t to
     int64_t nx, ny, ns;
     if (!span(tokens, a.x_stride, a.C, es, &nx) || !span(tokens, a.C, a.C, es, &ny) || !mul_ok(a.N, a.C * 3 * es, &ns))
         return GDN2_ERR_SHAPE;
-    // workgroups along x of the grid (256 threads of eight channels each)
-    if (ny / es / 8 > (int64_t)INT_MAX * 128 || ns / es / 8 > (int64_t)INT_MAX * 128) return GDN2_ERR_SHAPE;
+    // Threads of a launch, of four channels each: of a run of 16 tokens (shorter runs are for small
+    // calls), and of a sequence's state.
+    int64_t runs;
+    if (!mul_ok(a.cu_seqlens ? 1 : a.N, (a.T + 15) / 16, &runs) || runs > INT64_MAX / 4 - a.N ||
+        !mul_ok(runs + a.N, a.C / 4, &runs) || runs > UINT32_MAX - 1024)
+        return GDN2_ERR_SHAPE;
     if (a.x && !aligned_to(a.x, es)) return GDN2_ERR_MISALIGNED;
     for (const void* p : {(const void*)a.taps, (const void*)a.bias, a.initial_state, (const void*)a.y, (const void*)a.final_state})
         if (p && !aligned_to(p, 16)) return GDN2_ERR_MISALIGNED;

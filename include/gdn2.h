@@ -384,8 +384,8 @@ gdn2_status_t gdn2_mixer_out(const void* o, const void* z, const float* gamma, v
  * Token t of sequence n starts at element (n T + t) * stride of its tensor.
  * Built for dk and dv of 64 or 128 each.  The strides are at least a token's
  * elements and below 2^22; x_stride, b_stride and c_stride are whole 16-byte
- * units; H is a multiple of G, and H * dv is below 2^22 (GDN2_ERR_SHAPE, or
- * GDN2_ERR_MISALIGNED).  dt needs the alignment of its elements only.  Pairs of
+ * units; H is a multiple of G, and H * dv is below 2^22; B * H is below 2^23, T
+ * at most 2^31 - 1025 (GDN2_ERR_SHAPE, or GDN2_ERR_MISALIGNED).  dt needs the alignment of its elements only.  Pairs of
  * tokens are formed in chunks of 64, with zeros for the pairs of a later token:
  * a NaN or an infinity in x, b, c or dt makes the outputs of its whole chunk
  * undefined, those of earlier tokens among them.
@@ -457,8 +457,10 @@ gdn2_status_t gdn2_ssm_step(const void* x, const void* dt, const void* b, const 
  *                                     to skip; may be the same pointer as
  *                                     initial_state
  *
- * C is a multiple of 8 below 2^22, x_stride at least C and below 2^22.  x and
- * its tokens need the alignment of their elements only.
+ * C is a multiple of 8 below 2^22, x_stride at least C and below 2^22, and
+ * B (ceil(T / 16) + 1) C / 4 is below 2^32 - 1024 (packed: (ceil(total_T / 16) + N)
+ * C / 4), else GDN2_ERR_SHAPE.  x and its tokens need the alignment of their
+ * elements only.
  */
 gdn2_status_t gdn2_short_conv(const void* x, const float* taps, const float* bias,
                               const void* initial_state, void* y, void* final_state, int64_t B,

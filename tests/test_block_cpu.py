@@ -78,6 +78,28 @@ def test_scan_workspace_refusals(lib):
     assert ssm(lib, f, T=8192, ws=a256(10), wb=need - 1) == ERR_WORKSPACE
 
 
+def test_scan_limits(lib):
+    """Sizes whose indexes or whose launch would pass 32 bits (a tensor expanded along its tokens
+    takes no memory for them)."""
+    f = Fake()
+    top = (1 << 31) - 1024
+    assert ssm(lib, f, T=top) == ERR_SHAPE and packed(lib, f, total=top) == ERR_SHAPE
+    assert lib.gdn2_ssm_fwd_workspace_bytes(1, top, 2, 64, 64, BF16) == 0
+    assert lib.gdn2_ssm_fwd_varlen_workspace_bytes(2, top, 2, 64, 64, BF16) == 0
+    assert ssm(lib, f, B=1 << 23, T=1, H=1) == ERR_SHAPE and packed(lib, f, N=1 << 22, H=2) == ERR_SHAPE
+    assert step(lib, f, N=1 << 22, H=2) == ERR_SHAPE
+
+
+def test_conv_limits(lib):
+    """Launches of 2^32 threads: 2^21 sequences of one token of 8192 channels (34 GB) are one."""
+    f = Fake()
+    assert conv(lib, f, B=1 << 21, T=1, C=8192) == ERR_SHAPE
+    assert conv(lib, f, B=1, T=1 << 24, C=16384) == ERR_SHAPE
+    a = [f.p(i) for i in range(7)]
+    assert lib.gdn2_short_conv_varlen(*a, 1 << 21, 64, 8192, 8192, BF16, None) == ERR_SHAPE
+    assert lib.gdn2_short_conv_step(a[0], a[1], a[2], a[5], a[4], 1 << 21, 8192, 8192, BF16, None) == ERR_SHAPE
+
+
 def test_packed_and_step_refusals(lib):
     f = Fake()
     assert packed(lib, f, cu=None) == ERR_NULL
