@@ -15,7 +15,7 @@ namespace gdn2 {
 namespace conv {
 
 // Channels a thread.  In bf16 eight, with 16-byte accesses, held 134 registers and took 82 us where
-// four take 67 (8 x 4096 tokens of 2304 channels; 4.5 TB/s, near the rate of a large copy).
+// four take 66 (8 x 4096 tokens of 2304 channels; 4.6 TB/s, the rate of a large copy).
 constexpr int CH = 4;
 
 struct Params {

@@ -296,6 +296,13 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
 // at one tile took as long as the products.  The next chunk's inputs are loaded into registers
 // meanwhile, through buffer resources that end with the sequence: rows behind it read as zeros, and
 // their y is dropped.
+// Bound by issue.  A wave's chunk (dk = 128, 32 columns) is 152 matrix instructions of 16 cycles, 96
+// of them the state's three planes, and 715 vector ones, which hardly run beside the other wave's on
+// its SIMD.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 133 us of this pass (matrix 30% and
+// vector 35% of the cycles, LDS 25%), 67 of the pass for ENDS and 11 of the join under a profiler,
+// 180 in all without one (190 TFLOP/s; the inputs and outputs alone would take 61).  Eight waves a
+// workgroup spilled (269); 64 columns a workgroup repeat c . b and M (195); with 64 columns and four
+// more waves that only load and form M, one barrier a chunk, this pass took 171 and ENDS 55.
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
 constexpr int NW = 4;
