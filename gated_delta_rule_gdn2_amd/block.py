@@ -94,13 +94,11 @@ def _on_gpu(fn, t, ndim, layout):
 
 
 def _tokens(name, t, shape, inner, dtype, dev):
-    """Checks a token tensor whose last `inner` dimensions are a token's own elements; returns the
-    elements between tokens."""
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != dev:
+    """Checks a token tensor whose last `inner` (1 or 2) dimensions are a token's own elements; returns
+    the elements between tokens."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev):
         _check(name, t, shape, dtype, dev)  # says which
-    own = 1
-    for n in shape[len(shape) - inner:]:
-        own *= n
+    own = shape[-1] if inner == 1 else shape[-1] * shape[-2]
     if t.is_contiguous():
         return own
     strides = t.stride()
@@ -127,7 +125,7 @@ def _tokens(name, t, shape, inner, dtype, dev):
 
 def _in(name, t, shape, dtype, dev):
     """The address of a contiguous tensor, after its checks."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()):
         _check(name, t, shape, dtype, dev)  # says which
     return t.data_ptr()
 
@@ -137,10 +135,12 @@ def _opt(name, t, shape, dtype, dev):
 
 
 def _out(name, t, shape, dtype, dev, like=None):
-    """The caller's output after its checks, or a new one; `like`: a contiguous tensor of its shape
-    and dtype, if there is one (a quicker way to a new one)."""
+    """The caller's output after its checks, or a new one; `like`: a tensor of its shape and dtype, if
+    there is one (a quicker way to a new one)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like)
+        if like is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     _check(name, t, shape, dtype, dev)
     return t
 
@@ -171,10 +171,11 @@ def _ssm_args(lead, x, dt, B, C, A, D, dt_bias, dev):
         raise ValueError("B must be %s" % ("[B,T,G,dk]" if len(lead) == 2 else "[tokens,G,dk]"))
     G, dk = B.shape[-2:]
     t = x.dtype
-    xs = _tokens("x", x, lead + (H, dv), 2, t, dev)
+    group = lead + (G, dk)
+    xs = _tokens("x", x, x.shape, 2, t, dev)
     ds = _tokens("dt", dt, lead + (H,), 1, t, dev)
-    bs = _tokens("B", B, lead + (G, dk), 2, t, dev)
-    cs = _tokens("C", C, lead + (G, dk), 2, t, dev)
+    bs = _tokens("B", B, group, 2, t, dev)
+    cs = _tokens("C", C, group, 2, t, dev)
     ptrs = (x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(), _in("A", A, (H,), _F32, dev), _opt("D", D, (H,), _F32, dev),
             _opt("dt_bias", dt_bias, (H,), _F32, dev))
     return (H, G, dk, dv), (xs, ds, bs, cs), ptrs
@@ -192,7 +193,7 @@ def ssm_fwd(x, dt, B, C, A, D=None, dt_bias=None, initial_state=None, *, y=None,
     n, T = lead
     sshape = (n, H, dk, dv)
     s0 = _opt("initial_state", initial_state, sshape, _F32, dev)
-    y = _out("y", y, lead + (H, dv), x.dtype, dev)
+    y = _out("y", y, lead + (H, dv), x.dtype, dev, x)
     if final_state is not None or output_final_state:
         final_state = _out("final_state", final_state, sshape, _F32, dev, initial_state)
     need = _bytes("gdn2_ssm_fwd_workspace_bytes", dev, n, T, H, dk, dv, code)
@@ -223,7 +224,7 @@ def ssm_fwd_varlen(x, dt, B, C, A, cu_seqlens, D=None, dt_bias=None, initial_sta
     n = _offsets(cu_seqlens, dev)
     sshape = (n, H, dk, dv)
     s0 = _opt("initial_state", initial_state, sshape, _F32, dev)
-    y = _out("y", y, lead + (H, dv), x.dtype, dev)
+    y = _out("y", y, lead + (H, dv), x.dtype, dev, x)
     if final_state is not None or output_final_state:
         final_state = _out("final_state", final_state, sshape, _F32, dev, initial_state)
     need = _bytes("gdn2_ssm_fwd_varlen_workspace_bytes", dev, n, lead[0], H, dk, dv, code)
@@ -240,7 +241,7 @@ def ssm_step(x, dt, B, C, A, state, D=None, dt_bias=None, *, y=None, softplus=Tr
     lead = (x.shape[0],)
     (H, G, dk, dv), strides, ptrs = _ssm_args(lead, x, dt, B, C, A, D, dt_bias, dev)
     ps = _in("state", state, (lead[0], H, dk, dv), _F32, dev)
-    y = _out("y", y, lead + (H, dv), x.dtype, dev)
+    y = _out("y", y, lead + (H, dv), x.dtype, dev, x)
     _launch("gdn2_ssm_step", dev, *ptrs, ps, y.data_ptr(), lead[0], H, G, dk, dv, *strides, code,
             int(softplus))
     return y
@@ -253,7 +254,7 @@ def short_conv(x, taps, bias=None, initial_state=None, *, y=None, final_state=No
     ``initial_state`` itself)."""
     code, dev = _on_gpu("short_conv", x, 3, "[B,T,C]")
     n, T, ch = x.shape
-    xs = _tokens("x", x, (n, T, ch), 1, x.dtype, dev)
+    xs = _tokens("x", x, x.shape, 1, x.dtype, dev)
     y, ptrs, final_state = _conv_args(x, taps, bias, initial_state, y, final_state, output_final_state, n, dev)
     _launch("gdn2_short_conv", dev, *ptrs, n, T, ch, xs, code)
     return y, final_state
@@ -265,7 +266,7 @@ def short_conv_varlen(x, taps, cu_seqlens, bias=None, initial_state=None, *, y=N
     [N+1] on the device, the inputs kept [N,3,C]."""
     code, dev = _on_gpu("short_conv_varlen", x, 2, "[total_T,C]")
     total, ch = x.shape
-    xs = _tokens("x", x, (total, ch), 1, x.dtype, dev)
+    xs = _tokens("x", x, x.shape, 1, x.dtype, dev)
     n = _offsets(cu_seqlens, dev)
     y, ptrs, final_state = _conv_args(x, taps, bias, initial_state, y, final_state, output_final_state, n, dev)
     _launch("gdn2_short_conv_varlen", dev, *ptrs, cu_seqlens.data_ptr(), n, total, ch, xs, code)
@@ -277,7 +278,7 @@ def _conv_args(x, taps, bias, initial_state, y, final_state, output_final_state,
     pt = _in("taps", taps, (ch, 4), _F32, dev)
     b = _opt("bias", bias, (ch,), _F32, dev)
     s0 = _opt("initial_state", initial_state, (n, 3, ch), x.dtype, dev)
-    y = _out("y", y, tuple(x.shape), x.dtype, dev)
+    y = _out("y", y, tuple(x.shape), x.dtype, dev, x)
     if final_state is not None or output_final_state:
         final_state = _out("final_state", final_state, (n, 3, ch), x.dtype, dev, initial_state)
     return y, (x.data_ptr(), pt, b, s0, y.data_ptr(), _ptr(final_state)), final_state
@@ -288,11 +289,11 @@ def short_conv_step(x, taps, state, bias=None, *, y=None):
     in place.  Returns y."""
     code, dev = _on_gpu("short_conv_step", x, 2, "[N,C]")
     n, ch = x.shape
-    xs = _tokens("x", x, (n, ch), 1, x.dtype, dev)
+    xs = _tokens("x", x, x.shape, 1, x.dtype, dev)
     pt = _in("taps", taps, (ch, 4), _F32, dev)
     ps = _in("state", state, (n, 3, ch), x.dtype, dev)
     b = _opt("bias", bias, (ch,), _F32, dev)
-    y = _out("y", y, (n, ch), x.dtype, dev)
+    y = _out("y", y, (n, ch), x.dtype, dev, x)
     _launch("gdn2_short_conv_step", dev, x.data_ptr(), pt, b, ps, y.data_ptr(), n, ch, xs,
             code)
     return y
