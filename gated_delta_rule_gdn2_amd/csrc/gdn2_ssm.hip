@@ -242,7 +242,7 @@ struct Params {
     // segments of a sequence (of one length; 1: whole) and chunks of each; by an index that a
     // segment of a cut sequence has, the state that it starts from [.., H, dk, dv] and the
     // logarithm of its whole decay [.., H]
-    int segs, seg_chunks;
+    int segs, seg_chunks, few;  // few: up to so many segments, each forms its start itself
     float* starts;
     double* logs;
     // packed sequences that are cut: what split_kernel found
@@ -250,10 +250,10 @@ struct Params {
 };
 
 // Packed sequences cut into segments of seg_chunks chunks: the pieces in the order in which they
-// are walked, longest first; those of them whose end state the next segment needs; and the cut
-// sequences.  The arrays follow one another behind this header.
+// are walked, longest first; those of them whose end state the next segment needs; and the
+// sequences for join_kernel.  The arrays follow one another behind this header.
 struct Piece {
-    int n, seg, index, count;  // sequence, segment, index of its state (-1: uncut); a cut sequence's segments
+    int n, seg, index, count;  // sequence, segment, index of its state (-1: uncut); the sequence's segments
 };
 struct Split {
     int pieces, ends, cuts, pad;
@@ -306,6 +306,10 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
 constexpr int NW = 4;
+// A sequence of up to so many segments needs no join: each segment reads the ends before it and forms
+// its own start.  That is more to read with each segment (4 of 8 x 4096 tokens: 171 us without the
+// join, 176 with it; 6 of 2 x 333 tokens: 27 and 30; 32 of one of 32768: 214 and 182).
+constexpr int kFew = 6;
 template <typename T, int DK, int DV, int HP, bool ENDS>
 __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void chunk_kernel(Params a) {
     constexpr int CW = HP * DV, PT = CW / (16 * NW), NTH = 64 * NW, ES = (int)sizeof(T);
@@ -327,7 +331,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     const int h0 = hb * HP, hw = w * 16 * PT / DV;  // the first head, this wave's among them
     const int c0 = w * 16 * PT;                     // its first column of the workgroup's
     static_assert(sizeof(sB) >= (kMaxSort + 1) * sizeof(int), "scratch of longest_first");
-    int n, seg = 0, index = -1;  // index: of this segment's state, where its sequence is cut
+    int n, seg = 0, index = -1, count = 1;  // index: of this segment's state, where its sequence is cut
     if (a.split) {
         if (slot >= (ENDS ? a.split->ends : a.split->pieces)) return;
         const Piece piece = a.split->list(ENDS ? a.split->ends_at : 0)[slot];
@@ -335,6 +339,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         n = piece.n;
         seg = piece.seg;
         index = piece.index;
+        count = piece.count;
     } else if (a.cu) {
         n = __builtin_amdgcn_readfirstlane(longest_first(a.cu, a.N, slot, (int)a.T, reinterpret_cast<int*>(sB)));
     } else {
@@ -342,6 +347,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         n = slot / steps;
         seg = slot % steps;
         if (a.segs > 1) index = n * a.segs + seg;
+        count = a.segs;
     }
     int64_t lo = n * a.T, hi = lo + a.T;
     if (a.cu) {
@@ -367,7 +373,9 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     const int64_t state = (int64_t)n * a.H + h0 + hw;
     const int at0 = g4 * DV + c0 % DV + l16;
     const float* from = a.s0 ? a.s0 + state * (DK * DV) : nullptr;
-    if (index >= 0) from = ENDS ? nullptr : a.starts + ((int64_t)index * a.H + h0 + hw) * (DK * DV);
+    const bool own = index >= 0 && count <= a.few;  // the start is formed here
+    if (ENDS) from = nullptr;
+    else if (index >= 0 && !own) from = a.starts + ((int64_t)index * a.H + h0 + hw) * (DK * DV);
     // through a resource, the rows as scalar offsets: with an address a row the registers spilled
     const auto qs = cb::buffer_over(from, DK * DV * 4);
 #pragma unroll
@@ -378,6 +386,20 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
             for (int r = 0; r < 4; ++r)
                 S[pt][nt][r] = from ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
                                           qs, (at0 + pt * 16) * 4, (nt * 16 + r) * DV * 4, 0)) : 0.f;
+    if (!ENDS && own)
+        for (int e = index - seg; e < index; ++e) {
+            const float keep = exp_of(a.logs[(int64_t)e * a.H + h0 + hw]);
+            const auto qe = cb::buffer_over(a.starts + ((int64_t)(e + 1) * a.H + h0 + hw) * (DK * DV), DK * DV * 4);
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        S[pt][nt][r] = S[pt][nt][r] * keep +
+                                       __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                           qe, (at0 + pt * 16) * 4, (nt * 16 + r) * DV * 4, 0));
+        }
     // halves of M's operands that no tile writes: tiles above the diagonal
     if (!ENDS && w < HP) {
 #pragma unroll
@@ -668,41 +690,42 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     }
 }
 
-// For a cut sequence's segments: starts[0] = the initial state, starts[s + 1] = exp(logs[s])
-// starts[s] + the segment's own end, which is in starts[s + 1].  The forward pass reads every
-// segment's start from here, so it may write the final state over the initial one.
+// For the segments of a sequence cut into more than a.few: starts[0] = the initial state, starts[s + 1]
+// = exp(logs[s]) starts[s] + the segment's own end, which is in starts[s + 1].  The forward pass
+// reads every segment's start from here, so it may write the final state over the initial one (for
+// a call that does, a.few is 0).
 __global__ __launch_bounds__(256) void join_kernel(Params a, int dk) {
-    const int64_t quads = (int64_t)dk * a.dv / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = quads * a.H, j = id / row, r = id % row;  // r: place in a sequence's states
-    int n = (int)j, base = n * a.segs, segs = a.segs;
-    if (a.split) {
-        if (j >= a.split->cuts) return;
-        const Piece cut = a.split->list(a.split->cuts_at)[j];
-        n = cut.n;
-        base = cut.index;
-        segs = cut.count;
-    } else if (j >= a.N) {
-        return;
-    }
-    f32x4* st = reinterpret_cast<f32x4*>(a.starts) + base * row + r;
-    const double* lg = a.logs + (int64_t)base * a.H + r / quads;
-    f32x4 s = a.s0 ? reinterpret_cast<const f32x4*>(a.s0)[n * row + r] : zero4();
-    st[0] = s;
-    constexpr int AT = 4;  // segments whose ends are loaded together
-    for (int g = 0; g + 1 < segs; g += AT) {
-        f32x4 own[AT];
-        double l[AT];
-#pragma unroll
-        for (int k = 0; k < AT; ++k) {
-            const int at = min(g + k, segs - 2);
-            own[k] = st[(int64_t)(at + 1) * row];
-            l[k] = lg[(int64_t)at * a.H];
+    const int64_t quads = (int64_t)dk * a.dv / 4, row = quads * a.H;  // r: place in a sequence's states
+    const int64_t all = (a.split ? a.split->cuts : a.N) * row;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < all; id += (int64_t)gridDim.x * 256) {
+        const int64_t j = id / row, r = id % row;
+        int n = (int)j, base = n * a.segs, segs = a.segs;
+        if (a.split) {
+            const Piece cut = a.split->list(a.split->cuts_at)[j];
+            n = cut.n;
+            base = cut.index;
+            segs = cut.count;
         }
+        f32x4* st = reinterpret_cast<f32x4*>(a.starts) + base * row + r;
+        const double* lg = a.logs + (int64_t)base * a.H + r / quads;
+        f32x4 s = a.s0 ? reinterpret_cast<const f32x4*>(a.s0)[n * row + r] : zero4();
+        st[0] = s;
+        constexpr int AT = 4;  // segments whose ends are loaded together
+        for (int g = 0; g + 1 < segs; g += AT) {
+            f32x4 own[AT];
+            double l[AT];
 #pragma unroll
-        for (int k = 0; k < AT; ++k) {
-            if (g + k + 1 >= segs) break;
-            s = s * exp_of(l[k]) + own[k];
-            st[(int64_t)(g + k + 1) * row] = s;
+            for (int k = 0; k < AT; ++k) {
+                const int at = min(g + k, segs - 2);
+                own[k] = st[(int64_t)(at + 1) * row];
+                l[k] = lg[(int64_t)at * a.H];
+            }
+#pragma unroll
+            for (int k = 0; k < AT; ++k) {
+                if (g + k + 1 >= segs) break;
+                s = s * exp_of(l[k]) + own[k];
+                st[(int64_t)(g + k + 1) * row] = s;
+            }
         }
     }
 }
@@ -714,7 +737,7 @@ __global__ __launch_bounds__(256) void join_kernel(Params a, int dk) {
 constexpr int kBins = 2048;  // more than a segment's chunks
 __global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__ cu, int N, int64_t total, int seg_chunks,
                                                      Split* split, int max_ends, int64_t ends_at, int64_t cuts_at,
-                                                     int* index_of) {
+                                                     int* index_of, int few) {
     __shared__ int at[kBins];  // first pieces of a size: a count, then the place of the next one
     __shared__ int sums[1024];
     __shared__ int ends, cuts, states;
@@ -737,7 +760,7 @@ __global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__
             if (e + segs - 1 <= max_ends) {
                 index = atomicAdd(&states, segs);
                 for (int k = 0; k + 1 < segs; ++k) list[ends_at + e + k] = Piece{n, k, index + k, segs};
-                list[cuts_at + atomicAdd(&cuts, 1)] = Piece{n, 0, index, segs};
+                if (segs > few) list[cuts_at + atomicAdd(&cuts, 1)] = Piece{n, 0, index, segs};
                 atomicAdd(&at[seg_chunks], full);
                 if (rest) atomicAdd(&at[rest], 1);
             } else {  // given back as ends of nothing
@@ -781,7 +804,7 @@ __global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__
 Params params(const SsmArgs& a) {
     return Params{a.x, a.dt, a.b, a.c, a.A, a.D, a.dt_bias, a.initial_state, a.y, a.final_state, a.cu_seqlens, a.T,
                   (int)a.N, (int)a.H, (int)a.G, (int)a.dv, (int)a.x_stride, (int)a.dt_stride, (int)a.b_stride,
-                  (int)a.c_stride, a.softplus ? 1 : 0, 0, 0, 0, 1, 0, nullptr, nullptr, nullptr};
+                  (int)a.c_stride, a.softplus ? 1 : 0, 0, 0, 0, 1, 0, 0, nullptr, nullptr, nullptr};
 }
 
 // Parts of a slot's `blocks` workgroups: the fewest that leave the eight XCDs with about as many units each (at
@@ -877,12 +900,14 @@ hipError_t launch_chunks(const SsmArgs& a, const Plan& plan, void* workspace) {
         p.seg_chunks = plan.seg_chunks;
         p.starts = reinterpret_cast<float*>(ws + plan.starts);
         p.logs = reinterpret_cast<double*>(ws + plan.logs);
+        // not where a final state may replace the initial one that other segments still read
+        p.few = a.initial_state && a.initial_state == a.final_state ? 0 : kFew;
         if (a.cu_seqlens) {
             Split* split = reinterpret_cast<Split*>(ws + plan.split);
             p.split = split;
             hipLaunchKernelGGL(split_kernel, dim3(1), dim3(1024), 0, stream, a.cu_seqlens, (int)a.N, a.T, plan.seg_chunks,
                                split, (int)plan.ends, plan.pieces, plan.pieces + plan.ends,
-                               reinterpret_cast<int*>(ws + plan.index_of));
+                               reinterpret_cast<int*>(ws + plan.index_of), p.few);
             ends = plan.ends;
             cuts = plan.cuts;
             slots = plan.pieces;
@@ -893,8 +918,10 @@ hipError_t launch_chunks(const SsmArgs& a, const Plan& plan, void* workspace) {
         }
         set_grid(&p, (int)ends, blocks);
         hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, true>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);
-        const int64_t quads = cuts * a.H * DK * DV / 4;
-        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, p, DK);
+        // workgroups that fit the GPU at once: how many sequences there are to join the host does not know
+        const int64_t need = (cuts * a.H * DK * DV / 4 + 255) / 256, fit = a.cus * 8;
+        if ((a.cu_seqlens ? plan.ends + 1 : plan.segs) > p.few)
+            hipLaunchKernelGGL(join_kernel, dim3((unsigned)(need < fit ? need : fit)), dim3(256), 0, stream, p, DK);
     }
     set_grid(&p, (int)slots, blocks);
     hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, false>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);

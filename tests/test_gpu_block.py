@@ -219,6 +219,42 @@ def test_packed_scan_cut_into_segments(dtype, H, G, dk, dv, in_place):
         check_scan(one, y[None, lo:lo + n], s[i:i + 1], oracle_scan(one), (n + 63) // 64)
 
 
+@pytest.mark.parametrize("dtype,T", [(BF16, 1600), (F32, 333), (BF16, 3300)])
+def test_scan_forms_the_same_starts_in_place(dtype, T):
+    """Few segments form their starts themselves, unless the final state takes the initial one's
+    place (then, and for many segments, a pass of its own does)."""
+    k = scan_case(dtype, (2, T), 2, 1, 64, 64, 29, 2)
+    d = dev(k)
+    assert gdn2.ssm_fwd_workspace_bytes(2, T, 2, 64, 64, dtype) > 0
+    args = (d["x"], d["dt"], d["B"], d["C"], d["A"], d["D"], d["dt_bias"])
+    y, s = gdn2.ssm_fwd(*args, d["s0"])
+    check_scan(k, y, s, oracle_scan(k), (T + 63) // 64)
+    state = d["s0"].clone()
+    y2, s2 = gdn2.ssm_fwd(*args, state, final_state=state)
+    assert torch.equal(y, y2) and torch.equal(s, s2)
+    zero = torch.zeros_like(state)
+    y3, s3 = gdn2.ssm_fwd(*args, None)
+    y4, s4 = gdn2.ssm_fwd(*args, zero, final_state=zero)
+    assert torch.equal(y3, y4) and torch.equal(s3, s4)
+
+
+def test_packed_scan_with_few_and_many_segments():
+    lengths = [2300, 300, 1700, 0, 900, 5]
+    k, cu = packed_case(BF16, lengths, 2, 1, 64, 128, 31)
+    d = dev(k)
+    args = (d["x"], d["dt"], d["B"], d["C"], d["A"], cu.cuda(), d["D"], d["dt_bias"])
+    y, s = gdn2.ssm_fwd_varlen(*args, d["s0"])
+    state = d["s0"].clone()
+    y2, s2 = gdn2.ssm_fwd_varlen(*args, state, final_state=state)
+    assert torch.equal(y, y2) and torch.equal(s, s2)
+    for i, n in enumerate(lengths):
+        lo = int(cu[i])
+        one = {m: (v[None, lo:lo + n] if m in ("x", "dt", "B", "C") else v) for m, v in k.items()}
+        one["s0"] = k["s0"][i:i + 1]
+        if n:
+            check_scan(one, y[None, lo:lo + n], s[i:i + 1], oracle_scan(one), (n + 63) // 64)
+
+
 @pytest.mark.parametrize("N", [600, 2500])
 def test_packed_scan_of_many_sequences(N):
     """More sequences than the order by length is kept for, and more than a workgroup's threads; a few
