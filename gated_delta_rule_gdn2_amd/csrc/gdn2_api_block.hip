@@ -90,7 +90,7 @@ size_t ssm_workspace(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, i
     if (N < 1 || T < 1 || H < 1 || N > INT_MAX || T > kMaxTokens || H > INT_MAX || N * H > kMaxHeads) return 0;
     if (!gdn2::ssm_supported(dk, dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32)) return 0;
     const int cus = device_cus();
-    return gdn2::ssm_workspace_bytes(packed, N, T, H, dk, dv, cus > 0 ? cus : 256);
+    return gdn2::ssm_workspace_bytes(packed, N, T, H, dk, dv, dtype == GDN2_DTYPE_BF16, cus > 0 ? cus : 256);
 }
 
 // the scan of whole or packed prompts, with `tokens` rows in all

@@ -191,7 +191,8 @@ inline bool ssm_supported(int64_t dk, int64_t dv, bool bf16, bool f32) {
     return (bf16 || f32) && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
 }
 // bytes of the workspace with which sequences are walked in segments (0: whole); T as in SsmArgs
-size_t ssm_workspace_bytes(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t cus);
+size_t ssm_workspace_bytes(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf16_in,
+                           int64_t cus);
 hipError_t launch_ssm_fwd(const SsmArgs& a, void* workspace);
 hipError_t launch_ssm_step(const SsmArgs& a);
 hipError_t launch_short_conv(const ConvArgs& a);

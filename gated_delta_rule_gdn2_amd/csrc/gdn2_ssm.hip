@@ -298,11 +298,11 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
 // their y is dropped.
 // Bound by issue.  A wave's chunk (dk = 128, 32 columns) is 152 matrix instructions of 16 cycles, 96
 // of them the state's three planes, and 715 vector ones, which hardly run beside the other wave's on
-// its SIMD.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 133 us of this pass (matrix 30% and
-// vector 35% of the cycles, LDS 25%), 67 of the pass for ENDS and 11 of the join under a profiler,
-// 180 in all without one (190 TFLOP/s; the inputs and outputs alone would take 61).  Eight waves a
-// workgroup spilled (269); 64 columns a workgroup repeat c . b and M (195); with 64 columns and four
-// more waves that only load and form M, one barrier a chunk, this pass took 171 and ENDS 55.
+// its SIMD.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 132 us of this pass (matrix 30% and
+// vector 35% of the cycles, LDS 25%) and 63 of the pass for ENDS under a profiler, 171 in all
+// without one (1.7 TB/s; the inputs and outputs alone would take 61).  Eight waves a workgroup
+// spilled (269); 64 columns a workgroup repeat c . b and M (195); with 64 columns and four more
+// waves that only load and form M, one barrier a chunk, this pass took 171 and ENDS 55.
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
 constexpr int NW = 4;
@@ -833,10 +833,12 @@ struct Plan {
 
 // Sequences of one length.  A chunk's time is the unit.  A compute unit runs two workgroups (of 128
 // state columns) at once, each then 1.36 times as long as one alone; the pass for the segments' ends
-// takes half a chunk's time a chunk; its launch, the join's and the states' way through HBM are the
-// rest.  Fitted to 128 sequence-heads of 64 chunks (whole 64, in 2 / 3 / 4 / 8 segments 52 / 48 / 42 /
-// 47, of 4.4 us) and 16 of 512 (in 8 / 16 / 32 segments 97 / 53 / 43).
-Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
+// takes half a chunk's time a chunk; launches, the states' way through HBM and the join, which walks
+// the segments, are the rest.  Fitted to calls in us, the chosen one first: 128 sequence-heads of 64
+// chunks in 4 / 1 / 2 / 3 / 8 segments 170 / 242 / 192 / 180 / 193; 16 of 512 in 32 / 16 / 48 176 / 200 /
+// 192; 8 of 32 in 16 / 8 / 32 31 / 37 / 36; fp32, whose chunks take three times as long, 18 of 11 in
+// 11 / 6 44 / 57.
+Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf16_in, int64_t cus) {
     Plan p{};
     const int64_t nc = (T + Q - 1) / Q, heads = N * H;
     // workgroups of a segment: pairs of heads of 64 columns only where there are enough of them
@@ -847,8 +849,9 @@ Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t
     for (int64_t g = 2; g <= nc && g <= 128 && chains * g <= 8 * cus; ++g) {
         const int64_t len = (nc + g - 1) / g;
         if ((nc + len - 1) / len != g) continue;
-        const double cost = rounds(chains * g) * (double)len + 0.5 * rounds(chains * (g - 1)) * (double)len + 3.0 +
-                            0.009 * (double)(chains * g);
+        const double rest = (g > kFew ? 3.0 + 0.06 * (double)g : 2.0) + 0.009 * (double)(chains * g);
+        const double cost = rounds(chains * g) * (double)len + 0.5 * rounds(chains * (g - 1)) * (double)len +
+                            (bf16_in ? rest : 0.3 * rest);
         if (cost < best) {
             best = cost;
             p.segs = (int)g;
@@ -940,7 +943,7 @@ hipError_t launch_dk(const SsmArgs& a, const Plan& plan, void* ws) {
 template <typename T>
 hipError_t launch_fwd(const SsmArgs& a, void* ws) {
     Plan plan{};
-    if (ws) plan = a.cu_seqlens ? plan_packed(a.N, a.T, a.H, a.dk, a.dv, a.cus) : plan_fixed(a.N, a.T, a.H, a.dk, a.dv, a.cus);
+    if (ws) plan = a.cu_seqlens ? plan_packed(a.N, a.T, a.H, a.dk, a.dv, a.cus) : plan_fixed(a.N, a.T, a.H, a.dk, a.dv, a.dtype_bf16, a.cus);
     return a.dk == 128 ? launch_dk<T, 128>(a, plan, ws) : launch_dk<T, 64>(a, plan, ws);
 }
 
@@ -1013,8 +1016,10 @@ hipError_t launch_step(const SsmArgs& a) {
 
 }  // namespace ssm
 
-size_t ssm_workspace_bytes(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
-    return (size_t)(packed ? ssm::plan_packed(N, T, H, dk, dv, cus) : ssm::plan_fixed(N, T, H, dk, dv, cus)).total;
+size_t ssm_workspace_bytes(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf16_in,
+                           int64_t cus) {
+    return (size_t)(packed ? ssm::plan_packed(N, T, H, dk, dv, cus) : ssm::plan_fixed(N, T, H, dk, dv, bf16_in, cus))
+                        .total;
 }
 
 hipError_t launch_ssm_fwd(const SsmArgs& a, void* workspace) {
