@@ -867,14 +867,18 @@ Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf
 }
 
 // Packed sequences, whose lengths the host does not know: segments of as many chunks as a workgroup
-// slot of the GPU has of all, or half as many where there are sequences enough to fill the slots (then
-// only the longest are cut, and the launch does not wait for their chains alone).
-Plan plan_packed(int64_t N, int64_t total, int64_t H, int64_t dk, int64_t dv, int64_t cus) {
+// slot of the GPU has of all, or two thirds of it where there are sequences enough to fill the slots
+// (then only the longest are cut, and the launch does not wait for their chains alone); at least
+// four, in fp32, whose chunks outweigh a segment's costs, two.  In us, segments of the rule / half as
+// long / whole sequences: 16 prompts of about 700 tokens, 16 heads 136 / 149 / 243; 64 of 512, 32 heads
+// of 64 columns 266 / 307 / 326; 8 of 300, 6 heads in fp32 37 / - / 206 (segments of four 47).
+Plan plan_packed(int64_t N, int64_t total, int64_t H, int64_t dk, int64_t dv, bool bf16_in, int64_t cus) {
     Plan p{};
     p.segs = 1;
-    const int64_t nc = total / Q + N, wide = H * dv < 128 ? 1 : H * dv / 128, slots = N * wide < cus ? 2 * cus : 4 * cus;
+    const int64_t nc = total / Q + N, wide = H * dv < 128 ? 1 : H * dv / 128, slots = N * wide < 2 * cus ? 2 * cus : 3 * cus;
+    const int64_t least = bf16_in ? 4 : 2;
     int64_t len = (nc * wide + slots - 1) / slots;
-    if (len < 4) len = 4;
+    if (len < least) len = least;
     if (len > kBins - 1) len = kBins - 1;
     if (total <= len * Q) return p;  // no sequence can be longer than a segment
     p.segs = 0;
@@ -943,7 +947,8 @@ hipError_t launch_dk(const SsmArgs& a, const Plan& plan, void* ws) {
 template <typename T>
 hipError_t launch_fwd(const SsmArgs& a, void* ws) {
     Plan plan{};
-    if (ws) plan = a.cu_seqlens ? plan_packed(a.N, a.T, a.H, a.dk, a.dv, a.cus) : plan_fixed(a.N, a.T, a.H, a.dk, a.dv, a.dtype_bf16, a.cus);
+    if (ws) plan = a.cu_seqlens ? plan_packed(a.N, a.T, a.H, a.dk, a.dv, a.dtype_bf16, a.cus)
+                                : plan_fixed(a.N, a.T, a.H, a.dk, a.dv, a.dtype_bf16, a.cus);
     return a.dk == 128 ? launch_dk<T, 128>(a, plan, ws) : launch_dk<T, 64>(a, plan, ws);
 }
 
@@ -1018,7 +1023,7 @@ hipError_t launch_step(const SsmArgs& a) {
 
 size_t ssm_workspace_bytes(bool packed, int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf16_in,
                            int64_t cus) {
-    return (size_t)(packed ? ssm::plan_packed(N, T, H, dk, dv, cus) : ssm::plan_fixed(N, T, H, dk, dv, bf16_in, cus))
+    return (size_t)(packed ? ssm::plan_packed(N, T, H, dk, dv, bf16_in, cus) : ssm::plan_fixed(N, T, H, dk, dv, bf16_in, cus))
                         .total;
 }
 
