@@ -298,8 +298,8 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
 // their y is dropped.
 // Bound by issue.  A wave's chunk (dk = 128, 32 columns) is 152 matrix instructions of 16 cycles, 96
 // of them the state's three planes, and 715 vector ones, which hardly run beside the other wave's on
-// its SIMD.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 132 us of this pass (matrix 30% and
-// vector 35% of the cycles, LDS 25%) and 63 of the pass for ENDS under a profiler, 171 in all
+// its SIMD.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 137 us of this pass (matrix 30% and
+// vector 35% of the cycles, LDS 25%) and 64 of the pass for ENDS under a profiler, 172 in all
 // without one (1.7 TB/s; the inputs and outputs alone would take 61).  Eight waves a workgroup
 // spilled (269); 64 columns a workgroup repeat c . b and M (195); with 64 columns and four more
 // waves that only load and form M, one barrier a chunk, this pass took 171 and ENDS 55.
