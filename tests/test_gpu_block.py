@@ -627,3 +627,54 @@ def test_two_graphs_replayed_in_turn():
             makers[1 - i]()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(graphs[i][1], refs[i]))
+
+
+# ---- sizes past 32 bits ---------------------------------------------------------------------
+
+def test_scan_past_32_bit_offsets():
+    """2.3e9 elements (4.6 GB) of x: the last sequences give what they give alone."""
+    N, T, H, G, dk, dv = 17600, 64, 32, 1, 64, 64
+    k = dev(scan_case(BF16, (16, T), H, G, dk, dv, 60))
+    x = torch.zeros(N, T, H, dv, dtype=BF16, device="cuda")
+    dt = torch.zeros(N, T, H, dtype=BF16, device="cuda")
+    B = torch.zeros(N, T, G, dk, dtype=BF16, device="cuda")
+    C = torch.zeros_like(B)
+    assert x.numel() > 2 ** 31
+    for big, name in ((x, "x"), (dt, "dt"), (B, "B"), (C, "C")):
+        big[-16:] = k[name]
+    rest = (k["A"], k["D"], k["dt_bias"])
+    ref, sref = gdn2.ssm_fwd(k["x"], k["dt"], k["B"], k["C"], *rest)
+    y, s = gdn2.ssm_fwd(x, dt, B, C, *rest)
+    assert torch.equal(y[-16:], ref) and torch.equal(s[-16:], sref)
+    assert not y[:16].any() and not s[:16].any()
+    y.fill_(7)
+    cu = (torch.arange(N + 1) * T).cuda()
+    gdn2.ssm_fwd_varlen(x.flatten(0, 1), dt.flatten(0, 1), B.flatten(0, 1), C.flatten(0, 1), k["A"], cu, k["D"],
+                        k["dt_bias"], y=y.flatten(0, 1), final_state=s)
+    assert torch.equal(y[-16:], ref) and torch.equal(s[-16:], sref)
+
+
+def test_conv_and_norm_past_32_bit_offsets():
+    rows, width = 281000, 8192
+    g = torch.Generator("cpu").manual_seed(61)
+    tail = torch.randn(400, width, generator=g).to(BF16).cuda()
+    taps, bias, gamma = (torch.randn(s, generator=g).cuda() for s in ((width, 4), (width,), (width,)))
+    x = torch.zeros(rows, width, dtype=BF16, device="cuda")
+    assert x.numel() > 2 ** 31
+    x[-400:] = tail
+    y, kept = gdn2.short_conv(x[None], taps, bias)
+    ref, rkept = gdn2.short_conv(tail[None], taps, bias)
+    assert torch.equal(y[0, -400:], ref[0]) and torch.equal(kept, rkept)
+    cu = torch.tensor([0, 5, rows - 400, rows], device="cuda")
+    _, kept = gdn2.short_conv_varlen(x, taps, cu, bias, y=y[0].fill_(7))
+    assert torch.equal(y[0, -400:], ref[0]) and torch.equal(kept[2:], rkept)
+    y, mean, rstd = gdn2.layer_norm(x, gamma, y=y[0])
+    ref, rmean, rrstd = gdn2.layer_norm(tail, gamma)
+    assert torch.equal(y[-400:], ref) and torch.equal(mean[-400:], rmean) and torch.equal(rstd[-400:], rrstd)
+    # rows of zeros have dy = x = 0 here: only the last ones add to the sums
+    got = gdn2.layer_norm_bwd(x, x, gamma, mean, rstd, grads={"dx": y})
+    want = gdn2.layer_norm_bwd(tail, tail, gamma, rmean, rrstd)
+    assert torch.equal(got["dx"][-400:], want["dx"])
+    ab = (tail.double() * (tail.double() - rmean.double()[:, None]) * rrstd.double()[:, None]).abs().sum(0)
+    within("dgamma", got["dgamma"], f64(want["dgamma"]), 600 * U * f64(ab))
+    within("dbeta", got["dbeta"], f64(want["dbeta"]), 600 * U * f64(tail.double().abs().sum(0)))
