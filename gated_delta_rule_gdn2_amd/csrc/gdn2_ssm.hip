@@ -288,9 +288,9 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
     else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(U4, v), r, off, 0, 0);
 }
 
-// A workgroup of four waves walks HP heads of one sequence, HP DV = 16 PT columns per wave, chunk by
-// chunk: one head of 128 columns, two of 64 that share b and c (c . b is then formed once for
-// both), or one of 64.  Wave w holds its state columns in accumulators (rows n of all of them),
+// A workgroup of four waves walks CW state columns of one sequence, 16 PT of them a wave, chunk by
+// chunk: one head of 128 columns, half of one, two of 64 that share b and c (HP; c . b is then
+// formed once for both), or one of 64.  Wave w holds its state columns in accumulators (rows n of all of them),
 // computes its share of M's ten 16 x 16 tiles into LDS, and forms y^T (columns by tokens) and the
 // next state for its columns.  Two tiles of columns a wave halve the LDS reads of b, c and M, which
 // at one tile took as long as the products.  The next chunk's inputs are loaded into registers
@@ -301,8 +301,9 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
 // its SIMD.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 137 us of this pass (matrix 30% and
 // vector 35% of the cycles, LDS 25%) and 64 of the pass for ENDS under a profiler, 172 in all
 // without one (1.7 TB/s; the inputs and outputs alone would take 61).  Eight waves a workgroup
-// spilled (269); 64 columns a workgroup repeat c . b and M (195); with 64 columns and four more
-// waves that only load and form M, one barrier a chunk, this pass took 171 and ENDS 55.
+// spilled (269); 64 columns a workgroup repeat c . b and M (195; they are for calls that leave
+// compute units idle); with 64 columns and four more waves that only load and form M, one barrier a
+// chunk, this pass took 171 and ENDS 55.
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
 constexpr int NW = 4;
@@ -310,9 +311,9 @@ constexpr int NW = 4;
 // its own start.  That is more to read with each segment (4 of 8 x 4096 tokens: 171 us without the
 // join, 176 with it; 6 of 2 x 333 tokens: 27 and 30; 32 of one of 32768: 214 and 182).
 constexpr int kFew = 6;
-template <typename T, int DK, int DV, int HP, bool ENDS>
+template <typename T, int DK, int DV, int CW, bool ENDS>
 __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void chunk_kernel(Params a) {
-    constexpr int CW = HP * DV, PT = CW / (16 * NW), NTH = 64 * NW, ES = (int)sizeof(T);
+    constexpr int HP = CW > DV ? CW / DV : 1, PT = CW / (16 * NW), NTH = 64 * NW, ES = (int)sizeof(T);
     typedef Tile<T, DK, kCols> TB;
     typedef Tile<T, DK, kRows> TC;
     typedef Tile<T, CW, kBoth> TX;
@@ -328,7 +329,8 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     const int g4 = (lane >> 4) * 4;
     int slot, hb;
     if (!unit_of(a, &slot, &hb)) return;
-    const int h0 = hb * HP, hw = w * 16 * PT / DV;  // the first head, this wave's among them
+    const int h0 = hb * CW / DV, hw = w * 16 * PT / DV;  // the first head, this wave's among them
+    const int col0 = CW < DV ? hb * CW % DV : 0;         // of a head in parts: the first column
     const int c0 = w * 16 * PT;                     // its first column of the workgroup's
     static_assert(sizeof(sB) >= (kMaxSort + 1) * sizeof(int), "scratch of longest_first");
     int n, seg = 0, index = -1, count = 1;  // index: of this segment's state, where its sequence is cut
@@ -361,17 +363,17 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     }
     const int len = (int)(hi - lo), nc = (len + Q - 1) / Q;
     const int group = h0 / (a.H / a.G);
-    const T* gx = (const T*)a.x + lo * a.xs + h0 * DV;
+    const T* gx = (const T*)a.x + lo * a.xs + h0 * DV + col0;
     const T* gb = (const T*)a.b + lo * a.bs + group * DK;
     const T* gc = (const T*)a.c + lo * a.cs + group * DK;
     const T* gt = (const T*)a.dt + lo * a.dts + h0;
-    T* gy = (T*)a.y + (lo * a.H + h0) * DV;
+    T* gy = (T*)a.y + (lo * a.H + h0) * DV + col0;
     const int ys = a.H * DV;
     const float D = a.D ? a.D[h0 + hw] : 0.f;
 
     f32x4 S[PT][NT];  // rows 16 nt + 4g + r, column c0 + 16 pt + lane % 16
     const int64_t state = (int64_t)n * a.H + h0 + hw;
-    const int at0 = g4 * DV + c0 % DV + l16;
+    const int at0 = g4 * DV + col0 + c0 % DV + l16;
     const float* from = a.s0 ? a.s0 + state * (DK * DV) : nullptr;
     const bool own = index >= 0 && count <= a.few;  // the start is formed here
     if (ENDS) from = nullptr;
@@ -686,7 +688,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         for (int hp = 0; hp < HP; ++hp)
             if (lane == 0) sLogs[hp][w] = logs[hp];
         __syncthreads();
-        if (tid < HP) a.logs[(int64_t)index * a.H + h0 + tid] = (sLogs[tid][0] + sLogs[tid][1]) + (sLogs[tid][2] + sLogs[tid][3]);
+        if (tid < HP && col0 == 0) a.logs[(int64_t)index * a.H + h0 + tid] = (sLogs[tid][0] + sLogs[tid][1]) + (sLogs[tid][2] + sLogs[tid][3]);
     }
 }
 
@@ -832,18 +834,21 @@ struct Plan {
 };
 
 // Sequences of one length.  A chunk's time is the unit.  A compute unit runs two workgroups (of 128
-// state columns) at once, each then 1.36 times as long as one alone; the pass for the segments' ends
-// takes half a chunk's time a chunk; launches, the states' way through HBM and the join, which walks
-// the segments, are the rest.  Fitted to calls in us, the chosen one first: 128 sequence-heads of 64
-// chunks in 4 / 1 / 2 / 3 / 8 segments 170 / 242 / 192 / 180 / 193; 16 of 512 in 32 / 16 / 48 176 / 200 /
-// 192; 8 of 32 in 16 / 8 / 32 31 / 37 / 36; fp32, whose chunks take three times as long, 18 of 11 in
-// 11 / 6 44 / 57.
+// state columns) at once, each then 1.36 times as long as one alone; halves of heads take 0.65 of it;
+// the pass for the segments' ends takes half a chunk's time a chunk; launches, the states' way through
+// HBM and the join, which walks the segments, are the rest.  Fitted to calls in us, the chosen one
+// first: 128 sequence-heads of 64 chunks in 4 / 1 / 2 / 3 / 8 segments 170 / 242 / 192 / 180 / 193; 16 of
+// 512 in 32 / 16 / 48 176 / 200 / 192; before the halves 8 of 32 in 16 / 8 / 32 31 / 37 / 36, with them
+// 27; fp32, whose chunks take three times as long, 18 of 11 in 6 39.
 Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf16_in, int64_t cus) {
     Plan p{};
     const int64_t nc = (T + Q - 1) / Q, heads = N * H;
     // workgroups of a segment: pairs of heads of 64 columns only where there are enough of them
     const int64_t chains = dv == 128 || heads <= cus ? heads : (heads + 1) / 2;
-    auto rounds = [&](int64_t w) { return w <= cus ? 1.0 : 1.36 * (double)((w + 2 * cus - 1) / (2 * cus)); };
+    auto rounds = [&](int64_t w) {
+        if (dv == 128 && 2 * w <= cus) return 0.65;  // heads in halves
+        return w <= cus ? 1.0 : 1.36 * (double)((w + 2 * cus - 1) / (2 * cus));
+    };
     double best = rounds(chains) * (double)nc;
     p.segs = 1;
     for (int64_t g = 2; g <= nc && g <= 128 && chains * g <= 8 * cus; ++g) {
@@ -895,11 +900,11 @@ Plan plan_packed(int64_t N, int64_t total, int64_t H, int64_t dk, int64_t dv, bo
     return p;
 }
 
-template <typename T, int DK, int DV, int HP>
+template <typename T, int DK, int DV, int CW>
 hipError_t launch_chunks(const SsmArgs& a, const Plan& plan, void* workspace) {
     Params p = params(a);
     const hipStream_t stream = (hipStream_t)a.stream;
-    const int blocks = (int)a.H / HP;
+    const int blocks = (int)a.H * DV / CW;
     char* ws = static_cast<char*>(workspace);
     int64_t ends = 0, cuts = 0, slots = a.N;
     if (plan.total) {
@@ -924,25 +929,28 @@ hipError_t launch_chunks(const SsmArgs& a, const Plan& plan, void* workspace) {
             slots = a.N * plan.segs;
         }
         set_grid(&p, (int)ends, blocks);
-        hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, true>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);
+        hipLaunchKernelGGL((chunk_kernel<T, DK, DV, CW, true>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);
         // workgroups that fit the GPU at once: how many sequences there are to join the host does not know
         const int64_t need = (cuts * a.H * DK * DV / 4 + 255) / 256, fit = a.cus * 8;
         if ((a.cu_seqlens ? plan.ends + 1 : plan.segs) > p.few)
             hipLaunchKernelGGL(join_kernel, dim3((unsigned)(need < fit ? need : fit)), dim3(256), 0, stream, p, DK);
     }
     set_grid(&p, (int)slots, blocks);
-    hipLaunchKernelGGL((chunk_kernel<T, DK, DV, HP, false>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);
+    hipLaunchKernelGGL((chunk_kernel<T, DK, DV, CW, false>), dim3(grid_of(p)), dim3(64 * NW), 0, stream, p);
     return hipGetLastError();
 }
 
 template <typename T, int DK>
 hipError_t launch_dk(const SsmArgs& a, const Plan& plan, void* ws) {
-    if (a.dv == 128) return launch_chunks<T, DK, 128, 1>(a, plan, ws);
-    // Two heads a workgroup where a group has an even number of them and pairs still fill the GPU:
-    // c . b and the staging of b and c are shared, but few workgroups take longer.
-    const int64_t pairs = (plan.pieces ? plan.pieces : a.N * (plan.total ? plan.segs : 1)) * a.H / 2;
-    return a.H / a.G % 2 == 0 && pairs >= a.cus ? launch_chunks<T, DK, 64, 2>(a, plan, ws)
-                                                 : launch_chunks<T, DK, 64, 1>(a, plan, ws);
+    const int64_t heads = (plan.pieces ? plan.pieces : a.N * (plan.total ? plan.segs : 1)) * a.H;
+    // Heads of 128 columns go to two workgroups each while every one then has a compute unit of its own
+    // (8 heads of 300 tokens 14 us, whole 19; 160 heads of 128 in fp32, which have not, 44 and 35).
+    if (a.dv == 128)
+        return 2 * heads <= a.cus ? launch_chunks<T, DK, 128, 64>(a, plan, ws) : launch_chunks<T, DK, 128, 128>(a, plan, ws);
+    // Two heads of 64 a workgroup where a group has an even number of them and pairs still fill the
+    // GPU: c . b and the staging of b and c are shared, but few workgroups take longer.
+    return a.H / a.G % 2 == 0 && heads / 2 >= a.cus ? launch_chunks<T, DK, 64, 128>(a, plan, ws)
+                                                     : launch_chunks<T, DK, 64, 64>(a, plan, ws);
 }
 template <typename T>
 hipError_t launch_fwd(const SsmArgs& a, void* ws) {

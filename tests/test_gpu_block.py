@@ -102,6 +102,11 @@ SCANS = [  # dtype, B, T, H, G, dk, dv, states, strong
     (F32, 1, 200, 2, 2, 128, 128, False, True),
     (F32, 2, 333, 3, 3, 64, 128, True, False),
     (F32, 1, 2500, 2, 1, 64, 64, True, False),
+    # heads of 128 columns in one workgroup each (the few heads above are in halves), whole and cut
+    (BF16, 9, 70, 16, 2, 128, 128, True, False),
+    (BF16, 3, 1300, 16, 1, 64, 128, True, False),
+    (F32, 9, 70, 16, 1, 64, 128, True, False),
+    (F32, 2, 450, 18, 2, 64, 128, True, False),
 ]
 
 
