@@ -107,3 +107,75 @@ def test_packed_scan_forms_match_oracle(dtype, lengths, H, G, dk, dv, cut):
     y2, _ = gdn2.ssm_fwd_varlen(*args_of(d), cu.cuda(), d["D"], d["dt_bias"], state, y=torch.full_like(y, 7.0),
                                 final_state=state)
     assert torch.equal(y, y2) and torch.equal(s, state)
+
+
+# ---- step past the caches -------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,N,H,G,dk,dv", [(BF16, 140, 16, 1, 128, 128), (F32, 130, 17, 1, 128, 128),
+                                               (BF16, 263, 16, 4, 64, 128), (F32, 270, 16, 2, 128, 64),
+                                               (BF16, 530, 16, 8, 64, 64)])
+def test_step_past_the_caches_matches_oracle(dtype, N, H, G, dk, dv):
+    """More than 128 MB of states: every state and output, against the step's formula in 64 bits."""
+    assert N * H * dk * dv * 4 > 128 << 20
+    k = scan_case(dtype, (N,), H, G, dk, dv, 500 + N, N)
+    d = dev(k)
+    state = d["s0"].clone()
+    y = gdn2.ssm_step(*args_of(d), state, d["D"], d["dt_bias"])
+    x, raw, b, c, a, bias, s0 = (d[n].double() for n in ("x", "dt", "B", "C", "A", "dt_bias", "s0"))
+    dt = torch.nn.functional.softplus(raw + bias, threshold=40)
+    b, c = b.repeat_interleave(H // G, 1), c.repeat_interleave(H // G, 1)
+    keep, put = s0 * torch.exp(dt * a)[..., None, None], (dt[..., None] * b)[..., None] * x[:, :, None]
+    s, size = keep + put, keep.abs() + put.abs()
+    assert bool(((state.double() - s).abs() <= 320 * U * size + 1e-30).all())
+    dx = d["D"].double()[:, None] * x
+    want = (s * c[..., None]).sum(-2) + dx
+    tol = 320 * U * ((size * c.abs()[..., None]).sum(-2) + dx.abs()) + (2.0 ** -8 * want.abs() if dtype == BF16 else 0)
+    assert bool(((y.double() - want).abs() <= tol + 1e-30).all())
+
+
+# ---- convolution in runs of 16 tokens -------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_conv_in_long_runs_matches_oracle(dtype):
+    B, T, C = 3, 1201, 2560
+    assert B * T // 16 * (C // 4) >= 1 << 17
+    k = conv_case(dtype, (B, T), C, B, 600)
+    d = dev(k)
+    ref, tol, kr = conv_ref(k["x"], k["taps"], k["bias"], k["s0"])
+    y, kept = gdn2.short_conv(d["x"], d["taps"], d["bias"], d["s0"])
+    within("y", y, ref, tol)
+    assert np.array_equal(f64(kept), kr)
+    state = d["s0"].clone()
+    y2, _ = gdn2.short_conv(d["x"], d["taps"], d["bias"], state, final_state=state)
+    assert torch.equal(y, y2) and torch.equal(state, kept)
+    ref, tol, _ = conv_ref(k["x"][:1], k["taps"], None, None)
+    within("y", gdn2.short_conv(d["x"], d["taps"])[0][:1], ref, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_packed_conv_in_long_runs_matches_oracle(dtype, in_place):
+    """Several short sequences in a run, empty ones, and long ones that begin and end on and beside a run's edges."""
+    g = torch.Generator("cpu").manual_seed(610)
+    lengths = [16, 16, 15, 17, 1, 0, 0, 2, 3, 10, 0, 333, 1, 400, 31, 33] + torch.randint(0, 30, (120,), generator=g).tolist() + [1000, 16, 0]
+    C, lead, behind = 2560, 3, 21
+    total = lead + sum(lengths) + behind
+    assert total // 16 * (C // 4) >= 1 << 17
+    k = conv_case(dtype, (total,), C, len(lengths), 611)
+    cu = torch.tensor([lead] + lengths).cumsum(0)
+    end = int(cu[-1])
+    k["x"][:lead] = float("nan")
+    k["x"][end:] = float("nan")
+    d = dev(k)
+    y0 = torch.full((total, C), 7.0, dtype=dtype, device="cuda")
+    out = d["s0"] if in_place else torch.full_like(d["s0"], float("nan"))
+    y, kept = gdn2.short_conv_varlen(d["x"], d["taps"], cu.cuda(), d["bias"], d["s0"], y=y0, final_state=out)
+    assert (y[:lead] == 7).all() and (y[end:] == 7).all()
+    worst = 0.0
+    for i, n in enumerate(lengths):
+        lo = int(cu[i])
+        ref, tol, kr = conv_ref(k["x"][None, lo:lo + n], k["taps"], k["bias"], k["s0"][i:i + 1])
+        assert np.array_equal(f64(kept[i:i + 1]), kr), i
+        if n:
+            worst = max(worst, float((np.abs(f64(y[None, lo:lo + n]) - ref) / (tol + 1e-30)).max()))
+    assert worst <= 1.0, worst
