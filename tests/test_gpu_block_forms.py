@@ -109,6 +109,122 @@ def test_packed_scan_forms_match_oracle(dtype, lengths, H, G, dk, dv, cut):
     assert torch.equal(y, y2) and torch.equal(s, state)
 
 
+def whole(name, d, sizes, strides, y, s, code, *cu):
+    """The library's call without a workspace."""
+    ptrs = [t.data_ptr() for t in args_of(d)] + [d["D"].data_ptr(), d["dt_bias"].data_ptr(), d["s0"].data_ptr()]
+    block._launch(name, y.device, *ptrs, y.data_ptr(), s.data_ptr(), *cu, *sizes, *strides, code, 1, None, 0)
+
+
+@pytest.mark.parametrize("dtype,H,G,dk,dv", [(BF16, 2, 1, 128, 128), (F32, 4, 2, 64, 64), (BF16, 32, 2, 64, 64)])
+def test_scan_without_a_workspace(dtype, H, G, dk, dv):
+    """Sequences that would be cut, walked whole."""
+    B, T = 2, 900
+    k = scan_case(dtype, (B, T), H, G, dk, dv, 400 + H, B)
+    assert gdn2.ssm_fwd_workspace_bytes(B, T, H, dk, dv, dtype) > 0
+    d = dev(k)
+    y, s = torch.empty_like(d["x"]), torch.empty_like(d["s0"])
+    sizes, strides = (B, T, H, G, dk, dv), (H * dv, H, G * dk, G * dk)
+    whole("gdn2_ssm_fwd", d, sizes, strides, y, s, 1 if dtype == BF16 else 0)
+    for n in range(B):
+        one = sequence(k, n)
+        check_scan(one, y[n:n + 1], s[n:n + 1], oracle_scan(one), (T + 63) // 64)
+
+
+@pytest.mark.parametrize("dtype,H,G,dk,dv", [(BF16, 2, 1, 128, 128), (F32, 4, 2, 64, 64), (BF16, 128, 2, 64, 64)])
+def test_packed_scan_without_a_workspace(dtype, H, G, dk, dv):
+    lengths = [0, 256, 257, 1, 900, 700, 512, 0, 3]
+    k, cu = packed_case(dtype, lengths, H, G, dk, dv, 410 + H)
+    assert gdn2.ssm_fwd_varlen_workspace_bytes(len(lengths), sum(lengths), H, dk, dv, dtype) > 0
+    d = dev(k)
+    y, s = torch.empty_like(d["x"]), torch.empty_like(d["s0"])
+    at = cu.cuda()
+    sizes, strides = (len(lengths), sum(lengths), H, G, dk, dv), (H * dv, H, G * dk, G * dk)
+    whole("gdn2_ssm_fwd_varlen", d, sizes, strides, y, s, 1 if dtype == BF16 else 0, at.data_ptr())
+    for n, length in enumerate(lengths):
+        if length == 0:
+            assert torch.equal(s[n].cpu(), k["s0"][n])
+        elif H < 64 or n < 4:
+            one = part(k, cu, n)
+            check_scan(one, y[None, int(cu[n]):int(cu[n + 1])], s[n:n + 1], oracle_scan(one), (length + 63) // 64)
+
+
+def guarded(need, align):
+    """A caller's workspace at an odd address, and the check that the bytes around it stay."""
+    buf = torch.full((need + align + 1024,), 0xAB, dtype=torch.uint8, device="cuda")
+    ws = buf[513:513 + need + align]
+    lo = 513 + -ws.data_ptr() % align
+
+    def untouched():
+        assert (buf[:lo] == 0xAB).all() and (buf[lo + need:] == 0xAB).all()
+    return ws, untouched
+
+
+@pytest.mark.parametrize("dtype,T", [(BF16, 1600), (BF16, 3300), (F32, 333)])
+def test_scan_stays_in_the_callers_workspace(dtype, T):
+    k = scan_case(dtype, (2, T), 2, 1, 64, 128, 420 + T, 2)
+    d = dev(k)
+    need = gdn2.ssm_fwd_workspace_bytes(2, T, 2, 64, 128, dtype)
+    assert need > 0
+    ws, untouched = guarded(need, 256)
+    ref = gdn2.ssm_fwd(*args_of(d), d["D"], d["dt_bias"], d["s0"])
+    got = gdn2.ssm_fwd(*args_of(d), d["D"], d["dt_bias"], d["s0"], workspace=ws)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    untouched()
+
+
+@pytest.mark.parametrize("lengths", [[700, 0, 300, 2300, 1, 64], [4] * 700 + [600], [260] * 5])
+def test_packed_scan_stays_in_the_callers_workspace(lengths):
+    k, cu = packed_case(BF16, lengths, 2, 1, 64, 64, 430 + len(lengths))
+    d = dev(k)
+    need = gdn2.ssm_fwd_varlen_workspace_bytes(len(lengths), sum(lengths), 2, 64, 64, BF16)
+    assert need > 0
+    ws, untouched = guarded(need, 256)
+    ref = gdn2.ssm_fwd_varlen(*args_of(d), cu.cuda(), d["D"], d["dt_bias"], d["s0"])
+    got = gdn2.ssm_fwd_varlen(*args_of(d), cu.cuda(), d["D"], d["dt_bias"], d["s0"], workspace=ws)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    untouched()
+
+
+@pytest.mark.parametrize("N", [8, 1500])
+def test_packed_scan_of_offsets_that_overlap(N):
+    """Every second sequence is all of the tokens: more pieces than sequences side by side have.  All
+    of them agree with the oracle, those that are cut and those for which the lists have no place."""
+    T = 1500 if N == 8 else 300
+    k = scan_case(BF16, (T,), 2, 1, 64, 64, 440, None)
+    d = dev(k)
+    cu = torch.tensor([0, T] * (N // 2) + [0], device="cuda")
+    need = gdn2.ssm_fwd_varlen_workspace_bytes(N, T, 2, 64, 64, BF16)
+    assert need > 0
+    ws, untouched = guarded(need, 256)
+    y, s = gdn2.ssm_fwd_varlen(*args_of(d), cu, d["D"], d["dt_bias"], workspace=ws)
+    untouched()
+    one = {m: (v[None] if m in TOKENS else v) for m, v in k.items()}
+    ref = oracle_scan(one)
+    for n in (0, 2, N - 2):
+        check_scan(one, y[None], s[n:n + 1], ref, (T + 63) // 64)
+    assert not s[1::2].any()
+
+
+def test_packed_scan_writes_states_past_32_bit_offsets():
+    """2.3e9 elements of states, of no defined value before the call."""
+    N, T, H, G, dk, dv = 17600, 2, 32, 1, 64, 64
+    k = scan_case(BF16, (16 * T,), H, G, dk, dv, 450)
+    d = dev(k)
+    big = {n: torch.zeros(N * T, *d[n].shape[1:], dtype=BF16, device="cuda") for n in TOKENS}
+    for n in TOKENS:
+        big[n][-16 * T:] = d[n]
+    s = torch.full((N, H, dk, dv), float("nan"), device="cuda")
+    assert s.numel() > 2 ** 31
+    cu = (torch.arange(N + 1) * T).cuda()
+    y, _ = gdn2.ssm_fwd_varlen(big["x"], big["dt"], big["B"], big["C"], d["A"], cu, d["D"], d["dt_bias"], final_state=s)
+    assert all(not s[lo:lo + 1100].any() for lo in range(0, N - 1100, 1100)) and not s[N - 1100:N - 16].any()
+    at = torch.arange(17) * T
+    for n in (0, 15):
+        one = part(k, at, n)
+        lo = (N - 16 + n) * T
+        check_scan(one, y[None, lo:lo + T], s[N - 16 + n:N - 15 + n], oracle_scan(one), 1)
+
+
 # ---- step past the caches -------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype,N,H,G,dk,dv", [(BF16, 140, 16, 1, 128, 128), (F32, 130, 17, 1, 128, 128),
@@ -179,3 +295,20 @@ def test_packed_conv_in_long_runs_matches_oracle(dtype, in_place):
         if n:
             worst = max(worst, float((np.abs(f64(y[None, lo:lo + n]) - ref) / (tol + 1e-30)).max()))
     assert worst <= 1.0, worst
+
+
+# ---- norm -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,rows,width", [(BF16, 300, 1000), (F32, 1001, 1540), (F32, 9, 16384)])
+def test_norm_gradients_stay_in_the_callers_workspace(dtype, rows, width):
+    g = torch.Generator("cpu").manual_seed(rows)
+    x, dy = (torch.randn(rows, width, generator=g).to(dtype).cuda() for _ in range(2))
+    gamma = torch.randn(width, generator=g).cuda()
+    _, mean, rstd = gdn2.layer_norm(x, gamma)
+    need = gdn2.layer_norm_bwd_workspace_bytes(rows, width)
+    assert need > 0
+    ws, untouched = guarded(need, 16)
+    ref = gdn2.layer_norm_bwd(dy, x, gamma, mean, rstd)
+    got = gdn2.layer_norm_bwd(dy, x, gamma, mean, rstd, workspace=ws)
+    assert all(torch.equal(ref[n], got[n]) for n in ref)
+    untouched()
