@@ -19,6 +19,7 @@ using gdn2::Range;
 using gdn2::range_of;
 
 constexpr int64_t kMaxStride = int64_t(1) << 22;  // elements between tokens: 64 of them stay below 2^30 bytes
+constexpr int64_t kMaxStepStride = int64_t(1) << 31;  // and between a step's, which are multiplied in 64 bits
 constexpr int64_t kMaxWidth = 16384;
 // Tokens of a sequence, or of all packed ones: indexes a few chunks behind the last stay 32-bit.
 constexpr int64_t kMaxTokens = INT_MAX - 1024;
@@ -59,8 +60,8 @@ gdn2_status_t check_ssm(const gdn2::SsmArgs& a, gdn2_dtype_t dtype, int64_t toke
     if (a.H * a.dv >= kMaxStride || a.G * a.dk >= kMaxStride) return GDN2_ERR_SHAPE;
     if (a.x_stride < a.H * a.dv || a.dt_stride < a.H || a.b_stride < a.G * a.dk || a.c_stride < a.G * a.dk)
         return GDN2_ERR_SHAPE;
-    if (a.x_stride >= kMaxStride || a.dt_stride >= kMaxStride || a.b_stride >= kMaxStride || a.c_stride >= kMaxStride)
-        return GDN2_ERR_SHAPE;
+    const int64_t far = in_place ? kMaxStepStride : kMaxStride;
+    if (a.x_stride >= far || a.dt_stride >= far || a.b_stride >= far || a.c_stride >= far) return GDN2_ERR_SHAPE;
     const int64_t es = elem(dtype);
     int64_t nh, ns, nx, nt, nb, nc, ny;
     if (!mul_ok(a.N, a.H, &nh) || nh > kMaxHeads || !mul_ok(nh, a.dk * a.dv * 4, &ns)) return GDN2_ERR_SHAPE;
@@ -122,7 +123,8 @@ gdn2_status_t check_conv(const gdn2::ConvArgs& a, gdn2_dtype_t dtype, int64_t to
     if (a.N < 1 || a.T < 0 || tokens < 0 || a.C < 1 || a.C % 8) return GDN2_ERR_SHAPE;
     if (tokens > 0 && (!a.x || !a.y)) return GDN2_ERR_NULL;
     if (!a.taps || (in_place && !a.final_state)) return GDN2_ERR_NULL;
-    if (a.N > INT_MAX || a.T > INT_MAX || a.C >= kMaxStride || a.x_stride < a.C || a.x_stride >= kMaxStride)
+    const int64_t far = in_place ? kMaxStepStride : kMaxStride;
+    if (a.N > INT_MAX || a.T > INT_MAX || a.C >= kMaxStride || a.x_stride < a.C || a.x_stride >= far)
         return GDN2_ERR_SHAPE;
     const int64_t es = elem(dtype);
     int64_t nx, ny, ns;

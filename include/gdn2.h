@@ -432,7 +432,8 @@ size_t gdn2_ssm_fwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t H
                                            int64_t dv, gdn2_dtype_t dtype);
 
 /* gdn2_ssm_step -- one token for each of N sequences: x [N, H, dv], dt [N, H],
- * b, c [N, G, dk], y [N, H, dv]; state [N, H, dk, dv] is updated in place. */
+ * b, c [N, G, dk], y [N, H, dv]; state [N, H, dk, dv] is updated in place.
+ * Strides below 2^31: the last tokens of N prompts lie a prompt apart. */
 gdn2_status_t gdn2_ssm_step(const void* x, const void* dt, const void* b, const void* c,
                             const float* A, const float* D, const float* dt_bias, float* state,
                             void* y, int64_t N, int64_t H, int64_t G, int64_t dk, int64_t dv,
@@ -476,7 +477,7 @@ gdn2_status_t gdn2_short_conv_varlen(const void* x, const float* taps, const flo
                                      int64_t C, int64_t x_stride, gdn2_dtype_t dtype, void* stream);
 
 /* gdn2_short_conv_step -- one token for each of N sequences: x, y [N, C]; state
- * [N, 3, C] is updated in place. */
+ * [N, 3, C] is updated in place.  x_stride below 2^31. */
 gdn2_status_t gdn2_short_conv_step(const void* x, const float* taps, const float* bias, void* state,
                                    void* y, int64_t N, int64_t C, int64_t x_stride,
                                    gdn2_dtype_t dtype, void* stream);

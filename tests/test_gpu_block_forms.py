@@ -249,6 +249,33 @@ def test_step_past_the_caches_matches_oracle(dtype, N, H, G, dk, dv):
     assert bool(((y.double() - want).abs() <= tol + 1e-30).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_steps_on_the_last_tokens_of_long_prompts(dtype):
+    """[:, -1] of [N, T, C] with T C past 2^22 gives the bits of its copy."""
+    N, T, H, G, dk, dv = 3, 2050, 16, 1, 128, 128
+    C = H * dv + 2 * G * dk
+    assert T * C > 1 << 22
+    k = scan_case(dtype, (N,), H, G, dk, dv, 560, N)
+    d = dev(k)
+    c = dev(conv_case(dtype, (N,), C, N, 561))
+    flat = torch.cat([d["x"].flatten(1), d["B"].flatten(1), d["C"].flatten(1)], -1)
+    prompts = torch.zeros(N, T, C, dtype=dtype, device="cuda")
+    prompts[:, -1] = flat
+    steps = torch.zeros(N, T * C, H, dtype=dtype, device="cuda")[:, :1].squeeze(1)
+    steps.copy_(d["dt"])
+    parts = prompts[:, -1].split([H * dv, G * dk, G * dk], -1)
+    far = [v.unflatten(-1, (n, -1)) for v, n in zip(parts, (H, G, G))]
+    state, want = d["s0"].clone(), d["s0"].clone()
+    ref = gdn2.ssm_step(*args_of(d), want, d["D"], d["dt_bias"])
+    got = gdn2.ssm_step(far[0], steps, far[1], far[2], d["A"], state, d["D"], d["dt_bias"])
+    assert torch.equal(ref, got) and torch.equal(want, state)
+    c["x"] = flat
+    kept, want = c["s0"].clone(), c["s0"].clone()
+    ref = gdn2.short_conv_step(c["x"], c["taps"], want, c["bias"])
+    got = gdn2.short_conv_step(prompts[:, -1], c["taps"], kept, c["bias"])
+    assert torch.equal(ref, got) and torch.equal(want, kept)
+
+
 # ---- convolution in runs of 16 tokens -------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
