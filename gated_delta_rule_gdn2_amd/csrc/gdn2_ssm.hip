@@ -742,11 +742,15 @@ __global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__
                                                      int* index_of, int few) {
     __shared__ int at[kBins];  // first pieces of a size: a count, then the place of the next one
     __shared__ int sums[1024];
-    __shared__ int ends, cuts, states;
+    __shared__ unsigned long long ends;  // with the ends given back: of 2^23 sequences that overlap more than 2^32
+    __shared__ int cuts, states;
     const int tid = threadIdx.x;
     Piece* list = reinterpret_cast<Piece*>(split + 1);
     at[tid] = at[tid + 1024] = 0;
-    if (tid == 0) ends = cuts = states = 0;
+    if (tid == 0) {
+        ends = 0;
+        cuts = states = 0;
+    }
     __syncthreads();
     auto chunks = [&](int n) {
         const int64_t lo = min(max(cu[n], (int64_t)0), total), hi = min(max(cu[n + 1], lo), total);
@@ -758,7 +762,7 @@ __global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__
         const int c = chunks(n), full = c / seg_chunks, rest = c - full * seg_chunks, segs = full + (rest ? 1 : 0);
         int index = -1;
         if (segs > 1) {
-            const int e = atomicAdd(&ends, segs - 1);
+            const int64_t e = (int64_t)atomicAdd(&ends, (unsigned long long)(segs - 1));
             if (e + segs - 1 <= max_ends) {
                 index = atomicAdd(&states, segs);
                 for (int k = 0; k + 1 < segs; ++k) list[ends_at + e + k] = Piece{n, k, index + k, segs};
@@ -766,8 +770,7 @@ __global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__
                 atomicAdd(&at[seg_chunks], full);
                 if (rest) atomicAdd(&at[rest], 1);
             } else {  // given back as ends of nothing
-                for (int k = 0; k + 1 < segs; ++k)
-                    if (e + k < max_ends) list[ends_at + e + k] = Piece{-1, 0, 0, 0};
+                for (int k = 0; k + 1 < segs && e + k < max_ends; ++k) list[ends_at + e + k] = Piece{-1, 0, 0, 0};
             }
         }
         if (index < 0) atomicAdd(&at[bin(c)], 1);
@@ -800,7 +803,7 @@ __global__ __launch_bounds__(1024) void split_kernel(const int64_t* __restrict__
         for (int k = 0; k < full; ++k) list[p + k] = Piece{n, k, index + k, segs};
         if (rest) list[atomicAdd(&at[rest], 1)] = Piece{n, full, index + full, segs};
     }
-    if (tid == 0) *split = Split{pieces, min(ends, max_ends), cuts, 0, ends_at, cuts_at};
+    if (tid == 0) *split = Split{pieces, (int)min((int64_t)ends, (int64_t)max_ends), cuts, 0, ends_at, cuts_at};
 }
 
 Params params(const SsmArgs& a) {
