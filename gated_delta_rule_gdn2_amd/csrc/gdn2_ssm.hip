@@ -58,6 +58,8 @@ __device__ __forceinline__ double last_lane(double v) {
 // e^v, rounded to fp32 once before the hardware's base-2 exponential
 __device__ __forceinline__ float exp_of(double v) { return __builtin_amdgcn_exp2f((float)(v * 1.4426950408889634)); }
 
+__device__ __forceinline__ bool is_finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+
 // ---- LDS tiles ------------------------------------------------------------------------------
 // [64 tokens][W] row-major, in 16-byte units whose place in the row is XORed with a function of
 // the row.  Measured phases of the 64 banks: a 16-byte read takes lanes 0-3, 12-15 and 20-27
@@ -185,6 +187,15 @@ template <> struct Planes<bf16> {
             v[1] -= __uint_as_float(u & 0xffff0000u);
         }
     }
+    // the compiler may not move the forming behind this
+    __device__ __forceinline__ void formed() {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            U4 u = __builtin_bit_cast(U4, p[i].v);
+            asm volatile("" : "+v"(u));
+            p[i].v = __builtin_bit_cast(bf16x8, u);
+        }
+    }
 };
 template <> struct Planes<float> {
     static constexpr int N = 1;
@@ -192,6 +203,10 @@ template <> struct Planes<float> {
     __device__ __forceinline__ void set(const Frag<float>& x, int e, float w0, float w1) {
         p[0].v[e] = x.v[e] * w0;
         p[0].v[e + 1] = x.v[e + 1] * w1;
+    }
+    __device__ __forceinline__ void formed() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(p[0].v[e]));
     }
 };
 
@@ -411,6 +426,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
     }
 
     U4 rb[NB], rc[NB], rx[NX];
+    const int oy0 = (l16 * ys + c0 + g4) * ES;  // y of a lane's first tile
     auto load = [&](int ch) {
         const int64_t t0 = (int64_t)ch * Q;
         const int rows = min(len - ch * Q, Q);
@@ -586,6 +602,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
         auto plane = [&](int s, int u) { wx[s][u / 4].set(fx[u / 4][s], u % 4 * 2, wt[s][u % 4 * 2], wt[s][u % 4 * 2 + 1]); };
         const int rows = min(len - ch * Q, Q);
         const auto qy = cb::buffer_over(gy + (int64_t)ch * Q * ys, rows * ys * ES);
+        const int oy = fresh(oy0);
         Vec<T, 4> xq[2];
         auto read_x = [&](int u) { xq[u & 1] = lds_vec<T, 4>(sX, permX ^ ((c0 + u % PT * 16) * ES + u / PT * 16 * TX::RB)); };
         auto put_y = [&](int u) {
@@ -593,8 +610,10 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
             float o[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = Y[pt][it][r] + D * to_f32(xq[u & 1].v[r]);
-            bstore4<T>(qy, ((it * 16 + l16) * ys + c0 + pt * 16 + g4) * ES, o);
+            bstore4<T>(qy, oy + (it * 16 * ys + pt * 16) * ES, o);
         };
+        const float gone = Pair<T>::decay(sCum[k][hw][Q - 1]);
+        auto read_b = [&](int u) { fb[u % 3] = cols_perm<TB>(sB, colsB, u / NT * 32, u % NT * 16); };
         if constexpr (!ENDS) {
             // the chunk's own part: six pieces of M, with the first half's planes beside them
             Frag<T> fm[2];
@@ -604,6 +623,7 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
 #pragma unroll
                 for (int e = 0; e < 8; ++e) fm[u & 1].v[e] = v.v[e];
             };
+            float odd = 0.f;
             read_m(0);
             read_x(0);
             read_x(1);
@@ -627,25 +647,79 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
                         if (v + 2 < 4 * PT) read_x(v + 2);
                     }
                 }
+                if (done == 2) {
+#pragma unroll
+                    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) odd = fmaf(0.f, Y[pt][2][r], odd);
+                }
             }
 #pragma unroll
             for (int v = 3 * PT; v < 4 * PT; ++v) {
                 put_y(v);
                 if (v + 2 < 4 * PT) read_x(v + 2);
             }
+            read_b(0);
+            read_b(1);
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) wx[0][pt].formed();  // beside the products above
+            // M times x takes an x that is not finite to the tokens before it too: 0 x inf.  Tokens 32 to 47
+            // have met all of the chunk's x, so there it shows.  y once more, a tile at a time, with zeros in
+            // the place of such x, and NaN in its column from its token on.  Looking for it costs 2% of a
+            // call (8 x 4096 tokens of 16 heads of 128 x 128: 171 and 175 us).
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(odd != odd) != 0, 0)) {
+#pragma unroll 1
+                for (int it = 0; it < 4; ++it) {
+#pragma unroll
+                    for (int pt = 0; pt < PT; ++pt) {
+                        cb::sched_fence();
+                        const int ln = fresh(lane), l16 = ln & 15, g4 = (ln >> 4) * 4;
+                        const int permC = perm_base<TC>(ln), colsX = cols_base<TX, T>(ln);
+                        f32x4 y = zero4();
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) {
+                            f32x4 lo = S[pt][2 * s], hi = S[pt][2 * s + 1];
+                            asm volatile("" : "+v"(lo), "+v"(hi));  // not converted for all of the tiles at once
+                            mma(y, frag_from_acc<T>(lo, hi), rows_perm<TC, T>(sC, permC, it * 16, s * 32));
+                            cb::sched_fence();
+                        }
+                        y *= Pair<T>::decay(sCum[k][hw][it * 16 + l16]);
+                        for (int s = 0; s <= it >> 1; ++s) {
+                            Frag<T> x = cols_perm<TX>(sX, colsX, s * 32, c0 + pt * 16), m;
+                            const Vec<T, 8> v = load_vec<T, 8>(&sM[hw][((it * 2 + s) * 64 + ln) * 8]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                m.v[e] = v.v[e];
+                                x.v[e] = is_finite(to_f32(x.v[e])) ? x.v[e] : from_f32<T>(0.f);
+                            }
+                            mma(y, x, m);
+                        }
+#pragma unroll 1
+                        for (int j = 0; j < it * 16 + 16; ++j) {
+                            const Vec<T, 4> x = lds_vec<T, 4>(sX, TX::at(j, c0 + pt * 16 + g4));
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (!is_finite(to_f32(x.v[r])) && j <= it * 16 + l16) y[r] = __uint_as_float(__float_as_uint(y[r]) | 0x7fc00000u);
+                        }
+                        const Vec<T, 4> x = lds_vec<T, 4>(sX, TX::at(it * 16 + l16, c0 + pt * 16 + g4));
+                        float o[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[r] = y[r] + D * to_f32(x.v[r]);
+                        bstore4<T>(qy, ((it * 16 + l16) * ys + c0 + pt * 16 + g4) * ES, o);
+                    }
+                }
+            }
         } else {
 #pragma unroll
             for (int v = 0; v < 4 * PT; ++v) plane(0, v);
+            read_b(0);
+            read_b(1);
         }
         // the next state, a tile of rows at a time
-        const float gone = Pair<T>::decay(sCum[k][hw][Q - 1]);
-        auto read_b = [&](int u) { fb[u % 3] = cols_perm<TB>(sB, colsB, u / NT * 32, u % NT * 16); };
         auto scale = [&](int nt) {
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) S[pt][nt] *= gone;
         };
-        read_b(0);
-        read_b(1);
         scale(0);
         cb::sched_fence();
 #pragma unroll

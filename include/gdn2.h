@@ -385,10 +385,10 @@ gdn2_status_t gdn2_mixer_out(const void* o, const void* z, const float* gamma, v
  * Built for dk and dv of 64 or 128 each.  The strides are at least a token's
  * elements and below 2^22; x_stride, b_stride and c_stride are whole 16-byte
  * units; H is a multiple of G, and H * dv is below 2^22; B * H is below 2^23, T
- * at most 2^31 - 1025 (GDN2_ERR_SHAPE, or GDN2_ERR_MISALIGNED).  dt needs the alignment of its elements only.  Pairs of
- * tokens are formed in chunks of 64, with zeros for the pairs of a later token:
- * a NaN or an infinity in x, b, c or dt makes the outputs of its whole chunk
- * undefined, those of earlier tokens among them.
+ * at most 2^31 - 1025 (GDN2_ERR_SHAPE, or GDN2_ERR_MISALIGNED).  dt needs the
+ * alignment of its elements only.  A NaN or an infinity reaches no earlier token:
+ * in x its column of y and of the state from its token on, in c its token's y, in
+ * b and dt the y and states of their heads from their token on.
  * With workspace = NULL and workspace_bytes = 0 every sequence is walked whole.
  * With a workspace of gdn2_ssm_fwd_workspace_bytes bytes (256-byte aligned,
  * overlapping no argument) sequences are cut into segments that are walked in

@@ -339,3 +339,53 @@ def test_norm_gradients_stay_in_the_callers_workspace(dtype, rows, width):
     got = gdn2.layer_norm_bwd(dy, x, gamma, mean, rstd, workspace=ws)
     assert all(torch.equal(ref[n], got[n]) for n in ref)
     untouched()
+
+
+# ---- values that are not finite -------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,B,T,H,G,dk,dv", [
+    (BF16, 1, 150, 2, 1, 64, 64), (BF16, 1, 150, 2, 1, 128, 128), (BF16, 9, 150, 16, 2, 64, 128), (BF16, 16, 150, 32, 2, 128, 64),
+    (BF16, 1, 900, 2, 1, 128, 64), (F32, 1, 150, 2, 1, 64, 64), (F32, 9, 150, 16, 2, 128, 128), (F32, 16, 150, 32, 2, 64, 64)])
+def test_scan_of_values_that_are_not_finite_spares_earlier_tokens(dtype, B, T, H, G, dk, dv):
+    """The recurrence is causal, and the columns of x are independent: what is not finite reaches no
+    earlier token of its chunk, and of x no other column.  Bits, against the same call without it."""
+    k = scan_case(dtype, (B, T), H, G, dk, dv, 700 + T, B)
+    d = dev(k)
+    y0, s0 = gdn2.ssm_fwd(*args_of(d), d["D"], d["dt_bias"], d["s0"])
+    b, h = B - 1, H - 1
+    for t, value in ((0, "nan"), (5, "inf"), (17, "-inf"), (40, "nan"), (63, "inf"), (64, "nan"), (127, "inf"), (149, "nan")):
+        for name in TOKENS:
+            at = {"x": (b, t, h, 37), "dt": (b, t, h), "B": (b, t, G - 1, 3), "C": (b, t, G - 1, 3)}[name]
+            e = dict(d)
+            e[name] = d[name].clone()
+            e[name][at] = float(value)
+            y, s = gdn2.ssm_fwd(*args_of(e), d["D"], d["dt_bias"], d["s0"])
+            assert torch.equal(y[b, :t], y0[b, :t]), (name, t)
+            assert torch.equal(y[:b], y0[:b]) and torch.equal(s[:b], s0[:b]), (name, t)
+            heads = H // G if name in "BC" else 1  # that read it
+            assert torch.equal(y[b, :, :H - heads], y0[b, :, :H - heads]), (name, t)
+            if name == "x":
+                rest = torch.arange(dv, device="cuda") != 37
+                assert torch.equal(y[b, :, h][:, rest], y0[b, :, h][:, rest]) and torch.equal(s[b, h][:, rest], s0[b, h][:, rest]), t
+                assert not torch.isfinite(y[b, t:, h, 37]).any() and not torch.isfinite(s[b, h, :, 37]).any(), t
+            elif name == "C":
+                assert not torch.isfinite(y[b, t, h]).any() and torch.equal(s, s0), t
+                assert torch.equal(y[b, t + 1:], y0[b, t + 1:]), t
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_packed_scan_of_padding_that_is_not_finite(dtype):
+    """Padded rows taken as sequences: what lies behind a row's valid tokens, whatever it is, leaves
+    them alone."""
+    N, T, H, G, dk, dv = 3, 100, 2, 1, 64, 64
+    valid = [1, 37, 99]
+    k = scan_case(dtype, (N * T,), H, G, dk, dv, 720, N)
+    d = dev(k)
+    cu = torch.arange(N + 1, device="cuda") * T
+    y0, _ = gdn2.ssm_fwd_varlen(*args_of(d), cu, d["D"], d["dt_bias"], d["s0"])
+    for n, v in enumerate(valid):
+        for m in TOKENS:
+            d[m][n * T + v:(n + 1) * T] = float("nan" if n else "inf")
+    y, _ = gdn2.ssm_fwd_varlen(*args_of(d), cu, d["D"], d["dt_bias"], d["s0"])
+    for n, v in enumerate(valid):
+        assert torch.equal(y[n * T:n * T + v], y0[n * T:n * T + v]), n
