@@ -11,6 +11,7 @@ import torch
 
 import gated_delta_rule_gdn2_amd as gdn2
 from gated_delta_rule_gdn2_amd import block
+from oracle import block as O
 from tests.parity_util import say
 from tests.test_gpu_block import (BF16, F32, U, check_scan, conv_case, conv_ref, dev, f64, oracle_scan, packed_case, scan_case,
                                   within)
@@ -339,6 +340,51 @@ def test_norm_gradients_stay_in_the_callers_workspace(dtype, rows, width):
     got = gdn2.layer_norm_bwd(dy, x, gamma, mean, rstd, workspace=ws)
     assert all(torch.equal(ref[n], got[n]) for n in ref)
     untouched()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,width", [(1, 1), (4000, 130), (70, 1000), (1001, 1540), (1536, 2048), (300, 4096), (100, 8192),
+                                        (3, 16383)])
+def test_norm_within_the_roundings_of_its_sums(dtype, rows, width):
+    """Bars that count the roundings on the way of a row's sums: 8 elements of a lane (16 above 8192
+    columns), six steps over a wave, one a wave of the row, and two of the factor 1 / width; of the
+    sums over rows: the rows of a thread, those side by side in a workgroup, and the parts."""
+    say("case: norm roundings %s %d x %d" % (dtype, rows, width))
+    lanes = 16
+    while lanes < 1024 and width > lanes * 8:
+        lanes *= 2
+    a = (7 if width <= 8192 else 15) + 6 + lanes // 64 + 2
+    g = torch.Generator("cpu").manual_seed(rows + width)
+    x = (torch.randn(rows, width, generator=g) + torch.randn(rows, 1, generator=g)).to(dtype)
+    dy = torch.randn(rows, width, generator=g).to(dtype)
+    gamma, beta = torch.randn(width, generator=g), torch.randn(width, generator=g)
+    y, mean, rstd = gdn2.layer_norm(x.cuda(), gamma.cuda(), beta.cuda(), 1e-5)
+    xd, dyd, gd, bd = (f64(t) for t in (x, dy, gamma, beta))
+    yr, mr, rr = O.layer_norm(xd, gd, bd, 1e-5)
+    one = 1 + 2.0 ** -15  # the products of roundings
+    off = one * a * U * np.abs(xd).mean(-1)
+    var = 1 / rr ** 2 - 1e-5
+    rel = one * (0.5 * ((a + 4) * U * var + off ** 2 + U / rr ** 2) * rr ** 2 + 3 * U)
+    xh = (xd - mr[:, None]) * rr[:, None]
+    out = lambda v: 2.0 ** -8 * np.abs(v) if dtype == BF16 else 0
+    within("mean", mean, mr, off)
+    within("rstd", rstd, rr, rel * rr)
+    tol = np.abs(gd) * (rr * off * (1 + rel))[:, None] + np.abs(gd * xh) * (rel[:, None] + 3 * U) + U * (np.abs(yr) + np.abs(bd))
+    within("y", y, yr, one * tol + out(yr))
+
+    got = gdn2.layer_norm_bwd(dy.cuda(), x.cuda(), gamma.cuda(), mean, rstd)
+    m, r = f64(mean)[:, None], f64(rstd)[:, None]
+    dx, dg, db = O.layer_norm_bwd(dyd, xd, gd, m[:, 0], r[:, 0])
+    u, v = np.abs((xd - m) * r), np.abs(dyd * gd)
+    mv, muv = v.mean(-1, keepdims=True), (u * v).mean(-1, keepdims=True)
+    tol = r * U * ((a + 1) * mv + (a + 4) * u * muv + 5 * (v + mv + u * muv))
+    within("dx", got["dx"], dx, one * tol + out(dx))
+    side = max(1, 256 // lanes)  # rows of a workgroup at once
+    groups = -(-rows // side)
+    groups = 1 if groups <= 8 else min(groups, 512 if lanes == 1024 else 393216 // max(256, lanes))
+    n = -(-rows // (groups * side)) + side + -(-groups // 32) + 5
+    within("dgamma", got["dgamma"], dg, one * (n + 4) * U * (np.abs(dyd) * u).sum(0))
+    within("dbeta", got["dbeta"], db, one * n * U * np.abs(dyd).sum(0))
 
 
 # ---- values that are not finite -------------------------------------------------------------
