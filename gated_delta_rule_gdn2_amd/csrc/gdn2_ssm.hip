@@ -311,20 +311,22 @@ __device__ __forceinline__ void bstore4(__amdgpu_buffer_rsrc_t r, int off, const
 // at one tile took as long as the products.  The next chunk's inputs are loaded into registers
 // meanwhile, through buffer resources that end with the sequence: rows behind it read as zeros, and
 // their y is dropped.
-// Bound by issue.  A wave's chunk (dk = 128, 32 columns) is 152 matrix instructions of 16 cycles, 96
-// of them the state's three planes, and 715 vector ones, which hardly run beside the other wave's on
-// its SIMD.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 137 us of this pass (matrix 30% and
-// vector 35% of the cycles, LDS 25%) and 64 of the pass for ENDS under a profiler, 172 in all
-// without one (1.7 TB/s; the inputs and outputs alone would take 61).  Eight waves a workgroup
-// spilled (269); 64 columns a workgroup repeat c . b and M (195; they are for calls that leave
-// compute units idle); with 64 columns and four more waves that only load and form M, one barrier a
-// chunk, this pass took 171 and ENDS 55.
+// A wave's chunk (dk = 128, 32 columns) is 152 matrix instructions of 16 cycles, 96 of them the
+// state's three planes, and 743 vector ones.  8 x 4096 tokens of 16 heads of 128 x 128 in bf16: 138 us
+// of this pass and 63 of the pass for ENDS under a profiler, 175 in all without one (1.7 TB/s; the
+// inputs and outputs alone would take 61).  No unit is full: matrix 27% and vector 33% of the cycles,
+// LDS 20%.  Two waves a SIMD, which is what the registers allow, wait to issue 38% of their cycles and
+// for data and the three barriers of a chunk 22%.  Eight waves a workgroup spilled (269); 64 columns a
+// workgroup repeat c . b and M (195; they are for calls that leave compute units idle); with 64
+// columns and four more waves that only load and form M, one barrier a chunk, this pass took 171 and
+// ENDS 55.
 // ENDS: the state alone, from zero, over each of a sequence's segments but the last; it goes to
 // the next segment's place in `starts`, the segment's decay to `logs`.
 constexpr int NW = 4;
 // A sequence of up to so many segments needs no join: each segment reads the ends before it and forms
-// its own start.  That is more to read with each segment (4 of 8 x 4096 tokens: 171 us without the
-// join, 176 with it; 6 of 2 x 333 tokens: 27 and 30; 32 of one of 32768: 214 and 182).
+// its own start.  That is more to read with each segment (4 of 8 x 4096 tokens: 183 us without the
+// join, 187 with it; 6 of 2 x 333 tokens in fp32: 15 and 17; 32 of one of 32768: 216 and 190; on the
+// GPU alone, as the figures of the plans below).
 constexpr int kFew = 6;
 template <typename T, int DK, int DV, int CW, bool ENDS>
 __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void chunk_kernel(Params a) {
@@ -547,6 +549,9 @@ __global__ __launch_bounds__(64 * NW, (sizeof(T) == 2 ? NW / 2 : NW / 4)) void c
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 if (s + 1 < KS) read_c(s + 1);
+                // In bf16 one plane of S here, and of M below: with both y is off by 5e-4 of its size (RMS)
+                // before its own rounding, which is 17e-4.  Two planes would be 44 matrix instructions
+                // more of 152.  S itself keeps fp32.
                 Frag<T> fs[PT];
 #pragma unroll
                 for (int pt = 0; pt < PT; ++pt) fs[pt] = frag_from_acc<T>(S[pt][2 * s], S[pt][2 * s + 1]);
@@ -913,10 +918,10 @@ struct Plan {
 // Sequences of one length.  A chunk's time is the unit.  A compute unit runs two workgroups (of 128
 // state columns) at once, each then 1.36 times as long as one alone; halves of heads take 0.65 of it;
 // the pass for the segments' ends takes half a chunk's time a chunk; launches, the states' way through
-// HBM and the join, which walks the segments, are the rest.  Fitted to calls in us, the chosen one
-// first: 128 sequence-heads of 64 chunks in 4 / 1 / 2 / 3 / 8 segments 170 / 242 / 192 / 180 / 193; 16 of
-// 512 in 32 / 16 / 48 176 / 200 / 192; before the halves 8 of 32 in 16 / 8 / 32 31 / 37 / 36, with them
-// 27; fp32, whose chunks take three times as long, 18 of 11 in 6 39.
+// HBM and the join, which walks the segments, are the rest.  Fitted to calls; now in us, the chosen one
+// first: 128 sequence-heads of 64 chunks in 4 / 1 (halves) / 2 / 3 / 8 segments 183 / 201 / 208 / 182 /
+// 197; 16 of 512 in 32 / 16 / 48 190 / 219 / 189; 8 of 32 in 16 / 8 / 32 26 / 29 / 36, in whole heads 31 /
+// 37 / 36; fp32, whose chunks take three times as long, 18 of 11 in 6 / 3 / 11 39 / 56 / 44.
 Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf16_in, int64_t cus) {
     Plan p{};
     const int64_t nc = (T + Q - 1) / Q, heads = N * H;
@@ -952,8 +957,8 @@ Plan plan_fixed(int64_t N, int64_t T, int64_t H, int64_t dk, int64_t dv, bool bf
 // slot of the GPU has of all, or two thirds of it where there are sequences enough to fill the slots
 // (then only the longest are cut, and the launch does not wait for their chains alone); at least
 // four, in fp32, whose chunks outweigh a segment's costs, two.  In us, segments of the rule / half as
-// long / whole sequences: 16 prompts of about 700 tokens, 16 heads 136 / 149 / 243; 64 of 512, 32 heads
-// of 64 columns 266 / 307 / 326; 8 of 300, 6 heads in fp32 37 / - / 206 (segments of four 47).
+// long / whole sequences: 16 prompts of about 700 tokens, 16 heads 148 / 153 / 247; 64 of 512, 32 heads
+// of 64 columns 279 / 301 / 333; 8 of 300, 6 heads in fp32 36 / - / 206 (segments of four 47).
 Plan plan_packed(int64_t N, int64_t total, int64_t H, int64_t dk, int64_t dv, bool bf16_in, int64_t cus) {
     Plan p{};
     p.segs = 1;
@@ -1021,7 +1026,7 @@ template <typename T, int DK>
 hipError_t launch_dk(const SsmArgs& a, const Plan& plan, void* ws) {
     const int64_t heads = (plan.pieces ? plan.pieces : a.N * (plan.total ? plan.segs : 1)) * a.H;
     // Heads of 128 columns go to two workgroups each while every one then has a compute unit of its own
-    // (8 heads of 300 tokens 14 us, whole 19; 160 heads of 128 in fp32, which have not, 44 and 35).
+    // (8 heads of 300 tokens 17 us, whole 23; 160 heads of 128 in fp32, which have not, 44 and 36).
     if (a.dv == 128)
         return 2 * heads <= a.cus ? launch_chunks<T, DK, 128, 64>(a, plan, ws) : launch_chunks<T, DK, 128, 128>(a, plan, ws);
     // Two heads of 64 a workgroup where a group has an even number of them and pairs still fill the
