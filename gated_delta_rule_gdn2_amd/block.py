@@ -14,7 +14,10 @@ Layouts: x, y [B,T,H,dv]; dt [B,T,H]; B, C [B,T,G,dk]; A, D, dt_bias [H] fp32; s
 Convolution: x, y [B,T,C], taps [C,4] and bias [C] fp32, the inputs kept [B,3,C] in x's dtype.
 Norm: x, y [...,width], gamma, beta [width] and mean, rstd [...] fp32.  Everything else is bf16
 or fp32, one dtype in a call.  x, dt, B and C may be parts of one wider tensor (a token stride of
-their own, a token's elements contiguous); all other tensors are contiguous.
+their own, a token's elements contiguous); all other tensors are contiguous.  Addresses are 16-byte aligned
+(dt's and the convolution's x to their elements), token strides of x, B and C whole 16-byte units in
+the scan and its step, below 2^22 elements for prompts and 2^31 for steps; C of the convolution is a
+multiple of 8.  The library's refusals of other calls are Gdn2Error.
 """
 from __future__ import annotations
 
