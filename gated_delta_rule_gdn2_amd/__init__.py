@@ -14,7 +14,8 @@ the computation runs in the library's HIP kernels; there is no fallback.
     y      = mixer_out(o, z, gamma)                            # RMS norm and SiLU output gate
 
 The calls of a state space block beside it (its scan, short convolution and layer norm) are
-listed in ``block``, and imported here.
+listed in ``block``, those of an attention block (attention, rotary positions and the
+root-mean-square norm) in ``attention``; both are imported here.
 
 Layouts: q, k, b, log_alpha [B,T,H,dk]; v, w, o [B,T,H,dv]; state [B,H,dk,dv]
 (packed: [total_T,H,d] with int64 offsets cu_seqlens [N+1] and states [N,H,dk,dv];
@@ -89,6 +90,7 @@ def _load():
         lib.gdn2_mixer_out.argtypes = [P] * 4 + [I64] * 4 + [ctypes.c_float, I32, I32, P]
         lib.gdn2_mixer_out.restype = I32
         block._declare(lib)
+        attention._declare(lib)
         lib.gdn2_supported.argtypes = [I32, I64, I64, I32]
         lib.gdn2_supported.restype = I32
         lib.gdn2_status_string.argtypes = [I32]
@@ -103,7 +105,7 @@ def version() -> str:
 
 
 def supported(which: str, dk: int, dv: int, dtype: torch.dtype) -> bool:
-    w = {"chunk_fwd": 0, "decode_step": 1, "chunk_bwd": 2, "mixer": 3, "ssm": 5}[which]
+    w = {"chunk_fwd": 0, "decode_step": 1, "chunk_bwd": 2, "mixer": 3, "ssm": 5, "attn": 6}[which]
     return bool(_load().gdn2_supported(w, dk, dv, _DTYPES[dtype]))
 
 
@@ -450,4 +452,7 @@ def mixer_out(o, z, gamma, eps=1e-6, *, y=None):
 from . import block  # noqa: E402  (it uses the helpers above)
 from .block import *  # noqa: E402,F401,F403
 
-__all__ += block.__all__
+from . import attention  # noqa: E402
+from .attention import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__ + attention.__all__

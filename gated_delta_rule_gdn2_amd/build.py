@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libgdn2.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 SOURCES = ["gdn2_api.hip", "gdn2_chunk_fwd.hip", "gdn2_chunk_bf16.hip", "gdn2_chunk_split.hip", "gdn2_chunk_bwd.hip", "gdn2_decode.hip", "gdn2_mixer.hip",
-           "gdn2_api_block.hip", "gdn2_ssm.hip", "gdn2_conv.hip", "gdn2_norm.hip"]
+           "gdn2_api_block.hip", "gdn2_ssm.hip", "gdn2_conv.hip", "gdn2_norm.hip",
+           "gdn2_api_attn.hip", "gdn2_attn_fwd.hip", "gdn2_attn_bwd.hip", "gdn2_attn_step.hip", "gdn2_rotary.hip", "gdn2_rms.hip"]
 ARCH = "gfx950"
 
 COMMON = [

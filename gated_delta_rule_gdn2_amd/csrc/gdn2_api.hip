@@ -428,6 +428,7 @@ gdn2_status_t gdn2_mixer_out(const void* o, const void* z, const float* gamma, v
 int gdn2_supported(int which, int64_t dk, int64_t dv, gdn2_dtype_t dtype) {
     if (which == 3) return mixer_supported(dk, dv, dtype) ? 1 : 0;
     if (which == 5) return gdn2::ssm_supported(dk, dv, dtype == GDN2_DTYPE_BF16, dtype == GDN2_DTYPE_F32) ? 1 : 0;
+    if (which == 6) return gdn2::attn_supported(dk) && dk == dv && (dtype == GDN2_DTYPE_BF16 || dtype == GDN2_DTYPE_F32) ? 1 : 0;
     if (which == 0 || which == 2) return chunk_supported(dk, dv, dtype) ? 1 : 0;
     if (which == 1) return decode_supported(dk, dv, dtype) ? 1 : 0;
     return 0;

@@ -1,0 +1,421 @@
+// gdn2_attn.h -- device-side building blocks of the attention kernels.
+//
+// Products are 32 x 32 tiles (v_mfma_f32_32x32x16_bf16, or v_mfma_f32_32x32x2_f32 for fp32 inputs)
+// with fp32 accumulators.  An operand holds 16 contraction slots, 8 a lane: lane l covers row or
+// column l % 32 and the slots (g, e), g = l / 32, e = 0 .. 7, in one of two maps:
+//   contiguous: slot (g, e) -> 8 g + e
+//   permuted:   slot (g, e) -> 8 (e / 4) + 4 g + e % 4
+// An accumulator keeps rows 8 (i / 4) + 4 g + i % 4 of column l % 32 in its 16 registers i, so its
+// registers 0 .. 7 and 8 .. 15 are two operands in the permuted map as they stand.  Scores are
+// therefore formed with the axis that the next product sums over in the rows, and go from one
+// product into the next without leaving the registers.
+#pragma once
+
+#include "gdn2_device.h"
+#include "gdn2_launch.h"
+
+namespace gdn2 {
+namespace attn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+#define GDN2_LDS __attribute__((address_space(3)))
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <typename T> struct Op;
+template <> struct Op<bf16> { bf16x8 v; };
+template <> struct Op<float> { float v[8]; };
+
+__device__ __forceinline__ void mma(f32x16& c, const Op<bf16>& a, const Op<bf16>& b) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x16& c, const Op<float>& a, const Op<float>& b) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[e], b.v[e], c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    return z;
+}
+// registers 8 h .. 8 h + 7 of an accumulator as an operand in the permuted map
+template <typename T> __device__ __forceinline__ Op<T> op_of(const f32x16& c, int h) {
+    Op<T> r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(c[8 * h + e]);
+    return r;
+}
+// the row of an accumulator's register i
+__device__ __forceinline__ int acc_row(int i, int g) { return 8 * (i / 4) + 4 * g + i % 4; }
+
+// An address in LDS, as the number it is.  Bytes are addressed by a lane's own base and constants:
+// the base goes through `opaque` once a tile, or the compiler keeps every sum of the two in a register
+// of its own through the loop.
+typedef uint32_t Lds;
+__device__ __forceinline__ Lds lds_of(const void* p) { return (Lds)(uintptr_t)(GDN2_LDS const char*)p; }
+template <typename V> __device__ __forceinline__ V lds_get(Lds at) { return *(GDN2_LDS const V*)(uintptr_t)at; }
+__device__ __forceinline__ Lds opaque(Lds x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// A buffer resource's words (uniform): loads beyond `bytes` give zeros.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 rsrc_words(const void* p, uint32_t bytes) {
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+// 16 bytes a lane from `off` behind the resource's base to LDS, lane after lane from `to` (uniform) on.
+// In assembly because the compiler takes every read of LDS for one of what such a load writes, and
+// waits for it; the waits are tile_barrier's.  The load has no result registers, and nothing else here
+// uses m0.
+__device__ __forceinline__ void load_to_lds(Lds to, u32x4 r, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "memory");
+}
+
+// the same, 4 bytes a lane
+__device__ __forceinline__ void load_words_to_lds(Lds to, u32x4 r, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "memory");
+}
+
+// 16 bytes a lane from each lane's own address
+__device__ __forceinline__ void load_far_to_lds(Lds to, const void* from) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+
+// A tile of rows of D elements in LDS, filled by loads that go there directly; it begins at a multiple
+// of 1024 bytes.  Rows lie one behind the other without padding (such a load writes 64 lanes' 16-byte
+// units in lane order), so each row's units are permuted by an exclusive or: with it the lanes of a
+// row-wise read take different rows' units from different banks, and so do the 4 rows of a transposing
+// read.
+template <typename T, int D> struct Tile {
+    static constexpr int kRow = D * (int)sizeof(T), kUnits = kRow / 16;
+    __device__ static constexpr int swz(int row) {
+        return (kUnits >= 16 ? ((row >> 3) & 1) << 3 : 0) | ((row & 3) << 1) | ((row >> 2) & 1);
+    }
+    // ROWS rows from memory, rows behind `bytes` as zeros; the waves of a workgroup share them
+    template <int ROWS, int NW>
+    __device__ static __forceinline__ void stage(Lds lds, const void* src, uint32_t bytes, uint32_t stride, int wave,
+                                                 int lane) {
+        const u32x4 r = rsrc_words(src, bytes);
+        constexpr int kLoads = ROWS * kUnits / 64;
+        static_assert(ROWS * kUnits % 64 == 0 && kLoads % NW == 0, "whole loads for each wave");
+#pragma unroll
+        for (int i = 0; i < kLoads / NW; ++i) {
+            const int u = (i * NW + wave) * 64 + lane, row = u / kUnits;
+            const uint32_t off = (uint32_t)row * stride + (((u % kUnits) ^ swz(row)) << 4);
+            load_to_lds(lds + (i * NW + wave) * 1024, r, off);
+        }
+    }
+    // operand of row row0 + l % 32 (row0 a multiple of 16), columns 16 ks + slot in the contiguous map;
+    // base: row_base plus the tile's address
+    __device__ static __forceinline__ Lds row_base(int lane) {
+        const int row = lane & 31, g = lane >> 5;
+        return row * kRow + (((sizeof(T) == 2 ? g : 2 * g) ^ swz(row)) << 4);
+    }
+    __device__ static __forceinline__ Op<T> row_op(Lds base, int row0, int ks) {
+        Op<T> r;
+        if constexpr (sizeof(T) == 2) {
+            r.v = lds_get<bf16x8>((base ^ (ks << 5)) + row0 * kRow);
+        } else {
+            const f32x4 lo = lds_get<f32x4>((base ^ (ks << 6)) + row0 * kRow);
+            const f32x4 hi = lds_get<f32x4>((base ^ (ks << 6) ^ 16) + row0 * kRow);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { r.v[e] = lo[e]; r.v[e + 4] = hi[e]; }
+        }
+        return r;
+    }
+    // operand of column 32 dt + l % 32, rows row0 + slot (row0 a multiple of 16) in the permuted map;
+    // base: col_base plus the tile's address
+    __device__ static __forceinline__ Lds col_base(int lane) {
+        const int g = lane >> 5;
+        if constexpr (sizeof(T) == 2) {
+            // a transposing read: 16 lanes give 4 rows of 16 columns and get a column's 4 rows each
+            const int j = lane & 15, row = 4 * g + (j >> 2), unit = 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+            return row * kRow + ((unit ^ swz(row)) << 4) + ((j & 1) << 3);
+        } else {
+            const int c = lane & 31;
+            return 4 * g * kRow + (((c >> 2) ^ swz(4 * g)) << 4) + (c & 3) * 4;
+        }
+    }
+    __device__ static __forceinline__ Op<T> col_op(Lds base, int row0, int dt) {
+        Op<T> r;
+        if constexpr (sizeof(T) == 2) {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            bf16x4 h[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                h[k] = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((GDN2_LDS s16x4*)(uintptr_t)(
+                                                      (base ^ (4 * dt << 4) ^ (swz(8 * k) << 4)) + (row0 + 8 * k) * kRow)));
+            r.v = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int row = 8 * (e / 4) + e % 4;
+                r.v[e] = lds_get<float>((base ^ (8 * dt << 4) ^ (swz(row) << 4)) + (row0 + row) * kRow);
+            }
+        }
+        return r;
+    }
+};
+
+// operand of a row in memory, columns 16 ks + slot in the contiguous map; rows behind `bytes` as zeros
+template <typename T>
+__device__ __forceinline__ Op<T> global_op(__amdgpu_buffer_rsrc_t r, uint32_t row_off, int ks, int g) {
+    Op<T> o;
+    const uint32_t off = row_off + (16 * ks + 8 * g) * (uint32_t)sizeof(T);
+    if constexpr (sizeof(T) == 2) {
+        o.v = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    } else {
+        const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { o.v[e] = lo[e]; o.v[e + 4] = hi[e]; }
+    }
+    return o;
+}
+
+// bytes from the first of `rows` rows to the end of the last's `width` bytes (0 for none)
+__device__ __forceinline__ uint32_t span(int rows, uint32_t stride, uint32_t width) {
+    return rows > 0 ? (uint32_t)(rows - 1) * stride + width : 0u;
+}
+
+// 4 consecutive columns of each 8 of an accumulator's column: a lane's part of a row of D elements
+template <typename T, int D>
+__device__ __forceinline__ void store_column(T* row, const f32x16 (&c)[D / 32], float factor, int g) {
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = c[dt][4 * q + e] * factor;
+            store_vec_any<T, 4>(row + 32 * dt + 8 * q + 4 * g, f);
+        }
+}
+
+// v of the lane 32 away: the other half of an accumulator's column
+__device__ __forceinline__ float other_half(float v, int lane) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v), __builtin_bit_cast(unsigned, v), false, false);
+    return __builtin_bit_cast(float, lane < 32 ? r[1] : r[0]);
+}
+
+// loads that go to LDS directly have arrived, and every wave is here
+__device__ __forceinline__ void tile_barrier() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __syncthreads();
+}
+
+// ---- values that are not finite -------------------------------------------------------------
+// A product over a tile's rows multiplies what a mask hides by zero, which an infinity or a NaN there
+// survives.  Tiles that a mask cuts are therefore searched.  Where something is found, a product with
+// the mask itself says which infinities and NaN each column sees, and the tile is cleared of them
+// before the product with the weights.
+
+__device__ __forceinline__ bool finite_bits(bf16 x) { return (__builtin_bit_cast(unsigned short, x) & 0x7f80u) != 0x7f80u; }
+__device__ __forceinline__ bool finite_bits(float x) { return (__builtin_bit_cast(unsigned, x) & 0x7f800000u) != 0x7f800000u; }
+
+// whether this thread's part of a tile of BYTES bytes holds a value that is not finite
+template <typename T, int BYTES, int NT>
+__device__ __forceinline__ bool any_special(Lds lds, int tid) {
+    constexpr unsigned kMask = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
+    bool found = false;
+    for (int u = tid; u < BYTES / 16; u += NT) {
+        const u32x4 x = lds_get<u32x4>(lds + u * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned m = x[e] & kMask;
+            if (sizeof(T) == 2)
+                found |= (m & 0xffffu) == (kMask & 0xffffu) || (m >> 16) == (kMask >> 16);
+            else
+                found |= m == kMask;
+        }
+    }
+    return found;
+}
+// the thread's part of the tile with zeros for what is not finite
+template <typename T, int BYTES, int NT>
+__device__ __forceinline__ void clear_special(Lds lds, int tid) {
+    for (int u = tid; u < BYTES / (int)sizeof(T); u += NT) {
+        GDN2_LDS T* x = (GDN2_LDS T*)(uintptr_t)(lds + u * (int)sizeof(T));
+        if (!finite_bits((T)*x)) *x = from_f32<T>(0.f);
+    }
+}
+// 1 for a NaN, 128 for an infinity, 16384 for a negative one: sums over up to 64 rows keep the three
+// counts apart, and are exact
+template <typename T> __device__ __forceinline__ Op<T> special_code(const Op<T>& a) {
+    Op<T> r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float f = to_f32((T)a.v[e]);
+        const bool special = !finite_bits((T)a.v[e]);
+        r.v[e] = from_f32<T>(!special ? 0.f : f != f ? 1.f : f > 0.f ? 128.f : 16384.f);
+    }
+    return r;
+}
+__device__ __forceinline__ float from_code(float c) {
+    const float neg = floorf(c * (1.f / 16384.f)), rest = c - neg * 16384.f, pos = floorf(rest * (1.f / 128.f));
+    const bool nan = rest - pos * 128.f > 0.f || (neg > 0.f && pos > 0.f);
+    return nan ? __builtin_nanf("") : pos > 0.f ? __builtin_inff() : neg > 0.f ? -__builtin_inff() : 0.f;
+}
+
+// Which rows of a tile a lane's column has to do with: n of them from lo on.
+struct Seen {
+    int lo;
+    unsigned n;
+    __device__ __forceinline__ bool operator()(int row) const { return (unsigned)(row - lo) < n; }
+};
+__device__ __forceinline__ Seen seen_between(int lo, int hi) { return Seen{lo, hi < lo ? 0u : (unsigned)(hi - lo) + 1u}; }
+
+// What is not finite in column 32 dt + register's row of the tile's rows that a lane's column sees:
+// zero, an infinity or a NaN to add (`nan`: a NaN for infinities too, where weights may be zero).  A
+// call of its own, through memory, so that the loop around it keeps its registers.
+template <typename T, int D, int ROWS>
+__device__ __attribute__((noinline)) void special_sums(f32x16* out, Lds base, Seen seen, int g, bool nan) {
+    typedef Tile<T, D> L;
+    static_assert(ROWS <= 64, "counts below 128");
+    for (int dt = 0; dt < D / 32; ++dt) {
+        f32x16 code = zero16();
+        for (int ks = 0; ks < ROWS / 16; ++ks) {
+            Op<T> see;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) see.v[e] = from_f32<T>(seen(16 * ks + acc_row(e, g)) ? 1.f : 0.f);
+            mma(code, special_code<T>(L::col_op(base, 16 * ks, dt)), see);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) code[i] = nan && code[i] > 0.f ? __builtin_nanf("") : from_code(code[i]);
+        out[dt] = code;
+    }
+}
+
+// ---- which workgroup does what --------------------------------------------------------------
+
+struct Seq {
+    int64_t q0, k0;  // first token of the sequence's queries and keys
+    int lq, lk;      // how many there are
+};
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Blocks of `rows` tokens of the packed sequences, counted through: sequence and block of the
+// `index`th one, or false behind the last.  Every wave looks for itself, 64 sequences at a time.
+__device__ __forceinline__ bool find_block(const int64_t* cu, int64_t n, int64_t total, int rows, int64_t index, int lane,
+                                           int64_t* seq, int* block) {
+    int64_t before = 0;
+    for (int64_t base = 0; base < n; base += 64) {
+        int64_t mine = 0;
+        if (base + lane < n) {
+            const int64_t lo = clamp64(cu[base + lane], 0, total), hi = clamp64(cu[base + lane + 1], lo, total);
+            mine = (hi - lo + rows - 1) / rows;
+        }
+        int64_t sum = mine;
+#pragma unroll
+        for (int s = 1; s < 64; s *= 2) {
+            const int64_t up = __shfl_up(sum, s);
+            if (lane >= s) sum += up;
+        }
+        const uint64_t here = __ballot(before + sum > index);
+        if (here) {
+            const int at = __builtin_ctzll(here);
+            *seq = base + at;
+            *block = (int)(index - before - __shfl(sum - mine, at));
+            return true;
+        }
+        before += __shfl(sum, 63);
+    }
+    return false;
+}
+__device__ __forceinline__ Seq packed_seq(const int64_t* cu_q, const int64_t* cu_k, int64_t n, int64_t total_q, int64_t total_k) {
+    Seq s;
+    s.q0 = clamp64(cu_q[n], 0, total_q);
+    s.lq = (int)(clamp64(cu_q[n + 1], s.q0, total_q) - s.q0);
+    s.k0 = clamp64(cu_k[n], 0, total_k);
+    s.lk = (int)(clamp64(cu_k[n + 1], s.k0, total_k) - s.k0);
+    return s;
+}
+
+// What every attention kernel takes.
+struct Shape {
+    const int64_t* cu_q;  // packed sequences' offsets, or nullptr
+    const int64_t* cu_k;
+    int64_t n, tq, tk;    // sequences; tokens of each, or of all packed ones
+    int heads, groups, window;
+    uint32_t q_stride, k_stride, v_stride;  // bytes between tokens
+    float scale, scale_log2;                // scale, and scale log2(e)
+    int blocks;           // blocks of a head: of every sequence's, or of all packed ones
+    int slices;           // parts that a group's blocks are dealt out in, so that every XCD has as many
+};
+
+// Workgroups go to the 8 XCDs in turn, each with an L2 of its own: the blocks of one group (a
+// sequence's key head; packed, a key head) stay on one XCD, or with fewer groups than XCDs are dealt
+// out in `slices`.  Within a slice the blocks with the most work come first, the heads of the group
+// side by side.
+struct Work {
+    Seq s;
+    int block, head;  // head: of `per_group` in each group
+};
+__host__ __device__ inline int64_t groups_of(const Shape& p) { return p.cu_q ? p.groups : p.n * p.groups; }
+__device__ __forceinline__ bool find_work(const Shape& p, int rows, int per_group, bool last_first, bool keys, int lane, Work* w) {
+    const unsigned x = blockIdx.x & 7, r = blockIdx.x >> 3;
+    const unsigned per = (p.blocks + p.slices - 1) / p.slices, each = per * per_group;
+    const int64_t slice = (int64_t)(r / each) * 8 + x, group = slice / p.slices;
+    const unsigned in = r % each, nth = in / per_group;
+    const int64_t index = (int64_t)p.slices * (last_first ? per - 1 - nth : nth) + slice % p.slices;
+    if (group >= groups_of(p) || index >= p.blocks) return false;
+    w->head = (int)(group % p.groups) * per_group + in % per_group;
+    if (p.cu_q) {
+        int64_t seq;
+        if (!find_block(keys ? p.cu_k : p.cu_q, p.n, keys ? p.tk : p.tq, rows, index, lane, &seq, &w->block)) return false;
+        w->s = packed_seq(p.cu_q, p.cu_k, seq, p.tq, p.tk);
+    } else {
+        const int64_t n = group / p.groups;
+        w->s = Seq{n * p.tq, n * p.tk, (int)p.tq, (int)p.tk};
+        w->block = (int)index;
+    }
+    return true;
+}
+// the same in every lane: in scalar registers
+__device__ __forceinline__ Work uniform(const Work& w) {
+    return Work{Seq{uniform(w.s.q0), uniform(w.s.k0), uniform(w.s.lq), uniform(w.s.lk)}, uniform(w.block), uniform(w.head)};
+}
+constexpr int64_t kMaxGrid = (int64_t)1 << 23;  // workgroups of up to 512 threads: a launch has less than 2^32
+// fills in blocks and slices; workgroups of the launch (0: none), or -1 if they are too many
+inline int64_t deal(Shape* p, int64_t tokens, int rows, int per_group) {
+    const int64_t blocks = p->cu_q ? tokens / rows + p->n : (tokens + rows - 1) / rows, groups = groups_of(*p);
+    if (blocks > INT32_MAX || groups > (int64_t)1 << 40) return -1;
+    p->blocks = (int)blocks;
+    p->slices = 1;
+    while (groups * p->slices % 8) p->slices *= 2;
+    const int64_t per = (blocks + p->slices - 1) / p->slices;
+    if (per * per_group > INT32_MAX || groups * p->slices > INT32_MAX) return -1;
+    const int64_t grid = groups * p->slices * per * per_group;
+    return grid < kMaxGrid ? grid : -1;
+}
+
+// Rows whose keys were taken in parts: unnormalised sums o [splits][rows][d] in fp32, and of each row
+// and part the reference (base 2) and the sum (ml).  lse may be nullptr.
+struct Parts {
+    float* o;
+    float2* ml;
+    int64_t rows;
+    int splits;
+};
+inline size_t parts_bytes(int64_t rows, int64_t d, int splits) { return (size_t)splits * (size_t)rows * (size_t)(d + 2) * 4; }
+inline Parts parts_in(void* workspace, int64_t rows, int64_t d, int splits) {
+    float* o = static_cast<float*>(workspace);
+    return Parts{o, reinterpret_cast<float2*>(o + splits * rows * d), rows, splits};
+}
+// the tokens that rows belong to, `heads` rows each: all (no offsets), or those of packed sequences
+struct Owned {
+    const int64_t* cu;
+    int64_t n, total;
+    int heads;
+};
+hipError_t launch_join(const Parts& p, void* o, float* lse, int64_t d, bool bf16_out, const Owned& owned, hipStream_t stream);
+
+}  // namespace attn
+}  // namespace gdn2

@@ -1,0 +1,308 @@
+// gdn2_attn_fwd.hip -- causal attention with shared key heads and an optional window, forward.
+//
+//   s_ij = scale q_i . k_j for the keys j that query i sees: j <= p_i and j > p_i - window, where
+//   query i of lq stands at p_i = lk - lq + i of its sequence's lk keys;
+//   o_i = sum_j e^(s_ij - m) v_j / l,  l = sum_j e^(s_ij - m),  lse_i = m + log l.
+//
+// One pass over the keys with the running maximum m and sum l.  A workgroup takes 32 queries a wave
+// of one head; tiles of keys and values go from memory to LDS directly, one tile ahead of the
+// products.  A wave forms S^T = K Q^T, so that a lane holds scores of one query (its column): the
+// maximum and the sum are reductions within a lane and with the lane 32 away, and the probabilities
+// are the next product's operand (O^T = V^T P^T) as they stand.  S, m, l and O are fp32; with bf16
+// inputs a probability is rounded to bf16 once (the matrix unit's operand), the sum l takes it
+// unrounded, and o is rounded on the store.
+#include "gdn2_attn.h"
+
+namespace gdn2 {
+namespace attn {
+
+// keys in a tile
+template <typename T> constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
+// A row's maximum may lie up to this (in base 2) above the reference that its sums are formed with
+// before they are rescaled: probabilities stay below 2^8, and most tiles need no rescaling.
+constexpr float kSlack = 8.f;
+
+struct FwdParams {
+    const char* q;
+    const char* k;
+    const char* v;
+    void* o;
+    float* lse;
+    Parts parts;  // of more than one split, or unused
+    Shape p;
+};
+
+template <typename T, int D, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void fwd_kernel(FwdParams a) {
+    typedef Tile<T, D> L;
+    constexpr int BK = kKeys<T>, KS = D / 16, DT = D / 32, BM = NW * 32, BYTES = BK * L::kRow;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * BYTES];
+    __shared__ int special;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Shape& p = a.p;
+    Work w;
+    if (!find_work(p, BM, p.heads / p.groups, true, false, lane, &w)) return;
+    w = uniform(w);
+    const int head = w.head, kv = head / (p.heads / p.groups), lq = w.s.lq, lk = w.s.lk;
+    const char* k = a.k + w.s.k0 * p.k_stride + (int64_t)kv * L::kRow;
+    const char* v = a.v + w.s.k0 * p.v_stride + (int64_t)kv * L::kRow;
+    const int first = w.block * BM, off = lk - lq;  // the block's first query; where query 0 stands
+
+    // the tiles that some query of the block sees
+    const int64_t low = (int64_t)off + first, high = off + (int64_t)min(first + BM, lq) - 1;
+    const int64_t from = low - p.window + 1;
+    int t0 = from > 0 ? (int)(from / BK) : 0;
+    const int all = high >= 0 ? (int)(high / BK) + 1 : 0;
+    // and those of the workgroup's part of them
+    const int per = (max(all - t0, 0) + (int)gridDim.y - 1) / (int)gridDim.y;
+    t0 = min(t0 + per * (int)blockIdx.y, all);
+    const int t1 = min(t0 + per, all);
+
+    // the wave's queries; a lane's own is column l % 32
+    const int mine = first + wave * 32, rows = min(32, lq - mine);
+    const int64_t pos0 = (int64_t)off + mine;
+    const int pos = (int)(pos0 + (lane & 31));
+    Op<T> q[KS];
+    {
+        const auto r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char*>(a.q + (w.s.q0 + mine) * p.q_stride + (int64_t)head * L::kRow), 0,
+            span(rows, p.q_stride, L::kRow), 0x00020000);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[ks] = global_op<T>(r, (lane & 31) * p.q_stride, ks, g);
+    }
+    f32x16 o[DT];
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) o[dt] = zero16();
+    float m = -__builtin_inff(), l = 0.f;  // the reference (base 2) and the lane's part of the sum
+
+    const Lds base = lds_of(lds);
+    auto stage = [&](int t) {
+        const Lds to = base + (t & 1) * 2 * BYTES;
+        const int left = min(BK, lk - t * BK);
+        L::template stage<BK, NW>(to, k + (int64_t)t * BK * p.k_stride, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
+        L::template stage<BK, NW>(to + BYTES, v + (int64_t)t * BK * p.v_stride, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
+    };
+    const Lds row_base = L::row_base(lane), col_base = L::col_base(lane);
+    if (tid == 0) special = -1;
+    if (t0 < t1) stage(t0);
+    for (int t = t0; t < t1; ++t) {
+        tile_barrier();
+        if (t + 1 < t1) stage(t + 1);
+        const Lds tk = base + (t & 1) * 2 * BYTES, tv = tk + BYTES;
+        const Lds rb = opaque(row_base + tk);
+        const int key0 = t * BK;
+        const bool idle = rows <= 0 || key0 > pos0 + rows - 1 || key0 + BK - 1 <= pos0 - p.window;
+        const Seen seen = seen_between(pos - key0 - p.window + 1, pos - key0);  // the keys that the lane's query sees
+        // some query of the block does not see all of the tile: what it does not see may be anything
+        const bool cut = key0 + BK - 1 > low || key0 <= low + BM - 1 - p.window;
+        bool found = false;
+        if (cut) {
+            if (any_special<T, BYTES, NW * 64>(tv, tid)) special = t;
+            __syncthreads();
+            found = special == t;
+        }
+        Op<T> pr[BK / 16];
+        if (!idle) {
+            f32x16 s[BK / 32];
+#pragma unroll
+            for (int h = 0; h < BK / 32; ++h) {
+                s[h] = zero16();
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) mma(s[h], L::row_op(rb, 32 * h, ks), q[ks]);
+            }
+            if (cut) {
+#pragma unroll
+                for (int h = 0; h < BK / 32; ++h)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[h][i] = seen(32 * h + acc_row(i, g)) ? s[h][i] : -__builtin_inff();
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int h = 0; h < BK / 32; ++h)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[h][i]);
+            top = fmaxf(top, other_half(top, lane)) * p.scale_log2;
+            if (__any(top > m + kSlack)) {
+                const float next = fmaxf(m, top), f = next == m ? 1.f : __builtin_amdgcn_exp2f(m - next);
+                m = next;
+                l *= f;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) o[dt] *= f;
+            }
+            const float ref = m == -__builtin_inff() ? 0.f : m;  // nothing seen yet: all scores are -inf
+#pragma unroll
+            for (int h = 0; h < BK / 32; ++h) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], p.scale_log2, -ref));
+                    l += s[h][i];
+                }
+                pr[2 * h] = op_of<T>(s[h], 0);
+                pr[2 * h + 1] = op_of<T>(s[h], 1);
+            }
+        }
+        if (found) {
+            if (!idle) {
+                f32x16 add[DT];
+                special_sums<T, D, BK>(add, col_base + tv, seen, g, false);
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) o[dt] += add[dt];
+            }
+            __syncthreads();
+            clear_special<T, BYTES, NW * 64>(tv, tid);
+            __syncthreads();
+        }
+        if (!idle) {
+            const Lds cb = opaque(col_base + tv);
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) mma(o[dt], L::col_op(cb, 16 * ks, dt), pr[ks]);
+        }
+    }
+    if (rows <= 0) return;
+    l += other_half(l, lane);
+    if ((lane & 31) >= rows) return;
+    const int64_t token = w.s.q0 + mine + (lane & 31);
+    if (gridDim.y > 1) {
+        const int64_t row = token * p.heads + head, at = (int64_t)blockIdx.y * a.parts.rows + row;
+        store_column<float, D>(a.parts.o + at * D, o, 1.f, g);
+        if (g == 0) a.parts.ml[at] = float2{m, l};
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store_column<T, D>(reinterpret_cast<T*>(a.o) + (token * p.heads + head) * D, o, inv, g);
+    if (a.lse && g == 0) a.lse[token * p.heads + head] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Joins parts: a workgroup a row, groups of its threads taking the row's parts in turn.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void join_kernel(Parts p, T* __restrict__ o, float* __restrict__ lse, Owned owned) {
+    constexpr int SUB = 256 / (D / 2);
+    __shared__ float2 sum[SUB][D / 2];
+    __shared__ float total[SUB];
+    const int64_t row = blockIdx.x;
+    const int c = threadIdx.x % (D / 2), sub = threadIdx.x / (D / 2), lane = threadIdx.x & 63;
+    if (owned.cu) {  // a token of no sequence has no parts and stays as it was
+        const int64_t token = row / owned.heads;
+        bool found = false;
+        for (int64_t base = 0; base < owned.n && !found; base += 64) {
+            bool here = false;
+            if (base + lane < owned.n) {
+                const int64_t lo = clamp64(owned.cu[base + lane], 0, owned.total);
+                here = lo <= token && token < clamp64(owned.cu[base + lane + 1], lo, owned.total);
+            }
+            found = __any(here);
+        }
+        if (!found) return;
+    }
+    float m = -__builtin_inff();
+    for (int i = lane; i < p.splits; i += 64) m = fmaxf(m, p.ml[i * p.rows + row].x);
+#pragma unroll
+    for (int s = 32; s >= 1; s /= 2) m = fmaxf(m, __shfl_xor(m, s));
+    float2 x{0.f, 0.f};
+    float l = 0.f;
+    for (int i = sub; i < p.splits; i += SUB) {
+        const float2 ml = p.ml[i * p.rows + row];
+        if (ml.x == -__builtin_inff() && ml.y == 0.f) continue;  // a part that saw nothing
+        const float f = __builtin_amdgcn_exp2f(ml.x - m);
+        const float2 v = *reinterpret_cast<const float2*>(p.o + (i * p.rows + row) * D + 2 * c);
+        x.x += f * v.x;
+        x.y += f * v.y;
+        l += f * ml.y;
+    }
+    sum[sub][c] = x;
+    if (c == 0) total[sub] = l;
+    __syncthreads();
+    if (sub == 0) {
+#pragma unroll
+        for (int s = 1; s < SUB; ++s) {
+            x.x += sum[s][c].x;
+            x.y += sum[s][c].y;
+            l += total[s];
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float out[2] = {x.x * inv, x.y * inv};
+        store_vec_any<T, 2>(o + row * D + 2 * c, out);
+        if (lse && c == 0) lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+}
+
+hipError_t launch_join(const Parts& p, void* o, float* lse, int64_t d, bool bf16_out, const Owned& owned, hipStream_t stream) {
+    const dim3 grid((unsigned)p.rows), block(256);
+    if (bf16_out && d == 64) hipLaunchKernelGGL((join_kernel<bf16, 64>), grid, block, 0, stream, p, (bf16*)o, lse, owned);
+    else if (bf16_out) hipLaunchKernelGGL((join_kernel<bf16, 128>), grid, block, 0, stream, p, (bf16*)o, lse, owned);
+    else if (d == 64) hipLaunchKernelGGL((join_kernel<float, 64>), grid, block, 0, stream, p, (float*)o, lse, owned);
+    else hipLaunchKernelGGL((join_kernel<float, 128>), grid, block, 0, stream, p, (float*)o, lse, owned);
+    return hipGetLastError();
+}
+
+// Parts that a block's keys are taken in: with too few blocks for the GPU, as many as fill it twice, of
+// 256 keys and more.  (Sequences that are packed may be shorter than the longest: their parts are, too.)
+int fwd_splits(Shape p, int64_t cus) {
+    const int64_t grid = deal(&p, p.tq, 128, p.heads / p.groups);
+    const int64_t busy = p.cu_q ? ((p.tq + 127) / 128 + p.n - 1) * p.heads : (p.tq + 127) / 128 * p.n * p.heads;
+    if (grid <= 0 || busy >= cus) return 1;
+    const int64_t keys = min((int64_t)p.window + 128, p.tk), most = (keys + 255) / 256, want = (2 * cus + busy - 1) / busy;
+    return (int)max((int64_t)1, min(most, want));
+}
+
+template <typename T, int D, int NW>
+hipError_t run_fwd(FwdParams f, hipStream_t stream) {
+    const int64_t grid = deal(&f.p, f.p.tq, NW * 32, f.p.heads / f.p.groups);
+    if (grid < 0) return hipErrorInvalidValue;
+    if (grid == 0) return hipSuccess;
+    hipLaunchKernelGGL((fwd_kernel<T, D, NW>), dim3((unsigned)grid, (unsigned)f.parts.splits), dim3(NW * 64), 0, stream, f);
+    if (f.parts.splits > 1)
+        return launch_join(f.parts, f.o, f.lse, D, sizeof(T) == 2, Owned{f.p.cu_q, f.p.n, f.p.tq, f.p.heads}, stream);
+    return hipGetLastError();
+}
+
+}  // namespace attn
+
+// a window that no sequence is longer than, so that a position less it stays a 32-bit number
+constexpr int kAllKeys = INT32_MAX - 1024;
+
+attn::Shape attn_shape(const AttnArgs& a) {
+    attn::Shape p{};
+    const uint32_t es = a.dtype_bf16 ? 2 : 4;
+    p.cu_q = a.cu_q;
+    p.cu_k = a.cu_k;
+    p.n = a.N;
+    p.tq = a.T;
+    p.tk = a.S;
+    p.heads = (int)a.H;
+    p.groups = (int)a.G;
+    p.window = a.window > 0 && a.window < kAllKeys ? (int)a.window : kAllKeys;
+    p.q_stride = (uint32_t)a.q_stride * es;
+    p.k_stride = (uint32_t)a.k_stride * es;
+    p.v_stride = (uint32_t)a.v_stride * es;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * attn::kLog2e;
+    return p;
+}
+
+// the launches with the most workgroups: of 128 queries a head, and of 128 keys a key head
+bool attn_grid_ok(const AttnArgs& a) {
+    attn::Shape p = attn_shape(a);
+    const int64_t tokens = a.cu_q ? a.T : a.N * a.T;
+    return attn::deal(&p, a.T, 128, p.heads / p.groups) >= 0 && attn::deal(&p, a.S, 128, 1) >= 0 && tokens < ((int64_t)1 << 29);
+}
+
+size_t attn_fwd_workspace_bytes(const AttnArgs& a) {
+    const int splits = attn::fwd_splits(attn_shape(a), a.cus);
+    return splits > 1 ? attn::parts_bytes((a.cu_q ? a.T : a.N * a.T) * a.H, a.d, splits) : 0;
+}
+
+hipError_t launch_attn_fwd(const AttnArgs& a, void* workspace) {
+    const attn::Shape p = attn_shape(a);
+    const int64_t rows = (a.cu_q ? a.T : a.N * a.T) * a.H;
+    const attn::FwdParams f{(const char*)a.q, (const char*)a.k, (const char*)a.v, a.o, a.lse,
+                            attn::parts_in(workspace, rows, a.d, workspace ? attn::fwd_splits(p, a.cus) : 1), p};
+    const hipStream_t s = (hipStream_t)a.stream;
+    if (a.dtype_bf16) return a.d == 64 ? attn::run_fwd<bf16, 64, 4>(f, s) : attn::run_fwd<bf16, 128, 4>(f, s);
+    return a.d == 64 ? attn::run_fwd<float, 64, 4>(f, s) : attn::run_fwd<float, 128, 4>(f, s);
+}
+
+}  // namespace gdn2

@@ -186,6 +186,110 @@ struct NormBwdArgs {
     void* stream;
 };
 
+// Attention over key heads that groups of query heads share; the gradients' part is used by the
+// backward pass only.
+struct AttnArgs {
+    const void* q;       // [queries, H, d], token stride q_stride
+    const void* k;       // [keys, G, d], token stride k_stride
+    const void* v;       // [keys, G, d], token stride v_stride
+    void* o;             // [queries, H, d], contiguous
+    float* lse;          // [queries, H] or nullptr (forward)
+    int64_t N;           // sequences
+    int64_t T, S;        // queries and keys of each, or with offsets the packed totals
+    int64_t H, G, d;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t window;      // keys that a query sees up to its own; 0: all
+    float scale;
+    bool dtype_bf16;
+    const int64_t* cu_q;  // N + 1 offsets each (device memory), or nullptr
+    const int64_t* cu_k;
+    void* stream;
+    int cus;
+    // backward
+    const void* d_o = nullptr;  // [queries, H, d], contiguous; o and lse are inputs
+    void* dq = nullptr;         // laid out as q, k and v, contiguous
+    void* dk = nullptr;
+    void* dv = nullptr;
+    float* stats = nullptr;     // workspace: of every query and head lse in base 2 and sum(d_o o)
+};
+inline bool attn_supported(int64_t d) { return d == 64 || d == 128; }
+bool attn_grid_ok(const AttnArgs& a);  // whether every launch that the sizes may take fits
+size_t attn_fwd_workspace_bytes(const AttnArgs& a);
+hipError_t launch_attn_fwd(const AttnArgs& a, void* workspace);
+inline int64_t attn_stats_bytes(int64_t tokens, int64_t heads) { return tokens * heads * 8; }
+hipError_t launch_attn_bwd(const AttnArgs& a);
+
+// One token of each of N sequences over caches of their last C tokens.
+struct AttnStepArgs {
+    const void* q;             // [N, H, d], token stride q_stride
+    const void* k;             // [N, G, d], token stride k_stride
+    const void* v;
+    void* k_cache;             // [N, C, G, d], contiguous
+    void* v_cache;
+    const int64_t* positions;  // [N]
+    void* o;                   // [N, H, d], contiguous
+    int64_t N, H, G, d, C, q_stride, k_stride, v_stride;
+    int64_t window;            // 0: all that the cache holds
+    float scale;
+    bool dtype_bf16;
+    void* stream;
+    int cus;
+};
+size_t attn_step_workspace_bytes(const AttnStepArgs& a);
+hipError_t launch_attn_step(const AttnStepArgs& a, void* workspace);
+namespace attn {
+struct Shape;
+}
+attn::Shape attn_shape(const AttnArgs& a);
+
+// Root-mean-square norm of x + residual.
+struct RmsArgs {
+    const void* x;         // [rows, width]
+    const void* residual;  // [rows, width] or nullptr
+    const float* gamma;    // [width]
+    void* y;               // [rows, width], x's type; 8 bits with `scale`
+    float* scale;          // [rows], or nullptr for an output in x's type
+    void* h;               // [rows, width], the residual's type (with a residual)
+    float* rstd;           // [rows] or nullptr
+    int64_t rows, width;
+    bool dtype_bf16, residual_bf16;
+    float eps;
+    void* stream;
+};
+struct RmsBwdArgs {
+    const void* dy;      // [rows, width]
+    const void* h;       // [rows, width]
+    const float* gamma;
+    const float* rstd;
+    const void* dh;      // [rows, width] or nullptr, as h
+    void* dx;            // as h
+    float* dgamma;       // [width]
+    float* parts;        // workspace of rms_bwd_workspace_bytes
+    int64_t rows, width;
+    bool dtype_bf16, residual_bf16;  // of dy; of h, dh and dx
+    void* stream;
+};
+hipError_t launch_rms_norm(const RmsArgs& a);
+size_t rms_bwd_workspace_bytes(int64_t rows, int64_t width);
+hipError_t launch_rms_norm_bwd(const RmsBwdArgs& a);
+
+// Rotary positions.
+struct RotaryArgs {
+    const void* q;             // [tokens, H, d]
+    const void* k;             // [tokens, G, d], or nullptr with G = 0
+    const float* freq;         // [half], radians a position
+    const int64_t* positions;  // [tokens], or nullptr for the place in a sequence of T
+    void* qo;                  // [tokens, H, d]; may be q
+    void* ko;
+    int64_t tokens, T, H, G, d, half;
+    int64_t q_stride, k_stride, qo_stride, ko_stride;  // elements between tokens
+    float scale;
+    bool dtype_bf16, interleaved, inverse;
+    void* stream;
+};
+bool rotary_grid_ok(const RotaryArgs& a);
+hipError_t launch_rotary(const RotaryArgs& a);
+
 // head sizes and dtypes that the scan and its step are built for
 inline bool ssm_supported(int64_t dk, int64_t dv, bool bf16, bool f32) {
     return (bf16 || f32) && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);

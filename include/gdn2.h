@@ -22,7 +22,8 @@
  * them), a single-token recurrent decode step (the page's opening section:
  * decoding keeps a constant-size state), and the mixer's fused elementwise
  * passes on either side of the recurrence.  Beside them stand the calls of a
- * state space block (its scan, convolution and norm), described with them below.
+ * state space block (its scan, convolution and norm) and of an attention block
+ * (attention, rotary positions and norm), described with them below.
  *
  * Conventions for every call:
  *   - Tensor pointers are DEVICE pointers (HIP global memory) of the current
@@ -521,10 +522,215 @@ gdn2_status_t gdn2_layer_norm_bwd(const void* dy, const void* x, const float* ga
                                   float* dbeta, void* workspace, size_t workspace_bytes,
                                   int64_t rows, int64_t width, gdn2_dtype_t dtype, void* stream);
 
+/*
+ * The attention block.  Hybrid stacks put attention over a sliding window
+ * between the layers above (page "Why NVIDIA Gated DeltaNet-2 separates erase
+ * and write gates", axbrief.com: a hybrid cell alternates the recurrence with
+ * attention over a window of 2K tokens).  Such a layer is a norm with the
+ * residual's addition, projections (the caller's), rotary positions and
+ * attention.  These calls follow the conventions at the top; as in the state
+ * space block, q, k and v may have a token stride of their own.
+ */
+
+/*
+ * gdn2_attn_fwd -- causal attention of T queries over S keys in each of B
+ * sequences.  Query t stands at position S - T + t of the S keys and sees the
+ * keys at its own position and before it, with a window > 0 the last `window` of
+ * them; head h of H reads key head h / (H / G) of G.
+ *
+ *   s_j = scale q . k_j,  o = sum_j e^(s_j - lse) v_j,  lse = log sum_j e^(s_j)
+ *
+ *   q     [B, T, H, d]  dtype    q_stride elements between tokens
+ *   k, v  [B, S, G, d]  dtype    k_stride, v_stride
+ *   o     [B, T, H, d]  dtype    out
+ *   lse   [B, T, H]     float32  out, for the backward pass; or NULL to skip
+ *
+ * Built for d = 64 and 128, BF16 and F32.  T and S may be any sizes from 0 on, T
+ * greater than S too: a query that sees no key (or none with a score above
+ * minus infinity) has o = 0 and lse = -infinity.
+ * A NaN or an infinity in k or v reaches no query that does not see it.
+ * scale > 0.  H is a multiple of G; strides are at least a token's elements,
+ * below 2^22 and whole 16-byte units; H * d is below 2^22, T and S at most
+ * 2^31 - 1025, B * T below 2^29, and B * G * ceil(T / 128) * (H / G) and
+ * B * G * ceil(S / 128) below 2^23 (GDN2_ERR_SHAPE, or GDN2_ERR_MISALIGNED).
+ * With workspace = NULL and workspace_bytes = 0 a block of queries walks all its
+ * keys.  With a workspace of gdn2_attn_fwd_workspace_bytes bytes (16-byte
+ * aligned, overlapping no argument) the keys of few queries are taken in parts.
+ * A shorter workspace, or one where that call says 0, returns
+ * GDN2_ERR_WORKSPACE.
+ */
+gdn2_status_t gdn2_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B,
+                            int64_t T, int64_t S, int64_t H, int64_t G, int64_t d, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, int64_t window, float scale,
+                            gdn2_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The workspace with which gdn2_attn_fwd is fastest for these sizes on the current
+ * device: 0 where the blocks of queries fill it by themselves. */
+size_t gdn2_attn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t S, int64_t H, int64_t G, int64_t d,
+                                     int64_t window, gdn2_dtype_t dtype);
+
+/*
+ * gdn2_attn_fwd_varlen -- the same over N sequences packed along the token axis:
+ * sequence n has the queries [cu_seqlens[n], cu_seqlens[n + 1]) and the keys
+ * [cu_seqlens_k[n], cu_seqlens_k[n + 1]) (both int64 [N + 1] in device memory; the
+ * same pointer where the sequences stand alone).  q, o [total_T, H, d], k, v
+ * [total_S, G, d], lse [total_T, H].  Each range is clamped into the tensor;
+ * tokens of no sequence are left as they were in o and lse.  Offsets that
+ * decrease or overlap leave results unspecified.  The conditions on sizes hold
+ * with total_T / 128 + N for B * ceil(T / 128), and likewise for the keys.
+ */
+gdn2_status_t gdn2_attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                                   const int64_t* cu_seqlens, const int64_t* cu_seqlens_k, int64_t N,
+                                   int64_t total_T, int64_t total_S, int64_t H, int64_t G, int64_t d,
+                                   int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t window,
+                                   float scale, gdn2_dtype_t dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+size_t gdn2_attn_fwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t total_S, int64_t H,
+                                            int64_t G, int64_t d, int64_t window, gdn2_dtype_t dtype);
+
+/*
+ * gdn2_attn_bwd -- gradients of sum(d_o * o) for gdn2_attn_fwd, from its o and lse.
+ *
+ *   d_o, o      [B, T, H, d]  dtype    q, k, v, lse and all sizes as above
+ *   dq          [B, T, H, d]  dtype    out
+ *   dk, dv      [B, S, G, d]  dtype    out, summed over the heads that share them
+ *   workspace   16-byte aligned, overlapping no argument
+ *
+ * Sums are formed in a fixed order: equal calls give equal bits.  A NaN or an
+ * infinity of one token reaches the gradients only of tokens that it sees or that
+ * see it.
+ */
+gdn2_status_t gdn2_attn_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o,
+                            const float* lse, void* dq, void* dk, void* dv, int64_t B, int64_t T,
+                            int64_t S, int64_t H, int64_t G, int64_t d, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, int64_t window, float scale,
+                            gdn2_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* gdn2_attn_bwd_varlen -- the same for gdn2_attn_fwd_varlen; gradients of tokens of no
+ * sequence are left as they were. */
+gdn2_status_t gdn2_attn_bwd_varlen(const void* d_o, const void* q, const void* k, const void* v,
+                                   const void* o, const float* lse, void* dq, void* dk, void* dv,
+                                   const int64_t* cu_seqlens, const int64_t* cu_seqlens_k, int64_t N,
+                                   int64_t total_T, int64_t total_S, int64_t H, int64_t G, int64_t d,
+                                   int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t window,
+                                   float scale, gdn2_dtype_t dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace that both need, for all queries (B * T, or total_T). */
+size_t gdn2_attn_bwd_workspace_bytes(int64_t queries, int64_t H);
+
+/*
+ * gdn2_attn_step -- attention of one token for each of N sequences over a cache of
+ * its last C tokens, which the step's key and value join: the token at position p
+ * lies in slot p mod C.
+ *
+ *   q                 [N, H, d]     dtype  q_stride elements between sequences
+ *   k, v              [N, G, d]     dtype  the token's own; k_stride, v_stride
+ *   k_cache, v_cache  [N, C, G, d]  dtype  slot p mod C is written
+ *   positions         [N]           int64  p of each sequence's token, in device
+ *                                          memory
+ *   o                 [N, H, d]     dtype  out
+ *
+ * The token sees the last min(p + 1, C) tokens, itself among them, with a
+ * window > 0 at most `window` of them.  A position below 0 is no token: its output is zero and its
+ * cache is left as it was.  Slots behind a sequence's last token are not read.
+ * Strides below 2^31, N * G * ceil(H / G / 32) below 2^23; otherwise as for
+ * gdn2_attn_fwd.  With a workspace of gdn2_attn_step_workspace_bytes bytes (16-byte
+ * aligned) a sequence's tokens are taken in parts; NULL and 0: whole.
+ */
+gdn2_status_t gdn2_attn_step(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+                             const int64_t* positions, void* o, int64_t N, int64_t H, int64_t G,
+                             int64_t d, int64_t C, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             int64_t window, float scale, gdn2_dtype_t dtype, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The workspace with which gdn2_attn_step is fastest on the current device (0: none). */
+size_t gdn2_attn_step_workspace_bytes(int64_t N, int64_t H, int64_t G, int64_t d, int64_t C,
+                                      int64_t window, gdn2_dtype_t dtype);
+
+/*
+ * gdn2_rotary -- rotary positions on the first `rot` channels of the heads of q and k:
+ *
+ *   (a, b) -> scale (a cos t - b sin t, a sin t + b cos t),  t = position freq[i]
+ *
+ * for the pairs i of rot / 2: channels i and i + rot / 2, or with interleaved != 0
+ * channels 2 i and 2 i + 1.  The other channels are copied.  inverse != 0 turns by
+ * -t, which is the gradient of the call without it (scale is the same).
+ *
+ *   q, q_out   [tokens, H, d]  dtype    strides in elements between tokens
+ *   k, k_out   [tokens, G, d]  dtype    G = 0: q alone
+ *   freq       [rot / 2]       float32  radians a position
+ *   positions  [tokens]        int64    or NULL: token n is at n mod T
+ *
+ * Angles are formed in 64 bits, so far positions are exact.  q_out may be q and
+ * k_out k, with the same strides (in place; the channels from rot on are then not
+ * touched); outputs may be parts of one wider tensor, but share no byte with
+ * anything else.  rot is even, from 2 to d; d from 2 to 512; (H + G) d below 2^22;
+ * strides at least a token's elements and below 2^31; tensors need the alignment
+ * of their elements only.  scale > 0.
+ */
+gdn2_status_t gdn2_rotary(const void* q, const void* k, const float* freq, const int64_t* positions,
+                          void* q_out, void* k_out, int64_t tokens, int64_t T, int64_t H, int64_t G,
+                          int64_t d, int64_t rot, int64_t q_stride, int64_t k_stride,
+                          int64_t q_out_stride, int64_t k_out_stride, int interleaved, int inverse,
+                          float scale, gdn2_dtype_t dtype, void* stream);
+
+/*
+ * gdn2_rms_norm -- root-mean-square norm of a residual sum:
+ *
+ *   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd gamma
+ *
+ *   x, y      [rows, width]  dtype           y must not overlap an input
+ *   residual  [rows, width]  residual_dtype  (dtype or F32) or NULL: h = x
+ *   gamma     [width]        float32
+ *   h         [rows, width]  residual_dtype  out, with a residual; may be the same
+ *                                            pointer as residual
+ *   rstd      [rows]         float32         out, for the backward pass; NULL to skip
+ *
+ * y and rstd are formed from the sum before it is rounded to h.  width may be any
+ * value from 1 to 16384, rows any from 0 on.  eps >= 0.
+ */
+gdn2_status_t gdn2_rms_norm(const void* x, const void* residual, const float* gamma, void* y, void* h,
+                            float* rstd, int64_t rows, int64_t width, float eps, gdn2_dtype_t dtype,
+                            gdn2_dtype_t residual_dtype, void* stream);
+
+/* gdn2_rms_norm_fp8 -- the same with y in 8 bits (e4m3, [rows, width] bytes) and a scale for
+ * each row (float32 [rows]): scale = max|y| / 448, or 1 for a row of zeros, and the byte is
+ * the value nearest to y / scale. */
+gdn2_status_t gdn2_rms_norm_fp8(const void* x, const void* residual, const float* gamma, void* y,
+                                float* scales, void* h, float* rstd, int64_t rows, int64_t width,
+                                float eps, gdn2_dtype_t dtype, gdn2_dtype_t residual_dtype, void* stream);
+
+/* Bytes of device workspace that gdn2_rms_norm_bwd needs: partial sums of dgamma.  0 for
+ * few rows, and if the sizes are out of range. */
+size_t gdn2_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t width);
+
+/*
+ * gdn2_rms_norm_bwd -- gradients of sum(dy * y) + sum(dh * h) for gdn2_rms_norm:
+ *
+ *   dx = dh + rstd (v - u mean(u v)),  u = h rstd,  v = dy gamma   (of x and of the residual)
+ *   dgamma = sum over rows of dy u
+ *
+ *   dy          [rows, width]  dtype
+ *   h, dh, dx   [rows, width]  residual_dtype  dh may be NULL for zeros; dx may be dh
+ *                                              (h = x without a residual)
+ *   rstd        [rows]         float32         as the forward pass gave it
+ *   gamma, dgamma  [width]     float32
+ *   workspace   16-byte aligned, overlapping no argument
+ *
+ * The sums over rows are formed in a fixed order: equal calls give equal bits.
+ * With rows = 0 dgamma is zeros.
+ */
+gdn2_status_t gdn2_rms_norm_bwd(const void* dy, const void* h, const float* gamma, const float* rstd,
+                                const void* dh, void* dx, float* dgamma, void* workspace,
+                                size_t workspace_bytes, int64_t rows, int64_t width, gdn2_dtype_t dtype,
+                                gdn2_dtype_t residual_dtype, void* stream);
+
 /* 1 if gdn2_chunk_fwd and gdn2_chunk_fwd_varlen (which = 0), gdn2_decode_step
  * (which = 1), gdn2_chunk_bwd (which = 2), gdn2_mixer_prep and gdn2_mixer_out
- * (which = 3) or gdn2_ssm_fwd, gdn2_ssm_fwd_varlen and gdn2_ssm_step (which = 5)
- * support (dk, dv, dtype), else 0. */
+ * (which = 3), gdn2_ssm_fwd, gdn2_ssm_fwd_varlen and gdn2_ssm_step (which = 5) or the
+ * gdn2_attn calls (which = 6, with dk = dv = d) support (dk, dv, dtype), else 0. */
 int gdn2_supported(int which, int64_t dk, int64_t dv, gdn2_dtype_t dtype);
 
 /* Static, NUL-terminated description of a status code. */
