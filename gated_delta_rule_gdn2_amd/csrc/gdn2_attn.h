@@ -86,13 +86,13 @@ __device__ __forceinline__ void load_far_to_lds(Lds to, const void* from) {
 
 // A tile of rows of D elements in LDS, filled by loads that go there directly; it begins at a multiple
 // of 1024 bytes.  Rows lie one behind the other without padding (such a load writes 64 lanes' 16-byte
-// units in lane order), so each row's units are permuted by an exclusive or: with it the lanes of a
-// row-wise read take different rows' units from different banks, and so do the 4 rows of a transposing
-// read.
+// units in lane order), so each row's units are permuted by an exclusive or.  LDS serves 256 bytes at a
+// time: 16 lanes of a row-wise read, which are 16 rows' units, or 32 lanes of a transposing read, which
+// are 4 rows' quads of units; either come from different banks.
 template <typename T, int D> struct Tile {
     static constexpr int kRow = D * (int)sizeof(T), kUnits = kRow / 16;
     __device__ static constexpr int swz(int row) {
-        return (kUnits >= 16 ? ((row >> 3) & 1) << 3 : 0) | ((row & 3) << 1) | ((row >> 2) & 1);
+        return (kUnits >= 16 ? (row & 3) << 2 : (row & 2) << 1) | ((row >> 2) & 3);
     }
     // ROWS rows from memory, rows behind `bytes` as zeros; the waves of a workgroup share them
     template <int ROWS, int NW>
@@ -219,20 +219,27 @@ __device__ __forceinline__ bool finite_bits(float x) { return (__builtin_bit_cas
 // whether this thread's part of a tile of BYTES bytes holds a value that is not finite
 template <typename T, int BYTES, int NT>
 __device__ __forceinline__ bool any_special(Lds lds, int tid) {
-    constexpr unsigned kMask = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
-    bool found = false;
-    for (int u = tid; u < BYTES / 16; u += NT) {
-        const u32x4 x = lds_get<u32x4>(lds + u * 16);
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 two = 0;
+    uint32_t one = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const unsigned m = x[e] & kMask;
-            if (sizeof(T) == 2)
-                found |= (m & 0xffffu) == (kMask & 0xffffu) || (m >> 16) == (kMask >> 16);
+    for (int u = 0; u < BYTES / 16 / NT; ++u) {
+        const u32x4 x = lds_get<u32x4>(lds + (u * NT + tid) * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // the largest exponent and mantissa
+            if constexpr (sizeof(T) == 2)
+                two = __builtin_elementwise_max(two, __builtin_bit_cast(u16x2, x[e] & 0x7fff7fffu));
             else
-                found |= m == kMask;
+                one = __builtin_elementwise_max(one, x[e] & 0x7fffffffu);
         }
     }
-    return found;
+    return sizeof(T) == 2 ? two[0] >= 0x7f80u || two[1] >= 0x7f80u : one >= 0x7f800000u;
+}
+template <typename T> __device__ __forceinline__ Op<T> finite_part(Op<T> a) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (!finite_bits((T)a.v[e])) a.v[e] = from_f32<T>(0.f);
+    return a;
 }
 // the thread's part of the tile with zeros for what is not finite
 template <typename T, int BYTES, int NT>
@@ -269,24 +276,26 @@ struct Seen {
 __device__ __forceinline__ Seen seen_between(int lo, int hi) { return Seen{lo, hi < lo ? 0u : (unsigned)(hi - lo) + 1u}; }
 
 // What is not finite in column 32 dt + register's row of the tile's rows that a lane's column sees:
-// zero, an infinity or a NaN to add (`nan`: a NaN for infinities too, where weights may be zero).  A
-// call of its own, through memory, so that the loop around it keeps its registers.
+// zero, an infinity or a NaN to add (`nan`: a NaN for infinities too, where weights may be zero).
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ f32x16 special_sum(Lds base, int dt, Seen seen, int g, bool nan) {
+    static_assert(ROWS <= 64, "counts below 128");
+    f32x16 code = zero16();
+#pragma unroll 1
+    for (int ks = 0; ks < ROWS / 16; ++ks) {
+        Op<T> see;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) see.v[e] = from_f32<T>(seen(16 * ks + acc_row(e, g)) ? 1.f : 0.f);
+        mma(code, special_code<T>(Tile<T, D>::col_op(base, 16 * ks, dt)), see);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) code[i] = nan && code[i] > 0.f ? __builtin_nanf("") : from_code(code[i]);
+    return code;
+}
+// All columns of it, by a call of its own and through memory, so that the loop around it keeps its registers.
 template <typename T, int D, int ROWS>
 __device__ __attribute__((noinline)) void special_sums(f32x16* out, Lds base, Seen seen, int g, bool nan) {
-    typedef Tile<T, D> L;
-    static_assert(ROWS <= 64, "counts below 128");
-    for (int dt = 0; dt < D / 32; ++dt) {
-        f32x16 code = zero16();
-        for (int ks = 0; ks < ROWS / 16; ++ks) {
-            Op<T> see;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) see.v[e] = from_f32<T>(seen(16 * ks + acc_row(e, g)) ? 1.f : 0.f);
-            mma(code, special_code<T>(L::col_op(base, 16 * ks, dt)), see);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) code[i] = nan && code[i] > 0.f ? __builtin_nanf("") : from_code(code[i]);
-        out[dt] = code;
-    }
+    for (int dt = 0; dt < D / 32; ++dt) out[dt] = special_sum<T, D, ROWS>(base, dt, seen, g, nan);
 }
 
 // ---- which workgroup does what --------------------------------------------------------------
