@@ -60,28 +60,34 @@ __device__ __forceinline__ Lds opaque(Lds x) {
     return x;
 }
 
+// a value that is the same in every lane, in scalar registers
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
 // A buffer resource's words (uniform): loads beyond `bytes` give zeros.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x4 rsrc_words(const void* p, uint32_t bytes) {
     const uint64_t a = (uint64_t)(uintptr_t)p;
-    return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+    return u32x4{(uint32_t)uniform((int)a), (uint32_t)uniform((int)(a >> 32)) & 0xffffu, (uint32_t)uniform((int)bytes), 0x00020000u};
 }
 // 16 bytes a lane from `off` behind the resource's base to LDS, lane after lane from `to` (uniform) on.
 // In assembly because the compiler takes every read of LDS for one of what such a load writes, and
 // waits for it; the waits are tile_barrier's.  The load has no result registers, and nothing else here
 // uses m0.
 __device__ __forceinline__ void load_to_lds(Lds to, u32x4 r, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "memory");
-}
-
-// the same, 4 bytes a lane
-__device__ __forceinline__ void load_words_to_lds(Lds to, u32x4 r, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(uniform((int)to)), "v"(off), "s"(r) : "memory");
 }
 
 // 16 bytes a lane from each lane's own address
 __device__ __forceinline__ void load_far_to_lds(Lds to, const void* from) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform((int)to)), "v"(from) : "memory");
+}
+
+// the same, 4 bytes a lane
+__device__ __forceinline__ void load_far_words_to_lds(Lds to, const void* from) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform((int)to)), "v"(from) : "memory");
 }
 
 // A tile of rows of D elements in LDS, filled by loads that go there directly; it begins at a multiple
@@ -195,10 +201,52 @@ __device__ __forceinline__ void store_column(T* row, const f32x16 (&c)[D / 32], 
         }
 }
 
+// The same for a wave's 32 rows (`rows` of them there), through LDS of the wave's own, so that whole rows
+// go out 16 bytes a lane instead of 8 bytes of each row.  `to`: the first row's; `stride`: bytes between rows.
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(Lds lds, char* to, int64_t stride, int rows, const f32x16 (&c)[D / 32], float factor,
+                                           int lane) {
+    typedef Tile<T, D> L;
+    const int row = lane & 31, g = lane >> 5;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int byte = (32 * dt + 8 * q + 4 * g) * (int)sizeof(T);
+            const Lds at = lds + row * L::kRow + (((byte >> 4) ^ L::swz(row)) << 4) + (byte & 15);
+            if constexpr (sizeof(T) == 2) {
+                bf16x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = from_f32<bf16>(c[dt][4 * q + e] * factor);
+                *(GDN2_LDS bf16x4*)(uintptr_t)at = v;
+            } else {
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = c[dt][4 * q + e] * factor;
+                *(GDN2_LDS f32x4*)(uintptr_t)at = v;
+            }
+        }
+    __builtin_amdgcn_wave_barrier();  // a wave's reads of LDS follow its writes in order
+#pragma unroll
+    for (int i = 0; i < 32 * L::kUnits / 64; ++i) {
+        const int u = i * 64 + lane, r = u / L::kUnits, unit = u % L::kUnits;
+        const u32x4 v = lds_get<u32x4>(lds + r * L::kRow + ((unit ^ L::swz(r)) << 4));
+        if (r < rows) *reinterpret_cast<u32x4*>(to + r * stride + unit * 16) = v;
+    }
+}
+
 // v of the lane 32 away: the other half of an accumulator's column
 __device__ __forceinline__ float other_half(float v, int lane) {
     const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v), __builtin_bit_cast(unsigned, v), false, false);
     return __builtin_bit_cast(float, lane < 32 ? r[1] : r[0]);
+}
+
+// every wave is here, and what they wrote to LDS can be read; loads and stores are not waited for
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // loads that go to LDS directly have arrived, and every wave is here
@@ -206,6 +254,9 @@ __device__ __forceinline__ void tile_barrier() {
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     __syncthreads();
 }
+
+// zero times x, added to `sum`: a NaN once anything was not finite
+__device__ __forceinline__ float watch(float sum, float x) { return __builtin_fmaf(x, 0.f, sum); }
 
 // ---- values that are not finite -------------------------------------------------------------
 // A product over a tile's rows multiplies what a mask hides by zero, which an infinity or a NaN there
@@ -304,10 +355,6 @@ struct Seq {
     int64_t q0, k0;  // first token of the sequence's queries and keys
     int lq, lk;      // how many there are
 };
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
-}
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 // Blocks of `rows` tokens of the packed sequences, counted through: sequence and block of the
@@ -356,7 +403,8 @@ struct Shape {
     uint32_t q_stride, k_stride, v_stride;  // bytes between tokens
     float scale, scale_log2;                // scale, and scale log2(e)
     int blocks;           // blocks of a head: of every sequence's, or of all packed ones
-    int slices;           // parts that a group's blocks are dealt out in, so that every XCD has as many
+    unsigned all_groups;  // key heads of all sequences (packed: key heads)
+    int slice_bits;       // a group's blocks are dealt out in 2^slice_bits slices, so that every XCD has as many
 };
 
 // Workgroups go to the 8 XCDs in turn, each with an L2 of its own: the blocks of one group (a
@@ -367,21 +415,20 @@ struct Work {
     Seq s;
     int block, head;  // head: of `per_group` in each group
 };
-__host__ __device__ inline int64_t groups_of(const Shape& p) { return p.cu_q ? p.groups : p.n * p.groups; }
 __device__ __forceinline__ bool find_work(const Shape& p, int rows, int per_group, bool last_first, bool keys, int lane, Work* w) {
     const unsigned x = blockIdx.x & 7, r = blockIdx.x >> 3;
-    const unsigned per = (p.blocks + p.slices - 1) / p.slices, each = per * per_group;
-    const int64_t slice = (int64_t)(r / each) * 8 + x, group = slice / p.slices;
+    const unsigned per = (p.blocks + (1u << p.slice_bits) - 1) >> p.slice_bits, each = per * per_group;
+    const unsigned slice = r / each * 8 + x, group = slice >> p.slice_bits;
     const unsigned in = r % each, nth = in / per_group;
-    const int64_t index = (int64_t)p.slices * (last_first ? per - 1 - nth : nth) + slice % p.slices;
-    if (group >= groups_of(p) || index >= p.blocks) return false;
-    w->head = (int)(group % p.groups) * per_group + in % per_group;
+    const unsigned index = ((last_first ? per - 1 - nth : nth) << p.slice_bits) + (slice & ((1u << p.slice_bits) - 1));
+    if (group >= p.all_groups || index >= (unsigned)p.blocks) return false;
+    w->head = (int)(group % (unsigned)p.groups) * per_group + in % per_group;
     if (p.cu_q) {
         int64_t seq;
         if (!find_block(keys ? p.cu_k : p.cu_q, p.n, keys ? p.tk : p.tq, rows, index, lane, &seq, &w->block)) return false;
         w->s = packed_seq(p.cu_q, p.cu_k, seq, p.tq, p.tk);
     } else {
-        const int64_t n = group / p.groups;
+        const int64_t n = group / (unsigned)p.groups;
         w->s = Seq{n * p.tq, n * p.tk, (int)p.tq, (int)p.tk};
         w->block = (int)index;
     }
@@ -392,18 +439,22 @@ __device__ __forceinline__ Work uniform(const Work& w) {
     return Work{Seq{uniform(w.s.q0), uniform(w.s.k0), uniform(w.s.lq), uniform(w.s.lk)}, uniform(w.block), uniform(w.head)};
 }
 constexpr int64_t kMaxGrid = (int64_t)1 << 23;  // workgroups of up to 512 threads: a launch has less than 2^32
-// fills in blocks and slices; workgroups of the launch (0: none), or -1 if they are too many
+// fills in how work is dealt out; workgroups of the launch (0: none), or -1 if they are too many
 inline int64_t deal(Shape* p, int64_t tokens, int rows, int per_group) {
-    const int64_t blocks = p->cu_q ? tokens / rows + p->n : (tokens + rows - 1) / rows, groups = groups_of(*p);
-    if (blocks > INT32_MAX || groups > (int64_t)1 << 40) return -1;
+    const int64_t blocks = p->cu_q ? tokens / rows + p->n : (tokens + rows - 1) / rows;
+    const int64_t groups = p->cu_q ? p->groups : p->n * p->groups;
+    if (blocks >= kMaxGrid || groups >= kMaxGrid) return -1;
     p->blocks = (int)blocks;
-    p->slices = 1;
-    while (groups * p->slices % 8) p->slices *= 2;
-    const int64_t per = (blocks + p->slices - 1) / p->slices;
-    if (per * per_group > INT32_MAX || groups * p->slices > INT32_MAX) return -1;
-    const int64_t grid = groups * p->slices * per * per_group;
-    return grid < kMaxGrid ? grid : -1;
+    p->all_groups = (unsigned)groups;
+    p->slice_bits = 0;
+    while ((groups << p->slice_bits) % 8) ++p->slice_bits;
+    const int64_t per = (blocks + ((int64_t)1 << p->slice_bits) - 1) >> p->slice_bits;
+    const int64_t grid = (groups << p->slice_bits) * per;
+    return grid < kMaxGrid && grid * per_group < kMaxGrid ? grid * per_group : -1;
 }
+
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
 // Rows whose keys were taken in parts: unnormalised sums o [splits][rows][d] in fp32, and of each row
 // and part the reference (base 2) and the sum (ml).  lse may be nullptr.

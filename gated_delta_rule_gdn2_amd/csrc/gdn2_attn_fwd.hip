@@ -18,9 +18,9 @@ namespace attn {
 
 // keys in a tile
 template <typename T> constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
-// A row's maximum may lie up to this (in base 2) above the reference that its sums are formed with
-// before they are rescaled: probabilities stay below 2^8, and most tiles need no rescaling.
-constexpr float kSlack = 8.f;
+// Weights are formed against a reference near the row's largest score so far.  A row's sum over a tile
+// may grow up to this (in units of the reference's weight) before the reference follows.
+constexpr float kSlack = 4096.f;
 
 struct FwdParams {
     const char* q;
@@ -32,17 +32,18 @@ struct FwdParams {
     Shape p;
 };
 
-template <typename T, int D, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void fwd_kernel(FwdParams a) {
+// The work of one workgroup.  FIRST: returns whether some output of a wave is not finite, and leaves that
+// wave's outputs unwritten (`flag`: in LDS, zero).  A product multiplies what a query does not see by zero, which infinities
+// and NaN survive: the other form leaves out value by value what the mask hides.
+template <typename T, int D, int NW, bool FIRST>
+__device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* flag) {
     typedef Tile<T, D> L;
     constexpr int BK = kKeys<T>, KS = D / 16, DT = D / 32, BM = NW * 32, BYTES = BK * L::kRow;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * BYTES];
-    __shared__ int special;
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Shape& p = a.p;
     Work w;
-    if (!find_work(p, BM, p.heads / p.groups, true, false, lane, &w)) return;
+    if (!find_work(p, BM, p.heads / p.groups, true, false, lane, &w)) return false;
     w = uniform(w);
     const int head = w.head, kv = head / (p.heads / p.groups), lq = w.s.lq, lk = w.s.lk;
     const char* k = a.k + w.s.k0 * p.k_stride + (int64_t)kv * L::kRow;
@@ -63,117 +64,167 @@ __global__ __launch_bounds__(NW * 64, 2) void fwd_kernel(FwdParams a) {
     const int mine = first + wave * 32, rows = min(32, lq - mine);
     const int64_t pos0 = (int64_t)off + mine;
     const int pos = (int)(pos0 + (lane & 31));
+    const Lds row_base = L::row_base(lane), col_base = L::col_base(lane);
+    auto stage = [&](int t) {
+        const int left = min(BK, lk - t * BK);
+        const Lds to = base + (t & 1) * 2 * BYTES;
+        L::template stage<BK, NW>(to, k + (int64_t)t * BK * p.k_stride, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
+        L::template stage<BK, NW>(to + BYTES, v + (int64_t)t * BK * p.v_stride, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
+    };
+    // the queries come by way of the second tile's place in LDS, if they have room there: rows are read whole
+    constexpr bool VIA = BM * L::kRow <= 2 * BYTES;
+    const char* qp = a.q + (w.s.q0 + first) * p.q_stride + (int64_t)head * L::kRow;
     Op<T> q[KS];
-    {
-        const auto r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(a.q + (w.s.q0 + mine) * p.q_stride + (int64_t)head * L::kRow), 0,
-            span(rows, p.q_stride, L::kRow), 0x00020000);
+    if (t0 < t1) stage(t0);
+    if constexpr (VIA) {
+        const Lds to = base + (~t0 & 1) * 2 * BYTES;
+        L::template stage<BM, NW>(to, qp, span(min(BM, lq - first), p.q_stride, L::kRow), p.q_stride, wave, lane);
+        tile_barrier();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[ks] = global_op<T>(r, (lane & 31) * p.q_stride, ks, g);
+        for (int ks = 0; ks < KS; ++ks) q[ks] = L::row_op(row_base + to + wave * 32 * L::kRow, 0, ks);
+    } else {
+        const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(qp), 0, span(min(BM, lq - first), p.q_stride, L::kRow), 0x00020000);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[ks] = global_op<T>(r, (wave * 32 + (lane & 31)) * p.q_stride, ks, g);
     }
     f32x16 o[DT];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) o[dt] = zero16();
     float m = -__builtin_inff(), l = 0.f;  // the reference (base 2) and the lane's part of the sum
 
-    const Lds base = lds_of(lds);
-    auto stage = [&](int t) {
-        const Lds to = base + (t & 1) * 2 * BYTES;
-        const int left = min(BK, lk - t * BK);
-        L::template stage<BK, NW>(to, k + (int64_t)t * BK * p.k_stride, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
-        L::template stage<BK, NW>(to + BYTES, v + (int64_t)t * BK * p.v_stride, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
+    f32x16 s[BK / 32];
+    auto scores = [&](Lds rb) {
+#pragma unroll
+        for (int h = 0; h < BK / 32; ++h) {
+            s[h] = zero16();
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) mma(s[h], L::row_op(rb, 32 * h, ks), q[ks]);
+        }
     };
-    const Lds row_base = L::row_base(lane), col_base = L::col_base(lane);
-    if (tid == 0) special = -1;
-    if (t0 < t1) stage(t0);
+    auto hide = [&](const Seen& seen) {
+#pragma unroll
+        for (int h = 0; h < BK / 32; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[h][i] = seen(32 * h + acc_row(i, g)) ? s[h][i] : -__builtin_inff();
+    };
+    // the largest score becomes the reference, and the sums follow it, for the queries that `need` it
+    auto follow = [&](bool need) {
+        float top = s[0][0];
+#pragma unroll
+        for (int h = 0; h < BK / 32; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[h][i]);
+        top = fmaxf(top, other_half(top, lane)) * p.scale_log2;
+        const float to = need ? fmaxf(m, top) : m, f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        l *= f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[dt] *= f;
+    };
+    // scores become weights; returns their sum
+    auto weights = [&] {
+        const float ref = m == -__builtin_inff() ? 0.f : m;  // nothing seen yet: all scores are -inf
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < BK / 32; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], p.scale_log2, -ref));
+                sum += s[h][i];
+            }
+        return sum;
+    };
+    bool first_tile = true;  // of those that the wave has to do with
     for (int t = t0; t < t1; ++t) {
         tile_barrier();
         if (t + 1 < t1) stage(t + 1);
-        const Lds tk = base + (t & 1) * 2 * BYTES, tv = tk + BYTES;
-        const Lds rb = opaque(row_base + tk);
         const int key0 = t * BK;
-        const bool idle = rows <= 0 || key0 > pos0 + rows - 1 || key0 + BK - 1 <= pos0 - p.window;
-        const Seen seen = seen_between(pos - key0 - p.window + 1, pos - key0);  // the keys that the lane's query sees
-        // some query of the block does not see all of the tile: what it does not see may be anything
-        const bool cut = key0 + BK - 1 > low || key0 <= low + BM - 1 - p.window;
-        bool found = false;
-        if (cut) {
-            if (any_special<T, BYTES, NW * 64>(tv, tid)) special = t;
-            __syncthreads();
-            found = special == t;
+        if (rows <= 0 || key0 > pos0 + rows - 1 || key0 + BK - 1 <= pos0 - p.window) continue;  // nothing that the wave's queries see
+        const bool cut = key0 + BK - 1 > pos0 || key0 <= pos0 + 31 - p.window;                 // not all that they see
+        const Seen seen = seen_between(pos - key0 - p.window + 1, pos - key0);                 // the lane's query's
+        const Lds tk = base + (t & 1) * 2 * BYTES;
+        const Lds rb = opaque(row_base + tk);
+        scores(rb);
+        if (cut) hide(seen);
+        if (first_tile) follow(true);
+        float sum = weights();
+        // The reference is followed only where weights outgrow it (the exponents of fp32 and bf16 have room),
+        // or where there is none yet.  Each query goes by its own weights: what a neighbour does changes no bit.
+        auto outgrown = [&](float x) { return x > kSlack || (m == -__builtin_inff() && x == x); };
+        if (__any(!first_tile && outgrown(sum))) {
+            const bool need = outgrown(sum + other_half(sum, lane));
+            scores(rb);
+            if (cut) hide(seen);
+            follow(need);
+            sum = weights();
         }
+        first_tile = false;
+        l += sum;
         Op<T> pr[BK / 16];
-        if (!idle) {
-            f32x16 s[BK / 32];
 #pragma unroll
-            for (int h = 0; h < BK / 32; ++h) {
-                s[h] = zero16();
+        for (int c = 0; c < BK / 16; ++c) pr[c] = op_of<T>(s[c / 2], c % 2);
+        const Lds cb = opaque(col_base + tk + BYTES);
+        if (!FIRST && cut) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) mma(s[h], L::row_op(rb, 32 * h, ks), q[ks]);
+            for (int dt = 0; dt < DT; ++dt) {
+                const f32x16 add = special_sum<T, D, BK>(cb, dt, seen, g, false);
+#pragma unroll
+                for (int ks = 0; ks < BK / 16; ++ks) mma(o[dt], finite_part<T>(L::col_op(cb, 16 * ks, dt)), pr[ks]);
+                o[dt] += add;
             }
-            if (cut) {
-#pragma unroll
-                for (int h = 0; h < BK / 32; ++h)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[h][i] = seen(32 * h + acc_row(i, g)) ? s[h][i] : -__builtin_inff();
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int h = 0; h < BK / 32; ++h)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[h][i]);
-            top = fmaxf(top, other_half(top, lane)) * p.scale_log2;
-            if (__any(top > m + kSlack)) {
-                const float next = fmaxf(m, top), f = next == m ? 1.f : __builtin_amdgcn_exp2f(m - next);
-                m = next;
-                l *= f;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) o[dt] *= f;
-            }
-            const float ref = m == -__builtin_inff() ? 0.f : m;  // nothing seen yet: all scores are -inf
-#pragma unroll
-            for (int h = 0; h < BK / 32; ++h) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[h][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], p.scale_log2, -ref));
-                    l += s[h][i];
-                }
-                pr[2 * h] = op_of<T>(s[h], 0);
-                pr[2 * h + 1] = op_of<T>(s[h], 1);
-            }
+            continue;
         }
-        if (found) {
-            if (!idle) {
-                f32x16 add[DT];
-                special_sums<T, D, BK>(add, col_base + tv, seen, g, false);
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt) o[dt] += add[dt];
-            }
-            __syncthreads();
-            clear_special<T, BYTES, NW * 64>(tv, tid);
-            __syncthreads();
-        }
-        if (!idle) {
-            const Lds cb = opaque(col_base + tv);
+        for (int ks = 0; ks < BK / 16; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < BK / 16; ++ks)
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) mma(o[dt], L::col_op(cb, 16 * ks, dt), pr[ks]);
-        }
+            for (int dt = 0; dt < DT; ++dt) mma(o[dt], L::col_op(cb, 16 * ks, dt), pr[ks]);
     }
-    if (rows <= 0) return;
+    bool any = false;
+    if (FIRST) {
+        float sum = 0.f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum = watch(sum, o[dt][i]);
+        const bool again = __any(sum != 0.f);
+        if (again) *flag = 1;
+        lds_barrier();
+        any = *flag != 0;
+        if (again) return any;
+    } else {
+        lds_barrier();
+    }
+    if (rows <= 0) return any;
     l += other_half(l, lane);
-    if ((lane & 31) >= rows) return;
-    const int64_t token = w.s.q0 + mine + (lane & 31);
+    const int64_t row0 = (w.s.q0 + mine) * p.heads + head, row = row0 + (int64_t)(lane & 31) * p.heads;
+    const bool live = (lane & 31) < rows;
     if (gridDim.y > 1) {
-        const int64_t row = token * p.heads + head, at = (int64_t)blockIdx.y * a.parts.rows + row;
-        store_column<float, D>(a.parts.o + at * D, o, 1.f, g);
-        if (g == 0) a.parts.ml[at] = float2{m, l};
-        return;
+        if (live) {
+            const int64_t at = (int64_t)blockIdx.y * a.parts.rows + row;
+            store_column<float, D>(a.parts.o + at * D, o, 1.f, g);
+            if (g == 0) a.parts.ml[at] = float2{m, l};
+        }
+        return any;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store_column<T, D>(reinterpret_cast<T*>(a.o) + (token * p.heads + head) * D, o, inv, g);
-    if (a.lse && g == 0) a.lse[token * p.heads + head] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && live && g == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    store_rows<T, D>(base + wave * 32 * L::kRow, (char*)a.o + row0 * L::kRow, (int64_t)p.heads * L::kRow, rows, o, l == 0.f ? 0.f : 1.f / l, lane);
+    return any;
+}
+// a call of its own, so that the kernel keeps its registers to the first form
+template <typename T, int D, int NW>
+__device__ __attribute__((noinline)) void fwd_again(FwdParams a, Lds base) {
+    fwd_block<T, D, NW, false>(a, base, nullptr);
+}
+
+template <typename T, int D, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void fwd_kernel(FwdParams a) {
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * kKeys<T> * Tile<T, D>::kRow];
+    __shared__ int any_again;
+    if (threadIdx.x == 0) any_again = 0;
+    if (fwd_block<T, D, NW, true>(a, lds_of(lds), &any_again)) {
+        __syncthreads();
+        fwd_again<T, D, NW>(a, lds_of(lds));
+    }
 }
 
 // Joins parts: a workgroup a row, groups of its threads taking the row's parts in turn.
