@@ -357,31 +357,42 @@ struct Seq {
 };
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// Blocks of `rows` tokens of the packed sequences, counted through: sequence and block of the
-// `index`th one, or false behind the last.  Every wave looks for itself, 64 sequences at a time.
-__device__ __forceinline__ bool find_block(const int64_t* cu, int64_t n, int64_t total, int rows, int64_t index, int lane,
-                                           int64_t* seq, int* block) {
+// Blocks of `rows` tokens of the packed sequences, counted through: sequence and block of the `index`th one,
+// or false behind the last.  Up to 64 sequences are counted from the longest to the shortest, so that long ones
+// do not start late.  Every wave looks for itself, 64 sequences at a time.
+__device__ __forceinline__ bool find_block(const int64_t* cu, int64_t n, int64_t total, int rows, unsigned index, int lane,
+                                           int64_t* seq, int* block, int* blocks) {
     int64_t before = 0;
     for (int64_t base = 0; base < n; base += 64) {
-        int64_t mine = 0;
+        int mine = 0;
         if (base + lane < n) {
             const int64_t lo = clamp64(cu[base + lane], 0, total), hi = clamp64(cu[base + lane + 1], lo, total);
-            mine = (hi - lo + rows - 1) / rows;
+            mine = (int)((hi - lo + rows - 1) / rows);
         }
-        int64_t sum = mine;
+        int64_t first = before;  // blocks before the lane's
+        if (n <= 64) {
+            for (int j = 0; j < (int)n; ++j) {
+                const int other = __builtin_amdgcn_readlane(mine, j);
+                first += other > mine || (other == mine && j < lane) ? other : 0;
+            }
+        } else {
+            int64_t sum = mine;
 #pragma unroll
-        for (int s = 1; s < 64; s *= 2) {
-            const int64_t up = __shfl_up(sum, s);
-            if (lane >= s) sum += up;
+            for (int s = 1; s < 64; s *= 2) {
+                const int64_t up = __shfl_up(sum, s);
+                if (lane >= s) sum += up;
+            }
+            first += sum - mine;
+            before += __shfl(sum, 63);
         }
-        const uint64_t here = __ballot(before + sum > index);
+        const uint64_t here = __ballot(first <= index && index < first + mine);
         if (here) {
             const int at = __builtin_ctzll(here);
             *seq = base + at;
-            *block = (int)(index - before - __shfl(sum - mine, at));
+            *block = (int)(index - __shfl(first, at));
+            *blocks = __shfl(mine, at);
             return true;
         }
-        before += __shfl(sum, 63);
     }
     return false;
 }
@@ -420,12 +431,14 @@ __device__ __forceinline__ bool find_work(const Shape& p, int rows, int per_grou
     const unsigned per = (p.blocks + (1u << p.slice_bits) - 1) >> p.slice_bits, each = per * per_group;
     const unsigned slice = r / each * 8 + x, group = slice >> p.slice_bits;
     const unsigned in = r % each, nth = in / per_group;
-    const unsigned index = ((last_first ? per - 1 - nth : nth) << p.slice_bits) + (slice & ((1u << p.slice_bits) - 1));
+    const unsigned index = ((last_first && !p.cu_q ? per - 1 - nth : nth) << p.slice_bits) + (slice & ((1u << p.slice_bits) - 1));
     if (group >= p.all_groups || index >= (unsigned)p.blocks) return false;
     w->head = (int)(group % (unsigned)p.groups) * per_group + in % per_group;
     if (p.cu_q) {
         int64_t seq;
-        if (!find_block(keys ? p.cu_k : p.cu_q, p.n, keys ? p.tk : p.tq, rows, index, lane, &seq, &w->block)) return false;
+        int blocks;
+        if (!find_block(keys ? p.cu_k : p.cu_q, p.n, keys ? p.tk : p.tq, rows, index, lane, &seq, &w->block, &blocks)) return false;
+        if (last_first) w->block = blocks - 1 - w->block;
         w->s = packed_seq(p.cu_q, p.cu_k, seq, p.tq, p.tk);
     } else {
         const int64_t n = group / (unsigned)p.groups;

@@ -185,7 +185,7 @@ __device__ __attribute__((noinline)) void dq_again(BwdParams a, Lds base) {
 }
 
 template <typename T, int D, int NW>
-__global__ __launch_bounds__(NW * 64, D * sizeof(T) > 256 ? 1 : 2) void dq_kernel(BwdParams a) {
+__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : sizeof(T) == 4 ? 1 : 2) void dq_kernel(BwdParams a) {
     __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * kKeys<T> * Tile<T, D>::kRow];
     __shared__ int flag;
     if (threadIdx.x == 0) flag = 0;
@@ -363,7 +363,7 @@ __device__ __attribute__((noinline)) void dkv_again(BwdParams a, Lds base) {
 }
 
 template <typename T, int D, int NW>
-__global__ __launch_bounds__(NW * 64, D * sizeof(T) > 256 ? 1 : 2) void dkv_kernel(BwdParams a) {
+__global__ __launch_bounds__(NW * 64, D * sizeof(T) > 256 ? 1 : D * sizeof(T) > 128 ? 2 : 3) void dkv_kernel(BwdParams a) {
     __shared__ __attribute__((aligned(1024))) char lds[kDkvLds<T, D, NW>];
     __shared__ int flag;
     if (threadIdx.x == 0) flag = 0;

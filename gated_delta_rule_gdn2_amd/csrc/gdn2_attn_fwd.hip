@@ -217,7 +217,7 @@ __device__ __attribute__((noinline)) void fwd_again(FwdParams a, Lds base) {
 }
 
 template <typename T, int D, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void fwd_kernel(FwdParams a) {
+__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void fwd_kernel(FwdParams a) {
     __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * kKeys<T> * Tile<T, D>::kRow];
     __shared__ int any_again;
     if (threadIdx.x == 0) any_again = 0;
