@@ -32,7 +32,7 @@ from . import _DTYPES, _load, _ptr
 from .block import _bytes, _F32, _in, _launch, _offsets, _on_gpu, _opt, _out, _tokens, _workspace
 
 __all__ = ["attn_fwd", "attn_fwd_varlen", "attn_fwd_workspace_bytes", "attn_fwd_varlen_workspace_bytes", "attn_bwd",
-           "attn_bwd_varlen", "attn_bwd_workspace_bytes", "attn_step", "attn_step_workspace_bytes", "rotary",
+           "attn_bwd_varlen", "attn_bwd_workspace_bytes", "attn_bwd_varlen_workspace_bytes", "attn_step", "attn_step_workspace_bytes", "rotary",
            "rotary_frequencies", "rms_norm", "rms_norm_fp8", "rms_norm_bwd", "rms_norm_bwd_workspace_bytes"]
 
 
@@ -45,7 +45,8 @@ def _declare(lib):
             ("attn_fwd_varlen_workspace_bytes", [I64] * 7 + [I32], SZ),
             ("attn_bwd", [P] * 9 + [I64] * 10 + [F, I32, P, SZ, P], I32),
             ("attn_bwd_varlen", [P] * 11 + [I64] * 10 + [F, I32, P, SZ, P], I32),
-            ("attn_bwd_workspace_bytes", [I64] * 2, SZ),
+            ("attn_bwd_workspace_bytes", [I64] * 7 + [I32], SZ),
+            ("attn_bwd_varlen_workspace_bytes", [I64] * 7 + [I32], SZ),
             ("attn_step", [P] * 7 + [I64] * 9 + [F, I32, P, SZ, P], I32),
             ("attn_step_workspace_bytes", [I64] * 6 + [I32], SZ),
             ("rotary", [P] * 6 + [I64] * 10 + [I32, I32, F, I32, P], I32),
@@ -153,9 +154,14 @@ def attn_fwd_varlen_workspace_bytes(N, total_T, total_S, H, G, d, window=None, d
     return int(_load().gdn2_attn_fwd_varlen_workspace_bytes(N, total_T, total_S, H, G, d, _window(window), _DTYPES[dtype]))
 
 
-def attn_bwd_workspace_bytes(queries, H) -> int:
-    """Device workspace (bytes) that attn_bwd and attn_bwd_varlen need for all their queries (B T, or total_T)."""
-    return int(_load().gdn2_attn_bwd_workspace_bytes(queries, H))
+def attn_bwd_workspace_bytes(B, T, S, H, G, d, window=None, dtype=torch.bfloat16) -> int:
+    """Device workspace (bytes) that attn_bwd needs for these sizes (0: none)."""
+    return int(_load().gdn2_attn_bwd_workspace_bytes(B, T, S, H, G, d, _window(window), _DTYPES[dtype]))
+
+
+def attn_bwd_varlen_workspace_bytes(N, total_T, total_S, H, G, d, window=None, dtype=torch.bfloat16) -> int:
+    """Device workspace (bytes) that attn_bwd_varlen needs for these sizes (0: none)."""
+    return int(_load().gdn2_attn_bwd_varlen_workspace_bytes(N, total_T, total_S, H, G, d, _window(window), _DTYPES[dtype]))
 
 
 def _bwd(name, d_o, q, k, v, o, lse, lead_q, lead_k, sizes, offsets, window, scale, grads, workspace, code, dev):
@@ -168,10 +174,11 @@ def _bwd(name, d_o, q, k, v, o, lse, lead_q, lead_k, sizes, offsets, window, sca
     out["dq"] = _out("dq", out.get("dq"), qs, q.dtype, dev, q)
     out["dk"] = _out("dk", out.get("dk"), ks, q.dtype, dev, k)
     out["dv"] = _out("dv", out.get("dv"), ks, q.dtype, dev, v)
-    need = attn_bwd_workspace_bytes(math.prod(lead_q), H)
+    w = _window(window)
+    need = _bytes(name + "_workspace_bytes", dev, *sizes, *dims, w, code)
     ws, ws_bytes, keep = _parts(workspace, need, dev)
     _launch(name, dev, first, *ptrs, *kept, out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(), *offsets, *sizes,
-            *dims, *strides, _window(window), _scale(scale, d), code, ws, ws_bytes)
+            *dims, *strides, w, _scale(scale, d), code, ws, ws_bytes)
     return out
 
 
@@ -186,7 +193,8 @@ def attn_bwd(d_o, q, k, v, o, lse, *, window=None, scale=None, grads=None, works
 
 
 def attn_bwd_varlen(d_o, q, k, v, o, lse, cu_seqlens, *, cu_seqlens_k=None, window=None, scale=None, grads=None, workspace=None):
-    """attn_bwd for attn_fwd_varlen.  Gradients of tokens of no sequence are left as they were."""
+    """attn_bwd for attn_fwd_varlen.  Gradients of tokens of no sequence are left as they were.
+    ``workspace``: at least attn_bwd_varlen_workspace_bytes + 16."""
     code, dev = _on_gpu("attn_bwd_varlen", q, 3, "[total_T,H,d]")
     _keys(k, 3, "[total_S,G,d]")
     T, S = q.shape[0], k.shape[0]

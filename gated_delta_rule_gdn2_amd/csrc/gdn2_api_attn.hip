@@ -120,21 +120,21 @@ gdn2_status_t attn_bwd(gdn2::AttnArgs a, gdn2_dtype_t dtype, void* workspace, si
     const gdn2_status_t st = check_attn(a, dtype, &b);
     if (st != GDN2_OK) return st;
     if ((b.o && (!a.o || !a.d_o || !a.lse || !a.dq)) || (b.kv && (!a.dk || !a.dv))) return GDN2_ERR_NULL;
-    const int64_t need = gdn2::attn_stats_bytes(b.tokens_q, a.H);
+    a.cus = cus_or_default();
+    const int64_t need = b.tokens_q ? (int64_t)gdn2::attn_bwd_workspace_bytes(a) : 0;
     if (need && (!workspace || workspace_bytes < (size_t)need)) return GDN2_ERR_WORKSPACE;
     if (!aligned_to(workspace, 16)) return GDN2_ERR_MISALIGNED;
-    a.stats = static_cast<float*>(workspace);
     const int64_t cu = a.cu_q ? (a.N + 1) * 8 : 0;
     if (any_overlap({range_of(a.dq, b.o), range_of(a.dk, b.kv), range_of(a.dv, b.kv), range_of(workspace, need)},
                     {range_of(a.q, b.q), range_of(a.k, b.k), range_of(a.v, b.v), range_of(a.o, b.o), range_of(a.d_o, b.o),
                      range_of(a.lse, b.lse), range_of(a.cu_q, cu), range_of(a.cu_k, cu)}))
         return GDN2_ERR_ALIAS;
     if (b.tokens_q == 0 && b.tokens_k == 0) return GDN2_OK;
-    return gdn2::launch_attn_bwd(a) == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+    return gdn2::launch_attn_bwd(a, workspace) == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
 }
 
-size_t attn_fwd_workspace(bool packed, int64_t N, int64_t T, int64_t S, int64_t H, int64_t G, int64_t d, int64_t window,
-                          gdn2_dtype_t dtype) {
+size_t attn_workspace(size_t (*bytes)(const gdn2::AttnArgs&), bool packed, int64_t N, int64_t T, int64_t S, int64_t H, int64_t G,
+                      int64_t d, int64_t window, gdn2_dtype_t dtype) {
     static const int64_t cu[2] = {0, 0};  // never read: says that sequences are packed
     gdn2::AttnArgs a{};
     a.N = N, a.T = T, a.S = S, a.H = H, a.G = G, a.d = d, a.window = window, a.scale = 1.f;
@@ -145,7 +145,7 @@ size_t attn_fwd_workspace(bool packed, int64_t N, int64_t T, int64_t S, int64_t 
     AttnBytes b;
     if (check_attn(a, dtype, &b) != GDN2_OK || b.tokens_q == 0) return 0;
     a.cus = cus_or_default();
-    return gdn2::attn_fwd_workspace_bytes(a);
+    return bytes(a);
 }
 
 // Tokens of `width` bytes each, `stride` bytes apart: whether two such tensors share a byte.  Parts of
@@ -220,10 +220,14 @@ gdn2_status_t rms_norm(const gdn2::RmsArgs& a, gdn2_dtype_t dtype, gdn2_dtype_t 
 
 extern "C" {
 
-size_t gdn2_attn_bwd_workspace_bytes(int64_t queries, int64_t H) {
-    int64_t n;
-    if (queries < 1 || H < 1 || !mul_ok(queries, H, &n) || n > INT64_MAX / 16) return 0;
-    return (size_t)gdn2::attn_stats_bytes(queries, H);
+size_t gdn2_attn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t S, int64_t H, int64_t G, int64_t d, int64_t window,
+                                     gdn2_dtype_t dtype) {
+    return attn_workspace(gdn2::attn_bwd_workspace_bytes, false, B, T, S, H, G, d, window, dtype);
+}
+
+size_t gdn2_attn_bwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t total_S, int64_t H, int64_t G, int64_t d,
+                                            int64_t window, gdn2_dtype_t dtype) {
+    return attn_workspace(gdn2::attn_bwd_workspace_bytes, true, N, total_T, total_S, H, G, d, window, dtype);
 }
 
 gdn2_status_t gdn2_attn_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -231,7 +235,7 @@ gdn2_status_t gdn2_attn_bwd(const void* d_o, const void* q, const void* k, const
                             int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t window, float scale,
                             gdn2_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
     const gdn2::AttnArgs a{q, k, v, const_cast<void*>(o), const_cast<float*>(lse), B, T, S, H, G, d, q_stride, k_stride,
-                           v_stride, window, scale, dtype == GDN2_DTYPE_BF16, nullptr, nullptr, stream, 0, d_o, dq, dk, dv, nullptr};
+                           v_stride, window, scale, dtype == GDN2_DTYPE_BF16, nullptr, nullptr, stream, 0, d_o, dq, dk, dv};
     return attn_bwd(a, dtype, workspace, workspace_bytes);
 }
 
@@ -244,7 +248,7 @@ gdn2_status_t gdn2_attn_bwd_varlen(const void* d_o, const void* q, const void* k
     if (!aligned_to(cu_seqlens, 8) || !aligned_to(cu_seqlens_k, 8)) return GDN2_ERR_MISALIGNED;
     const gdn2::AttnArgs a{q, k, v, const_cast<void*>(o), const_cast<float*>(lse), N, total_T, total_S, H, G, d, q_stride,
                            k_stride, v_stride, window, scale, dtype == GDN2_DTYPE_BF16, cu_seqlens, cu_seqlens_k, stream, 0,
-                           d_o, dq, dk, dv, nullptr};
+                           d_o, dq, dk, dv};
     return attn_bwd(a, dtype, workspace, workspace_bytes);
 }
 
@@ -270,12 +274,12 @@ gdn2_status_t gdn2_attn_fwd_varlen(const void* q, const void* k, const void* v, 
 
 size_t gdn2_attn_fwd_workspace_bytes(int64_t B, int64_t T, int64_t S, int64_t H, int64_t G, int64_t d, int64_t window,
                                      gdn2_dtype_t dtype) {
-    return attn_fwd_workspace(false, B, T, S, H, G, d, window, dtype);
+    return attn_workspace(gdn2::attn_fwd_workspace_bytes, false, B, T, S, H, G, d, window, dtype);
 }
 
 size_t gdn2_attn_fwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t total_S, int64_t H, int64_t G, int64_t d,
                                             int64_t window, gdn2_dtype_t dtype) {
-    return attn_fwd_workspace(true, N, total_T, total_S, H, G, d, window, dtype);
+    return attn_workspace(gdn2::attn_fwd_workspace_bytes, true, N, total_T, total_S, H, G, d, window, dtype);
 }
 
 size_t gdn2_attn_step_workspace_bytes(int64_t N, int64_t H, int64_t G, int64_t d, int64_t C, int64_t window, gdn2_dtype_t dtype) {

@@ -17,6 +17,7 @@
 namespace gdn2 {
 namespace attn {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define GDN2_LDS __attribute__((address_space(3)))
 
@@ -255,6 +256,48 @@ __device__ __forceinline__ void tile_barrier() {
     __syncthreads();
 }
 
+// The same for a wave's own loads and LDS.
+__device__ __forceinline__ void own_tile_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Sums over SW waves, in the order of the waves, of the 32 x D that each holds: each wave gets a part of
+// them, columns 8 (wave kUnits + u) + 4 g + e of row l % 32.  Takes kBytes of LDS, where nobody reads any
+// more; whoever writes there next waits for every wave first.
+template <int D, int SW> struct WaveSums {
+    static constexpr int kUnits = D / 8 / SW, kBytes = SW * D / 8 * 1024;
+    f32x4 v[kUnits];
+    __device__ __forceinline__ void add(Lds lds, const f32x16 (&c)[D / 32], float factor, int wave, int lane) {
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+            f32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = c[u / 4][4 * (u % 4) + e] * factor;
+            *(GDN2_LDS f32x4*)(uintptr_t)(lds + ((wave * (D / 8) + u) * 64 + lane) * 16) = x;
+        }
+        lds_barrier();
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const Lds at = lds + ((wave * kUnits + u) * 64 + lane) * 16;
+            v[u] = lds_get<f32x4>(at);
+#pragma unroll
+            for (int w = 1; w < SW; ++w) v[u] += lds_get<f32x4>(at + w * (D / 8) * 1024);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void store(T* row, float factor, int wave, int g) const {
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = v[u][e] * factor;
+            store_vec_any<T, 4>(row + 8 * (wave * kUnits + u) + 4 * g, f);
+        }
+    }
+};
+
 // zero times x, added to `sum`: a NaN once anything was not finite
 __device__ __forceinline__ float watch(float sum, float x) { return __builtin_fmaf(x, 0.f, sum); }
 
@@ -488,6 +531,16 @@ struct Owned {
     int64_t n, total;
     int heads;
 };
+// whether a token belongs to a sequence; each lane asks for its own
+__device__ __forceinline__ bool owned_by_lane(const Owned& o, int64_t token) {
+    if (!o.cu) return true;
+    bool found = false;
+    for (int64_t n = 0; n < o.n && !found; ++n) {
+        const int64_t lo = clamp64(o.cu[n], 0, o.total);
+        found = lo <= token && token < clamp64(o.cu[n + 1], lo, o.total);
+    }
+    return found;
+}
 hipError_t launch_join(const Parts& p, void* o, float* lse, int64_t d, bool bf16_out, const Owned& owned, hipStream_t stream);
 
 }  // namespace attn

@@ -32,22 +32,28 @@ struct BwdParams {
     float* lse2;      // [heads][tokens]: lse in base 2
     float* no_delta;  // [heads][tokens]: -delta, what dP starts from
     int64_t tokens;   // queries in all
+    float* parts;     // of more than one part: [part][dk, dv][keys][key heads][d], unscaled
+    int64_t keys;     // keys in all
     Shape p;
 };
 
 // ---- dq ---------------------------------------------------------------------------------------
 
-template <typename T> constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;  // keys in a tile
+template <typename T, int SW> constexpr int kKeys = sizeof(T) == 2 && SW == 1 ? 64 : 32;  // keys in a tile
+template <typename T, int D, int SW> constexpr int kDqLds = SW * 2 * 2 * kKeys<T, SW> * Tile<T, D>::kRow;
 
 // A workgroup takes 32 queries of one head a wave; keys and values come by in tiles.  S^T = K Q^T and
-// dP^T = V d_O^T have keys in the rows, so that dS is the next product's operand (dQ^T = K^T dS^T).  Returns
-// whether some wave gave up; it has written nothing then.
-template <typename T, int D, int NW, bool FIRST>
+// dP^T = V d_O^T have keys in the rows, so that dS is the next product's operand (dQ^T = K^T dS^T).
+// SW > 1: all waves share 32 queries; each takes every SWth tile of keys, with tiles of its own in LDS, and
+// their sums are joined at the end.  Returns whether some wave gave up; it has written nothing then.
+template <typename T, int D, int NW, int SW, bool FIRST>
 __device__ __forceinline__ bool dq_block(const BwdParams& a, Lds base, int* flag) {
     typedef Tile<T, D> L;
-    constexpr int BK = kKeys<T>, KS = D / 16, DT = D / 32, BM = NW * 32, BYTES = BK * L::kRow;
+    static_assert(SW == 1 || SW == NW, "each wave its own queries, or all the same");
+    constexpr int BK = kKeys<T, SW>, KS = D / 16, DT = D / 32, BM = NW / SW * 32, BYTES = BK * L::kRow;
     const int lane = threadIdx.x & 63, g = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = SW == 1 ? all_waves : 0, part = SW == 1 ? 0 : all_waves;
     const Shape& p = a.p;
     Work w;
     if (!find_work(p, BM, p.heads / p.groups, true, false, lane, &w)) return false;
@@ -65,11 +71,12 @@ __device__ __forceinline__ bool dq_block(const BwdParams& a, Lds base, int* flag
     const uint32_t o_stride = (uint32_t)p.heads * L::kRow;
 
     const Lds row_base = L::row_base(lane), col_base = L::col_base(lane);
+    auto place = [&](int t) { return base + (part * 2 + (t / SW & 1)) * 2 * BYTES; };
     auto stage = [&](int t) {
-        const Lds at = base + (t & 1) * 2 * BYTES;
+        const Lds at = place(t);
         const int left = min(BK, lk - t * BK);
-        L::template stage<BK, NW>(at, kp + (int64_t)t * BK * p.k_stride, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
-        L::template stage<BK, NW>(at + BYTES, vp + (int64_t)t * BK * p.v_stride, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
+        L::template stage<BK, NW / SW>(at, kp + (int64_t)t * BK * p.k_stride, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
+        L::template stage<BK, NW / SW>(at + BYTES, vp + (int64_t)t * BK * p.v_stride, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
     };
     // queries, d_o and o: by way of the tiles' places in LDS, if they have room there, so that rows are read whole
     constexpr bool VIA = BM * L::kRow <= 2 * BYTES;
@@ -83,9 +90,10 @@ __device__ __forceinline__ bool dq_block(const BwdParams& a, Lds base, int* flag
         for (int e = 0; e < 8; ++e) delta = __builtin_fmaf(to_f32((T)x.v[e]), to_f32((T)y.v[e]), delta);
     };
     if constexpr (VIA) {
-        const Lds one = base + (t0 & 1) * 2 * BYTES, two = base + (~t0 & 1) * 2 * BYTES, own = row_base + wave * 32 * L::kRow;
-        L::template stage<BM, NW>(one, qp, q_span, p.q_stride, wave, lane);
-        L::template stage<BM, NW>(two, a.d_o + row0 * L::kRow, o_span, o_stride, wave, lane);
+        // (of the first wave, where waves have tiles of their own)
+        const Lds one = base + (t0 / SW & 1) * 2 * BYTES, two = base + (~(t0 / SW) & 1) * 2 * BYTES, own = row_base + wave * 32 * L::kRow;
+        L::template stage<BM, NW>(one, qp, q_span, p.q_stride, all_waves, lane);
+        L::template stage<BM, NW>(two, a.d_o + row0 * L::kRow, o_span, o_stride, all_waves, lane);
         tile_barrier();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -93,11 +101,12 @@ __device__ __forceinline__ bool dq_block(const BwdParams& a, Lds base, int* flag
             d_o[ks] = L::row_op(own + two, 0, ks);
         }
         lds_barrier();
-        if (t0 < t1) stage(t0);
-        L::template stage<BM, NW>(two, a.o + row0 * L::kRow, o_span, o_stride, wave, lane);
+        if (t0 + part < t1) stage(t0 + part);
+        L::template stage<BM, NW>(two, a.o + row0 * L::kRow, o_span, o_stride, all_waves, lane);
         tile_barrier();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) dot(d_o[ks], L::row_op(own + two, 0, ks));
+        if (SW > 1) lds_barrier();
     } else {
         const auto rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(qp), 0, q_span, 0x00020000);
         const auto rd = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.d_o + row0 * L::kRow), 0, o_span, 0x00020000);
@@ -109,27 +118,28 @@ __device__ __forceinline__ bool dq_block(const BwdParams& a, Lds base, int* flag
             d_o[ks] = global_op<T>(rd, row * o_stride, ks, g);
             dot(d_o[ks], global_op<T>(ro, row * o_stride, ks, g));
         }
-        if (t0 < t1) stage(t0);
+        if (t0 + part < t1) stage(t0 + part);
     }
     delta += other_half(delta, lane);
     float lse = 0.f;
     if ((lane & 31) < rows) {
         lse = a.lse[row0 + (int64_t)(wave * 32 + (lane & 31)) * p.heads] * kLog2e;
         const int64_t at = (int64_t)head * a.tokens + w.s.q0 + mine + (lane & 31);
-        if (g == 0) a.lse2[at] = lse;
-        else a.no_delta[at] = -delta;
+        if (part == 0 && g == 0) a.lse2[at] = lse;
+        if (part == 0 && g == 1) a.no_delta[at] = -delta;
     }
     f32x16 dq[DT];
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) dq[dt] = zero16();
     bool again = false;
-    for (int t = t0; t < t1; ++t) {
-        tile_barrier();
-        if (t + 1 < t1) stage(t + 1);
+    for (int t = t0 + part; t < t1; t += SW) {
+        if (SW == 1) tile_barrier();
+        else own_tile_wait();
+        if (t + SW < t1) stage(t + SW);
         const int key0 = t * BK;
         if (rows <= 0 || key0 > pos0 + rows - 1 || key0 + BK - 1 <= pos0 - p.window) continue;  // nothing that the wave's queries see
         const bool cut = key0 + BK - 1 > pos0 || key0 <= pos0 + 31 - p.window;                 // not all that they see
-        const Lds tk = base + (t & 1) * 2 * BYTES, rk = opaque(row_base + tk), rv = opaque(row_base + tk + BYTES);
+        const Lds tk = place(t), rk = opaque(row_base + tk), rv = opaque(row_base + tk + BYTES);
         const Seen seen = seen_between(pos - key0 - p.window + 1, pos - key0);  // the lane's query's
         Op<T> ds[BK / 16];
         float sum = watch(watch(0.f, lse), delta);
@@ -174,24 +184,33 @@ __device__ __forceinline__ bool dq_block(const BwdParams& a, Lds base, int* flag
     }
     if (FIRST && again) *flag = 1;
     lds_barrier();
+    const bool any = FIRST && *flag != 0;
+    if constexpr (SW > 1) {
+        if (any) return any;
+        static_assert(WaveSums<D, SW>::kBytes <= kDqLds<T, D, SW>, "room for the sums");
+        WaveSums<D, SW> sums;
+        sums.add(base, dq, p.scale, part, lane);
+        if ((lane & 31) < rows) sums.template store<T>((T*)a.dq + (row0 + (int64_t)(lane & 31) * p.heads) * D, 1.f, part, g);
+        return any;
+    }
     if (rows > 0 && !again)
         store_rows<T, D>(base + wave * 32 * L::kRow, (char*)a.dq + (row0 + (int64_t)wave * 32 * p.heads) * L::kRow, o_stride, rows, dq, p.scale, lane);
-    return FIRST && *flag != 0;
+    return any;
 }
 // a call of its own, so that the kernel keeps its registers to the first form
-template <typename T, int D, int NW>
+template <typename T, int D, int NW, int SW>
 __device__ __attribute__((noinline)) void dq_again(BwdParams a, Lds base) {
-    dq_block<T, D, NW, false>(a, base, nullptr);
+    dq_block<T, D, NW, SW, false>(a, base, nullptr);
 }
 
-template <typename T, int D, int NW>
-__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : sizeof(T) == 4 ? 1 : 2) void dq_kernel(BwdParams a) {
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * kKeys<T> * Tile<T, D>::kRow];
+template <typename T, int D, int NW, int SW>
+__global__ __launch_bounds__(NW * 64, SW > 1 ? (kDqLds<T, D, SW> > 80000 ? 1 : 2) : D == 64 ? 3 : sizeof(T) == 4 ? 1 : 2) void dq_kernel(BwdParams a) {
+    __shared__ __attribute__((aligned(1024))) char lds[kDqLds<T, D, SW>];
     __shared__ int flag;
     if (threadIdx.x == 0) flag = 0;
-    if (dq_block<T, D, NW, true>(a, lds_of(lds), &flag)) {
+    if (dq_block<T, D, NW, SW, true>(a, lds_of(lds), &flag)) {
         __syncthreads();
-        dq_again<T, D, NW>(a, lds_of(lds));
+        dq_again<T, D, NW, SW>(a, lds_of(lds));
     }
 }
 
@@ -200,19 +219,22 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : sizeof(T) == 4 ? 1 : 2) void
 constexpr int kQueries = 32;  // queries in a tile
 // LDS of a tile: queries, d_o, and of each lse in base 2 and -delta; and of the whole workgroup
 template <typename T, int D> constexpr int kStage = 2 * kQueries * Tile<T, D>::kRow + 1024;
-template <typename T, int D, int NW> constexpr int kDkvLds = 2 * kStage<T, D> + NW * 32 * Tile<T, D>::kRow;
+template <typename T, int D, int NW, int SW> constexpr int kDkvLds = SW * 2 * kStage<T, D> + NW / SW * 32 * Tile<T, D>::kRow;
 
 // A workgroup takes NW * 32 keys of one key head, a wave 32; the queries that see them come by in tiles, the
 // heads that share them one after the other.  S = Q K^T and dP = d_O V^T have queries in the rows, so that P and
 // dS are the next products' operands as they stand (dV^T = d_O^T P, dK^T = Q^T dS).  Keys stay in registers,
 // values in LDS: with both in registers there is one wave a SIMD, which took 1.65 ms at 8 x 4096 tokens, 16 heads
 // of 128 sharing 8, window 2048, against 1.05 ms.
-template <typename T, int D, int NW, bool FIRST>
+// SW > 1: all waves share 32 keys; each takes every SWth tile of queries, as in dq_block.
+template <typename T, int D, int NW, int SW, bool FIRST>
 __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* flag) {
     typedef Tile<T, D> L;
-    constexpr int KS = D / 16, DT = D / 32, BN = NW * 32, BQ = kQueries, BYTES = BQ * L::kRow, STAGE = kStage<T, D>;
+    static_assert(SW == 1 || SW == NW, "each wave its own keys, or all the same");
+    constexpr int KS = D / 16, DT = D / 32, BN = NW / SW * 32, BQ = kQueries, BYTES = BQ * L::kRow, STAGE = kStage<T, D>;
     const int lane = threadIdx.x & 63, g = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = SW == 1 ? all_waves : 0, part = SW == 1 ? 0 : all_waves;
     const Shape& p = a.p;
     Work w;
     if (!find_work(p, BN, 1, false, true, lane, &w)) return false;
@@ -221,14 +243,14 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
     const int first = w.block * BN, mine = first + wave * 32, rows = min(32, lk - mine);
     const int64_t off = (int64_t)lk - lq;  // where query 0 stands
 
-    const Lds row_base = L::row_base(lane), col_base = L::col_base(lane), tv = base + 2 * STAGE;
+    const Lds row_base = L::row_base(lane), col_base = L::col_base(lane), tv = base + SW * 2 * STAGE;
     // keys come by way of the tiles' places in LDS
     Op<T> k[KS];
     {
         const int left = min(BN, lk - first);
         static_assert(BN * L::kRow <= 2 * STAGE, "room for the keys");
-        L::template stage<BN, NW>(base, a.k + (w.s.k0 + first) * p.k_stride + (int64_t)kv * L::kRow, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
-        L::template stage<BN, NW>(tv, a.v + (w.s.k0 + first) * p.v_stride + (int64_t)kv * L::kRow, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
+        L::template stage<BN, NW>(base, a.k + (w.s.k0 + first) * p.k_stride + (int64_t)kv * L::kRow, span(left, p.k_stride, L::kRow), p.k_stride, all_waves, lane);
+        L::template stage<BN, NW>(tv, a.v + (w.s.k0 + first) * p.v_stride + (int64_t)kv * L::kRow, span(left, p.v_stride, L::kRow), p.v_stride, all_waves, lane);
         tile_barrier();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) k[ks] = L::row_op(row_base + base + wave * 32 * L::kRow, 0, ks);
@@ -246,32 +268,41 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
     auto stage = [&](int h, int t, int buf) {
         const int head = kv * share + h, left = min(BQ, lq - t * BQ);
         const int64_t token = w.s.q0 + (int64_t)t * BQ;
-        const Lds at = base + buf * STAGE;
-        L::template stage<BQ, NW>(at, a.q + token * p.q_stride + (int64_t)head * L::kRow, span(left, p.q_stride, L::kRow), p.q_stride, wave, lane);
-        L::template stage<BQ, NW>(at + BYTES, a.d_o + token * o_stride + (int64_t)head * L::kRow, span(left, o_stride, L::kRow), o_stride, wave, lane);
+        const Lds at = base + (part * 2 + buf) * STAGE;
+        L::template stage<BQ, NW / SW>(at, a.q + token * p.q_stride + (int64_t)head * L::kRow, span(left, p.q_stride, L::kRow), p.q_stride, wave, lane);
+        L::template stage<BQ, NW / SW>(at + BYTES, a.d_o + token * o_stride + (int64_t)head * L::kRow, span(left, o_stride, L::kRow), o_stride, wave, lane);
         if (wave == 0)  // rows that are none repeat the last
             load_far_words_to_lds(at + 2 * BYTES, (g ? a.no_delta : a.lse2) + (int64_t)head * a.tokens + token + min(lane & 31, left - 1));
     };
-    const int count = t1 > t0 ? share * (t1 - t0) : 0;
+    // the workgroup's part of them
+    const int all = t1 > t0 ? share * (t1 - t0) : 0, per = (all + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int n0 = min(per * (int)blockIdx.y, all) + part, count = min(n0 - part + per, all);
     int h = 0, t = t0;
-    bool again = false;
-    if (count > 0) stage(h, t, 0);
-    for (int n = 0; n < count; ++n) {
-        tile_barrier();
-        int next_h = h, next_t = t + 1;
-        if (next_t == t1) {
-            next_t = t0;
-            ++next_h;
+    auto after = [&](int steps) {  // `steps` tiles on
+        t += steps;
+        while (t >= t1) {
+            t -= t1 - t0;
+            ++h;
         }
-        if (n + 1 < count) stage(next_h, next_t, (n + 1) & 1);
+    };
+    bool again = false;
+    if (n0 < count) {
+        after(n0);
+        stage(h, t, 0);
+    }
+    for (int n = n0; n < count; n += SW) {
+        if (SW == 1) tile_barrier();
+        else own_tile_wait();
         const int64_t place = off + (int64_t)t * BQ;  // of the tile's first query
         const int left = lq - t * BQ;                 // its queries
-        h = next_h;
-        t = next_t;
+        if (n + SW < count) {
+            after(SW);
+            stage(h, t, ((n - n0) / SW + 1) & 1);
+        }
         // no query of the tile sees a key of the wave's; or some query does not see some key, or is none
         if (rows <= 0 || place + BQ - 1 < mine || place > (int64_t)mine + 30 + p.window) continue;
         const bool cut = place < (int64_t)mine + 31 || place + BQ - 1 >= (int64_t)mine + p.window || left < BQ;
-        const Lds tq = base + (n & 1) * STAGE, ts = tq + 2 * BYTES + 16 * g;
+        const Lds tq = base + (part * 2 + ((n - n0) / SW & 1)) * STAGE, ts = tq + 2 * BYTES + 16 * g;
         const Lds rq = opaque(row_base + tq), ro = opaque(row_base + tq + BYTES), rv = opaque(row_base + tv + wave * 32 * L::kRow);
         f32x16 s = zero16(), dp;
 #pragma unroll
@@ -348,6 +379,23 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
     }
     if (FIRST && again) *flag = 1;
     lds_barrier();
+    const bool any = FIRST && *flag != 0;
+    if constexpr (SW > 1) {
+        if (any) return any;
+        static_assert(WaveSums<D, SW>::kBytes <= kDkvLds<T, D, NW, SW>, "room for the sums");
+        const int64_t at = ((w.s.k0 + mine + (lane & 31)) * p.groups + kv) * D, size = a.keys * p.groups * D;
+        const bool whole = gridDim.y == 1, live = (lane & 31) < rows;
+        float* parts = a.parts + 2 * blockIdx.y * size + at;
+        WaveSums<D, SW> sums;
+        sums.add(base, dk, whole ? p.scale : 1.f, part, lane);
+        if (live && whole) sums.template store<T>((T*)a.dk + at, 1.f, part, g);
+        else if (live) sums.template store<float>(parts, 1.f, part, g);
+        lds_barrier();
+        sums.add(base, dv, 1.f, part, lane);
+        if (live && whole) sums.template store<T>((T*)a.dv + at, 1.f, part, g);
+        else if (live) sums.template store<float>(parts + size, 1.f, part, g);
+        return any;
+    }
     if (rows > 0 && !again) {
         const int64_t at = ((w.s.k0 + mine) * p.groups + kv) * L::kRow, stride = (int64_t)p.groups * L::kRow;
         const Lds own = base + wave * 32 * L::kRow;
@@ -355,46 +403,124 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
         __builtin_amdgcn_wave_barrier();
         store_rows<T, D>(own, (char*)a.dv + at, stride, rows, dv, 1.f, lane);
     }
-    return FIRST && *flag != 0;
+    return any;
 }
-template <typename T, int D, int NW>
+template <typename T, int D, int NW, int SW>
 __device__ __attribute__((noinline)) void dkv_again(BwdParams a, Lds base) {
-    dkv_block<T, D, NW, false>(a, base, nullptr);
+    dkv_block<T, D, NW, SW, false>(a, base, nullptr);
 }
 
-template <typename T, int D, int NW>
-__global__ __launch_bounds__(NW * 64, D * sizeof(T) > 256 ? 1 : D * sizeof(T) > 128 ? 2 : 3) void dkv_kernel(BwdParams a) {
-    __shared__ __attribute__((aligned(1024))) char lds[kDkvLds<T, D, NW>];
+template <typename T, int D, int NW, int SW>
+__global__ __launch_bounds__(NW * 64, SW > 1 ? (kDkvLds<T, D, NW, SW> > 80000 ? 1 : 2) : D * sizeof(T) > 256 ? 1 : D * sizeof(T) > 128 ? 2 : 3) void dkv_kernel(BwdParams a) {
+    __shared__ __attribute__((aligned(1024))) char lds[kDkvLds<T, D, NW, SW>];
     __shared__ int flag;
     if (threadIdx.x == 0) flag = 0;
-    if (dkv_block<T, D, NW, true>(a, lds_of(lds), &flag)) {
+    if (dkv_block<T, D, NW, SW, true>(a, lds_of(lds), &flag)) {
         __syncthreads();
-        dkv_again<T, D, NW>(a, lds_of(lds));
+        dkv_again<T, D, NW, SW>(a, lds_of(lds));
     }
 }
 
+// Joins the parts of dk and dv, in their order: D / 4 threads a row.
 template <typename T, int D>
-hipError_t run_bwd(const BwdParams& b, hipStream_t stream) {
-    constexpr int NW = 4;
-    BwdParams x = b;
-    int64_t grid = deal(&x.p, x.p.tq, NW * 32, b.p.heads / b.p.groups);
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ parts, T* __restrict__ dk, T* __restrict__ dv,
+                                                   float scale, int64_t rows, int splits, Owned owned) {
+    const int64_t row = (int64_t)blockIdx.x * (1024 / D) + threadIdx.x / (D / 4);
+    const int64_t at = row * D + threadIdx.x % (D / 4) * 4, size = rows * D;
+    if (row >= rows || !owned_by_lane(owned, row / owned.heads)) return;
+    f32x4 sk{0.f, 0.f, 0.f, 0.f}, sv = sk;
+    for (int i = 0; i < splits; ++i) {
+        sk += *reinterpret_cast<const f32x4*>(parts + 2 * i * size + at);
+        sv += *reinterpret_cast<const f32x4*>(parts + (2 * i + 1) * size + at);
+    }
+    float a[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[e] = sk[e] * scale;
+        b[e] = sv[e];
+    }
+    store_vec_any<T, 4>(dk + at, a);
+    store_vec_any<T, 4>(dv + at, b);
+}
+
+template <typename T, int D, int NW, int SW>
+hipError_t run_dq(BwdParams x, hipStream_t stream) {
+    const int64_t grid = deal(&x.p, x.p.tq, NW / SW * 32, x.p.heads / x.p.groups);
     if (grid < 0) return hipErrorInvalidValue;
-    if (grid > 0) hipLaunchKernelGGL((dq_kernel<T, D, NW>), dim3((unsigned)grid), dim3(NW * 64), 0, stream, x);
-    grid = deal(&x.p, x.p.tk, NW * 32, 1);
-    if (grid < 0) return hipErrorInvalidValue;
-    if (grid > 0) hipLaunchKernelGGL((dkv_kernel<T, D, NW>), dim3((unsigned)grid), dim3(NW * 64), 0, stream, x);
+    if (grid > 0) hipLaunchKernelGGL((dq_kernel<T, D, NW, SW>), dim3((unsigned)grid), dim3(NW * 64), 0, stream, x);
     return hipGetLastError();
+}
+template <typename T, int D, int NW, int SW>
+hipError_t run_dkv(BwdParams x, int splits, hipStream_t stream) {
+    const int64_t grid = deal(&x.p, x.p.tk, NW / SW * 32, 1);
+    if (grid < 0) return hipErrorInvalidValue;
+    if (grid == 0) return hipSuccess;
+    hipLaunchKernelGGL((dkv_kernel<T, D, NW, SW>), dim3((unsigned)grid, (unsigned)splits), dim3(NW * 64), 0, stream, x);
+    if (splits > 1) {
+        const int64_t rows = x.keys * x.p.groups;
+        hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)((rows + 1024 / D - 1) / (1024 / D))), dim3(256), 0, stream, x.parts,
+                           (T*)x.dk, (T*)x.dv, x.p.scale, rows, splits, Owned{x.p.cu_k, x.p.n, x.p.tk, x.p.groups});
+    }
+    return hipGetLastError();
+}
+
+// How the backward pass is launched.  Workgroups whose waves share 32 queries or keys are four times as many,
+// with loops a fourth as long, but read the other side's tiles four times as often, and with more LDS each fewer
+// run at once.  dk and dv, whose loops go over the heads that share a key head too, gain most: 4096 tokens, 8
+// heads of 64 sharing 2, bf16, took 478 us in all with 64 workgroups, 180 us shared, 150 us in two parts (below);
+// 4 x 4096 tokens, 16 heads sharing 8: 593 and 559; 16 x 1000 tokens of 12 heads: 160 and 173.  Heads of 128 take
+// twice the LDS: 8192 tokens, 8 heads sharing 4, 859 and 781; 2 x 4096 tokens, 16 heads sharing 8, 605 and 743.
+// Packed sequences differ in length, and the longest one's loops end last: 16 of 4096 tokens and fewer, 12 heads
+// of 64, 253 and 243.
+// With fewer workgroups than the GPU runs at once the tiles of queries are taken in parts whose sums a further
+// launch joins: the same 4096 tokens of 4 heads sharing one, 143 us in one part, 82 in four.
+struct BwdForm {
+    bool share_q, share_k;
+    int splits;  // parts that dk and dv are taken in
+};
+BwdForm bwd_form(const Shape& p, int64_t d, bool is_bf16, int64_t cus) {
+    auto workgroups = [&](int64_t tokens, int64_t heads) {
+        const int64_t b = (tokens + 31) / 32;
+        return (p.cu_q ? b + p.n - 1 : b * p.n) * heads;
+    };
+    const int64_t wq = workgroups(p.tq, p.heads), wk = workgroups(p.tk, p.groups);
+    BwdForm f{wq <= 2 * cus, wk <= (d == 64 ? (p.cu_q ? 32 : 16) : is_bf16 ? 4 : 2) * cus, 1};
+    // tiles of queries that see a block of keys, and those that a part is worth
+    const int64_t tiles = (min((int64_t)p.window + 32, p.tq) + 31) / 32 * (p.heads / p.groups), least = is_bf16 ? 16 : 4;
+    if (f.share_k && wk > 0) f.splits = (int)max((int64_t)1, min(tiles / least, 2 * cus / wk));
+    return f;
+}
+
+template <typename T, int D>
+hipError_t run_bwd(const BwdParams& b, const BwdForm& f, hipStream_t stream) {
+    constexpr int SW = D * sizeof(T) > 256 ? 2 : 4;  // what LDS has room for
+    const hipError_t e = f.share_q ? run_dq<T, D, SW, SW>(b, stream) : run_dq<T, D, 4, 1>(b, stream);
+    if (e != hipSuccess) return e;
+    return f.share_k ? run_dkv<T, D, SW, SW>(b, f.splits, stream) : run_dkv<T, D, 4, 1>(b, 1, stream);
 }
 
 }  // namespace attn
 
-hipError_t launch_attn_bwd(const AttnArgs& a) {
-    const int64_t tokens = a.cu_q ? a.T : a.N * a.T;
+namespace {
+int64_t stats_bytes(const AttnArgs& a) { return ((a.cu_q ? a.T : a.N * a.T) * a.H * 8 + 15) / 16 * 16; }
+}  // namespace
+
+size_t attn_bwd_workspace_bytes(const AttnArgs& a) {
+    const int splits = attn::bwd_form(attn_shape(a), a.d, a.dtype_bf16, a.cus).splits;
+    return (size_t)(stats_bytes(a) + (splits > 1 ? splits * 2 * (a.cu_q ? a.S : a.N * a.S) * a.G * a.d * 4 : 0));
+}
+
+hipError_t launch_attn_bwd(const AttnArgs& a, void* workspace) {
+    const int64_t queries = a.cu_q ? a.T : a.N * a.T, keys = a.cu_q ? a.S : a.N * a.S;
+    float* stats = static_cast<float*>(workspace);
+    const attn::Shape p = attn_shape(a);
     const attn::BwdParams b{(const char*)a.q, (const char*)a.k, (const char*)a.v, (const char*)a.o, (const char*)a.d_o, a.lse,
-                            a.dq, a.dk, a.dv, a.stats, a.stats + tokens * a.H, tokens, attn_shape(a)};
+                            a.dq, a.dk, a.dv, stats, stats + queries * a.H, queries,
+                            workspace ? stats + stats_bytes(a) / 4 : nullptr, keys, p};
+    const attn::BwdForm f = attn::bwd_form(p, a.d, a.dtype_bf16, a.cus);
     const hipStream_t s = (hipStream_t)a.stream;
-    if (a.dtype_bf16) return a.d == 64 ? attn::run_bwd<bf16, 64>(b, s) : attn::run_bwd<bf16, 128>(b, s);
-    return a.d == 64 ? attn::run_bwd<float, 64>(b, s) : attn::run_bwd<float, 128>(b, s);
+    if (a.dtype_bf16) return a.d == 64 ? attn::run_bwd<bf16, 64>(b, f, s) : attn::run_bwd<bf16, 128>(b, f, s);
+    return a.d == 64 ? attn::run_bwd<float, 64>(b, f, s) : attn::run_bwd<float, 128>(b, f, s);
 }
 
 }  // namespace gdn2

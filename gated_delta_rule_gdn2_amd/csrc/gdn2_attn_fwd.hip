@@ -17,7 +17,8 @@ namespace gdn2 {
 namespace attn {
 
 // keys in a tile
-template <typename T> constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
+template <typename T, int SW> constexpr int kKeys = sizeof(T) == 2 && SW == 1 ? 64 : 32;
+template <typename T, int D, int SW> constexpr int kFwdLds = SW * 2 * 2 * kKeys<T, SW> * Tile<T, D>::kRow;
 // Weights are formed against a reference near the row's largest score so far.  A row's sum over a tile
 // may grow up to this (in units of the reference's weight) before the reference follows.
 constexpr float kSlack = 4096.f;
@@ -32,15 +33,18 @@ struct FwdParams {
     Shape p;
 };
 
-// The work of one workgroup.  FIRST: returns whether some output of a wave is not finite, and leaves that
+// The work of one workgroup of NW waves.  SW of them share 32 queries: each takes every SWth tile of keys, with
+// tiles of its own in LDS, and their sums are joined at the end.  FIRST: returns whether some output of a wave is not finite, and leaves that
 // wave's outputs unwritten (`flag`: in LDS, zero).  A product multiplies what a query does not see by zero, which infinities
 // and NaN survive: the other form leaves out value by value what the mask hides.
-template <typename T, int D, int NW, bool FIRST>
+template <typename T, int D, int NW, int SW, bool FIRST>
 __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* flag) {
     typedef Tile<T, D> L;
-    constexpr int BK = kKeys<T>, KS = D / 16, DT = D / 32, BM = NW * 32, BYTES = BK * L::kRow;
+    static_assert(SW == 1 || SW == NW, "each wave its own queries, or all the same");
+    constexpr int BK = kKeys<T, SW>, KS = D / 16, DT = D / 32, BM = NW / SW * 32, BYTES = BK * L::kRow;
     const int lane = threadIdx.x & 63, g = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = SW == 1 ? all_waves : 0, part = SW == 1 ? 0 : all_waves;
     const Shape& p = a.p;
     Work w;
     if (!find_work(p, BM, p.heads / p.groups, true, false, lane, &w)) return false;
@@ -65,23 +69,25 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
     const int64_t pos0 = (int64_t)off + mine;
     const int pos = (int)(pos0 + (lane & 31));
     const Lds row_base = L::row_base(lane), col_base = L::col_base(lane);
+    auto place = [&](int t) { return base + (part * 2 + (t / SW & 1)) * 2 * BYTES; };
     auto stage = [&](int t) {
         const int left = min(BK, lk - t * BK);
-        const Lds to = base + (t & 1) * 2 * BYTES;
-        L::template stage<BK, NW>(to, k + (int64_t)t * BK * p.k_stride, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
-        L::template stage<BK, NW>(to + BYTES, v + (int64_t)t * BK * p.v_stride, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
+        const Lds to = place(t);
+        L::template stage<BK, NW / SW>(to, k + (int64_t)t * BK * p.k_stride, span(left, p.k_stride, L::kRow), p.k_stride, wave, lane);
+        L::template stage<BK, NW / SW>(to + BYTES, v + (int64_t)t * BK * p.v_stride, span(left, p.v_stride, L::kRow), p.v_stride, wave, lane);
     };
-    // the queries come by way of the second tile's place in LDS, if they have room there: rows are read whole
+    // the queries come by way of the (first wave's) second tile's place in LDS, if they have room there: rows are read whole
     constexpr bool VIA = BM * L::kRow <= 2 * BYTES;
     const char* qp = a.q + (w.s.q0 + first) * p.q_stride + (int64_t)head * L::kRow;
     Op<T> q[KS];
-    if (t0 < t1) stage(t0);
+    if (t0 + part < t1) stage(t0 + part);
     if constexpr (VIA) {
-        const Lds to = base + (~t0 & 1) * 2 * BYTES;
-        L::template stage<BM, NW>(to, qp, span(min(BM, lq - first), p.q_stride, L::kRow), p.q_stride, wave, lane);
+        const Lds to = base + (~(t0 / SW) & 1) * 2 * BYTES;
+        L::template stage<BM, NW>(to, qp, span(min(BM, lq - first), p.q_stride, L::kRow), p.q_stride, all_waves, lane);
         tile_barrier();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) q[ks] = L::row_op(row_base + to + wave * 32 * L::kRow, 0, ks);
+        if (SW > 1) lds_barrier();
     } else {
         const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(qp), 0, span(min(BM, lq - first), p.q_stride, L::kRow), 0x00020000);
 #pragma unroll
@@ -135,14 +141,15 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
         return sum;
     };
     bool first_tile = true;  // of those that the wave has to do with
-    for (int t = t0; t < t1; ++t) {
-        tile_barrier();
-        if (t + 1 < t1) stage(t + 1);
+    for (int t = t0 + part; t < t1; t += SW) {
+        if (SW == 1) tile_barrier();
+        else own_tile_wait();
+        if (t + SW < t1) stage(t + SW);
         const int key0 = t * BK;
         if (rows <= 0 || key0 > pos0 + rows - 1 || key0 + BK - 1 <= pos0 - p.window) continue;  // nothing that the wave's queries see
         const bool cut = key0 + BK - 1 > pos0 || key0 <= pos0 + 31 - p.window;                 // not all that they see
         const Seen seen = seen_between(pos - key0 - p.window + 1, pos - key0);                 // the lane's query's
-        const Lds tk = base + (t & 1) * 2 * BYTES;
+        const Lds tk = place(t);
         const Lds rb = opaque(row_base + tk);
         scores(rb);
         if (cut) hide(seen);
@@ -190,7 +197,7 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
         if (again) *flag = 1;
         lds_barrier();
         any = *flag != 0;
-        if (again) return any;
+        if (SW == 1 ? again : any) return any;
     } else {
         lds_barrier();
     }
@@ -198,9 +205,39 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
     l += other_half(l, lane);
     const int64_t row0 = (w.s.q0 + mine) * p.heads + head, row = row0 + (int64_t)(lane & 31) * p.heads;
     const bool live = (lane & 31) < rows;
+    const int64_t at = (int64_t)blockIdx.y * a.parts.rows + row;
+    if constexpr (SW > 1) {
+        typedef WaveSums<D, SW> Sums;
+        static_assert(Sums::kBytes <= kFwdLds<T, D, SW> && SW * 256 <= kFwdLds<T, D, SW>, "room for the sums");
+        if (g == 0) *(GDN2_LDS f32x2*)(uintptr_t)(base + (part * 32 + lane) * 8) = f32x2{m, l};
+        lds_barrier();
+        f32x2 ml[SW];
+        float ref = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < SW; ++i) {
+            ml[i] = lds_get<f32x2>(base + (i * 32 + (lane & 31)) * 8);
+            ref = fmaxf(ref, ml[i][0]);
+        }
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < SW; ++i) l += ml[i][1] * (ml[i][0] == ref ? 1.f : __builtin_amdgcn_exp2f(ml[i][0] - ref));
+        const float f = m == ref ? 1.f : __builtin_amdgcn_exp2f(m - ref);
+        m = ref;
+        lds_barrier();
+        Sums sums;
+        sums.add(base, o, f, part, lane);
+        if (!live) return any;
+        if (gridDim.y > 1) {
+            sums.template store<float>(a.parts.o + at * D, 1.f, part, g);
+            if (g == 0 && part == 0) a.parts.ml[at] = float2{m, l};
+            return any;
+        }
+        sums.template store<T>((T*)a.o + row * D, l == 0.f ? 0.f : 1.f / l, part, g);
+        if (a.lse && g == 0 && part == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        return any;
+    }
     if (gridDim.y > 1) {
         if (live) {
-            const int64_t at = (int64_t)blockIdx.y * a.parts.rows + row;
             store_column<float, D>(a.parts.o + at * D, o, 1.f, g);
             if (g == 0) a.parts.ml[at] = float2{m, l};
         }
@@ -211,19 +248,19 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
     return any;
 }
 // a call of its own, so that the kernel keeps its registers to the first form
-template <typename T, int D, int NW>
+template <typename T, int D, int NW, int SW>
 __device__ __attribute__((noinline)) void fwd_again(FwdParams a, Lds base) {
-    fwd_block<T, D, NW, false>(a, base, nullptr);
+    fwd_block<T, D, NW, SW, false>(a, base, nullptr);
 }
 
-template <typename T, int D, int NW>
-__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void fwd_kernel(FwdParams a) {
-    __shared__ __attribute__((aligned(1024))) char lds[2 * 2 * kKeys<T> * Tile<T, D>::kRow];
+template <typename T, int D, int NW, int SW>
+__global__ __launch_bounds__(NW * 64, SW > 1 ? (kFwdLds<T, D, SW> > 80000 ? 1 : 2) : D == 64 ? 3 : 2) void fwd_kernel(FwdParams a) {
+    __shared__ __attribute__((aligned(1024))) char lds[kFwdLds<T, D, SW>];
     __shared__ int any_again;
     if (threadIdx.x == 0) any_again = 0;
-    if (fwd_block<T, D, NW, true>(a, lds_of(lds), &any_again)) {
+    if (fwd_block<T, D, NW, SW, true>(a, lds_of(lds), &any_again)) {
         __syncthreads();
-        fwd_again<T, D, NW>(a, lds_of(lds));
+        fwd_again<T, D, NW, SW>(a, lds_of(lds));
     }
 }
 
@@ -289,25 +326,44 @@ hipError_t launch_join(const Parts& p, void* o, float* lse, int64_t d, bool bf16
     return hipGetLastError();
 }
 
-// Parts that a block's keys are taken in: with too few blocks for the GPU, as many as fill it twice, of
-// 256 keys and more.  (Sequences that are packed may be shorter than the longest: their parts are, too.)
-int fwd_splits(Shape p, int64_t cus) {
-    const int64_t grid = deal(&p, p.tq, 128, p.heads / p.groups);
-    const int64_t busy = p.cu_q ? ((p.tq + 127) / 128 + p.n - 1) * p.heads : (p.tq + 127) / 128 * p.n * p.heads;
-    if (grid <= 0 || busy >= cus) return 1;
-    const int64_t keys = min((int64_t)p.window + 128, p.tk), most = (keys + 255) / 256, want = (2 * cus + busy - 1) / busy;
-    return (int)max((int64_t)1, min(most, want));
+// How the forward pass is launched.  Workgroups whose waves share 32 queries are four times as many, and their
+// loops a fourth as long, but they read keys and values four times as often: they are taken while they fit the
+// GPU in two rounds (fp32 heads of 128, which two waves share: while they leave most of it idle).  bf16 in
+// us, shared against not: 14 and 24 at 1024 tokens of 4 heads of 64, 36 and 56 at 4096 of 8, 64 and 60 of 16;
+// heads of 128: 15 and 24, 96 and 84, 191 and 96.
+// With few workgroups and many keys a block's keys are also taken in parts, as many as fill the GPU, whose sums
+// a second launch joins: 4096 tokens of one head of 64 take 19 us in 4 parts, 23 in one.  (Sequences that
+// are packed may be shorter than the longest: their parts are, too.)
+struct FwdForm {
+    bool share;
+    int splits;
+};
+FwdForm fwd_form(Shape p, int64_t d, bool is_bf16, int64_t cus) {
+    if (deal(&p, p.tq, 128, p.heads / p.groups) <= 0) return {false, 1};
+    auto workgroups = [&](int64_t rows) {
+        const int64_t b = (p.tq + rows - 1) / rows;
+        return (p.cu_q ? b + p.n - 1 : b * p.n) * p.heads;
+    };
+    const bool share = workgroups(32) <= (d == 64 ? 4 * cus : is_bf16 ? 2 * cus : cus / 4);
+    const int64_t w = workgroups(share ? 32 : 128), keys = min((int64_t)p.window + (share ? 32 : 128), p.tk);
+    const int64_t least = is_bf16 ? 1024 : 256;  // keys of a part: below, the second launch costs more
+    return {share, w >= cus ? 1 : (int)max((int64_t)1, min(keys / least, 2 * cus / w))};
 }
 
-template <typename T, int D, int NW>
+template <typename T, int D, int NW, int SW>
 hipError_t run_fwd(FwdParams f, hipStream_t stream) {
-    const int64_t grid = deal(&f.p, f.p.tq, NW * 32, f.p.heads / f.p.groups);
+    const int64_t grid = deal(&f.p, f.p.tq, NW / SW * 32, f.p.heads / f.p.groups);
     if (grid < 0) return hipErrorInvalidValue;
     if (grid == 0) return hipSuccess;
-    hipLaunchKernelGGL((fwd_kernel<T, D, NW>), dim3((unsigned)grid, (unsigned)f.parts.splits), dim3(NW * 64), 0, stream, f);
+    hipLaunchKernelGGL((fwd_kernel<T, D, NW, SW>), dim3((unsigned)grid, (unsigned)f.parts.splits), dim3(NW * 64), 0, stream, f);
     if (f.parts.splits > 1)
         return launch_join(f.parts, f.o, f.lse, D, sizeof(T) == 2, Owned{f.p.cu_q, f.p.n, f.p.tq, f.p.heads}, stream);
     return hipGetLastError();
+}
+template <typename T, int D>
+hipError_t choose_fwd(const FwdParams& f, bool share, hipStream_t stream) {
+    constexpr int SW = D * sizeof(T) > 256 ? 2 : 4;
+    return share ? run_fwd<T, D, SW, SW>(f, stream) : run_fwd<T, D, 4, 1>(f, stream);
 }
 
 }  // namespace attn
@@ -342,18 +398,20 @@ bool attn_grid_ok(const AttnArgs& a) {
 }
 
 size_t attn_fwd_workspace_bytes(const AttnArgs& a) {
-    const int splits = attn::fwd_splits(attn_shape(a), a.cus);
+    const int splits = attn::fwd_form(attn_shape(a), a.d, a.dtype_bf16, a.cus).splits;
     return splits > 1 ? attn::parts_bytes((a.cu_q ? a.T : a.N * a.T) * a.H, a.d, splits) : 0;
 }
 
 hipError_t launch_attn_fwd(const AttnArgs& a, void* workspace) {
     const attn::Shape p = attn_shape(a);
     const int64_t rows = (a.cu_q ? a.T : a.N * a.T) * a.H;
+    const attn::FwdForm form = attn::fwd_form(p, a.d, a.dtype_bf16, a.cus);
     const attn::FwdParams f{(const char*)a.q, (const char*)a.k, (const char*)a.v, a.o, a.lse,
-                            attn::parts_in(workspace, rows, a.d, workspace ? attn::fwd_splits(p, a.cus) : 1), p};
+                            attn::parts_in(workspace, rows, a.d, workspace ? form.splits : 1), p};
     const hipStream_t s = (hipStream_t)a.stream;
-    if (a.dtype_bf16) return a.d == 64 ? attn::run_fwd<bf16, 64, 4>(f, s) : attn::run_fwd<bf16, 128, 4>(f, s);
-    return a.d == 64 ? attn::run_fwd<float, 64, 4>(f, s) : attn::run_fwd<float, 128, 4>(f, s);
+    const bool share = form.share;
+    if (a.dtype_bf16) return a.d == 64 ? attn::choose_fwd<bf16, 64>(f, share, s) : attn::choose_fwd<bf16, 128>(f, share, s);
+    return a.d == 64 ? attn::choose_fwd<float, 64>(f, share, s) : attn::choose_fwd<float, 128>(f, share, s);
 }
 
 }  // namespace gdn2

@@ -210,14 +210,13 @@ struct AttnArgs {
     void* dq = nullptr;         // laid out as q, k and v, contiguous
     void* dk = nullptr;
     void* dv = nullptr;
-    float* stats = nullptr;     // workspace: of every query and head lse in base 2 and sum(d_o o)
 };
 inline bool attn_supported(int64_t d) { return d == 64 || d == 128; }
 bool attn_grid_ok(const AttnArgs& a);  // whether every launch that the sizes may take fits
 size_t attn_fwd_workspace_bytes(const AttnArgs& a);
 hipError_t launch_attn_fwd(const AttnArgs& a, void* workspace);
-inline int64_t attn_stats_bytes(int64_t tokens, int64_t heads) { return tokens * heads * 8; }
-hipError_t launch_attn_bwd(const AttnArgs& a);
+size_t attn_bwd_workspace_bytes(const AttnArgs& a);
+hipError_t launch_attn_bwd(const AttnArgs& a, void* workspace);
 
 // One token of each of N sequences over caches of their last C tokens.
 struct AttnStepArgs {

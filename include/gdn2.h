@@ -617,8 +617,11 @@ gdn2_status_t gdn2_attn_bwd_varlen(const void* d_o, const void* q, const void* k
                                    float scale, gdn2_dtype_t dtype, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace that both need, for all queries (B * T, or total_T). */
-size_t gdn2_attn_bwd_workspace_bytes(int64_t queries, int64_t H);
+/* Bytes of device workspace that they need for these sizes on the current device (0: none). */
+size_t gdn2_attn_bwd_workspace_bytes(int64_t B, int64_t T, int64_t S, int64_t H, int64_t G, int64_t d,
+                                     int64_t window, gdn2_dtype_t dtype);
+size_t gdn2_attn_bwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t total_S, int64_t H,
+                                            int64_t G, int64_t d, int64_t window, gdn2_dtype_t dtype);
 
 /*
  * gdn2_attn_step -- attention of one token for each of N sequences over a cache of

@@ -132,8 +132,11 @@ def test_workspaces(lib):
     assert need > 0
     assert fwd_packed(lib, f, T=8, S=4096, ws=a16(8), wb=need - 4) == ERR_WORKSPACE
     assert fwd_packed(lib, f, T=8, S=4096, ws=a16(6), wb=need) == ERR_ALIAS
-    # gradients: eight bytes a query and head
-    assert gdn2.attn_bwd_workspace_bytes(100, 6) == 4800 and gdn2.attn_bwd_workspace_bytes(0, 6) == 0
+    # gradients: eight bytes a query and head, more where heads share keys and workgroups are few
+    assert gdn2.attn_bwd_workspace_bytes(1, 100, 100, 6, 6, 64) == 4800 and gdn2.attn_bwd_workspace_bytes(1, 0, 4, 6, 6, 64) == 0
+    assert gdn2.attn_bwd_varlen_workspace_bytes(2, 100, 100, 6, 6, 64) == 4800
+    parts = gdn2.attn_bwd_workspace_bytes(1, 4096, 4096, 4, 1, 64) - 4096 * 4 * 8
+    assert parts > 0 and parts % (2 * 4096 * 64 * 4) == 0
     assert bwd(lib, f, ws=None, wb=0) == ERR_WORKSPACE and bwd(lib, f, wb=64 * 2 * 8 - 1) == ERR_WORKSPACE
     assert bwd(lib, f, ws=f.p(10, 8)) == ERR_MISALIGNED
     # steps

@@ -126,6 +126,42 @@ def check_bwd(d_o, q, k, v, o, lse, grads, window=None, scale=None):
         within(name, grads[name], x, t + (r + 2 * U) * np.abs(x))
 
 
+# Few workgroups share their rows between waves and are taken in parts; the same sequences many times over
+# are not.  Every copy of a sequence has the same bits.
+MANY = pytest.mark.parametrize("many", [False, True], ids=["few", "many"])
+
+
+def copies(many, q, k):
+    """Copies of the sequences q [B,T,H,d], k [B,S,G,d] that make more than 4096 blocks of 32 rows."""
+    (B, T, H, _), (_, S, G, _) = q.shape, k.shape
+    return 1 + 4096 // max(1, B * min(-(-T // 32) * H, -(-S // 32) * G)) if many else 1
+
+
+def first_of(n, *outs):
+    firsts = []
+    for x in outs:
+        B = x.shape[0] // n
+        bits = x.view(torch.int16 if x.dtype == BF16 else torch.int32).reshape(n, -1)
+        assert (bits == bits[:1]).all()
+        firsts.append(x[:B])
+    return firsts
+
+
+def times(n, x):
+    return x.repeat(n, *[1] * (x.dim() - 1)) if n > 1 else x
+
+
+def fwd(many, q, k, v, **kw):
+    n = copies(many, q, k)
+    return first_of(n, *gdn2.attn_fwd(*[times(n, x) for x in (q, k, v)], **kw))
+
+
+def bwd(many, d_o, q, k, v, o, lse, **kw):
+    n = copies(many, q, k)
+    grads = gdn2.attn_bwd(*[times(n, x) for x in (d_o, q, k, v, o, lse)], **kw)
+    return dict(zip(grads, first_of(n, *grads.values())))
+
+
 FWD = [  # dtype, B, T, S, H, G, d, window
     (BF16, 1, 1, 1, 1, 1, 64, None), (F32, 1, 1, 1, 2, 1, 128, None),
     (BF16, 2, 1, 77, 8, 2, 128, None), (BF16, 1, 31, 31, 2, 2, 64, None), (BF16, 2, 33, 33, 6, 2, 128, None),
@@ -138,33 +174,38 @@ FWD = [  # dtype, B, T, S, H, G, d, window
 ]
 
 
+@MANY
 @pytest.mark.parametrize("dtype,B,T,S,H,G,d,window", FWD)
-def test_forward_matches_oracle(dtype, B, T, S, H, G, d, window):
+def test_forward_matches_oracle(dtype, B, T, S, H, G, d, window, many):
     say("case: forward %s B%d T%d S%d H%d G%d d%d window %s" % (dtype, B, T, S, H, G, d, window))
     q, k, v, _ = case(dtype, T, S, H, G, d, 7 * T + S, B)
     dev = [x.cuda() for x in (q, k, v)]
-    o, lse = gdn2.attn_fwd(*dev, window=window)
+    o, lse = fwd(many, *dev, window=window)
     torch.cuda.synchronize()
     for b in range(B):
         check_fwd(q[b], k[b], v[b], o[b], lse[b], window)
-    again, lse2 = gdn2.attn_fwd(*dev, window=window)
+    again, lse2 = fwd(many, *dev, window=window)
     assert torch.equal(o, again) and torch.equal(lse, lse2)
+    if many:
+        return
     only, none = gdn2.attn_fwd(*dev, window=window, stats=False)
     assert none is None and torch.equal(only, o)
 
 
+@MANY
 @pytest.mark.parametrize("dtype,T,S,H,G,d,window", [c[:1] + c[2:] for c in FWD if c[3]] + [
-    (BF16, 96, 96, 4, 1, 128, 96), (BF16, 260, 260, 4, 2, 128, 130), (F32, 100, 160, 6, 2, 64, 50)])
-def test_gradients_match_oracle(dtype, T, S, H, G, d, window):
+    (BF16, 96, 96, 4, 1, 128, 96), (BF16, 260, 260, 4, 2, 128, 130), (F32, 100, 160, 6, 2, 64, 50), (BF16, 600, 620, 8, 1, 64, None),
+    (BF16, 530, 530, 12, 2, 128, 400), (F32, 410, 410, 4, 1, 128, None), (F32, 300, 333, 8, 1, 64, 250)])
+def test_gradients_match_oracle(dtype, T, S, H, G, d, window, many):
     say("case: gradients %s T%d S%d H%d G%d d%d window %s" % (dtype, T, S, H, G, d, window))
     q, k, v, g = case(dtype, T, S, H, G, d, 3 * T + S)
     o, lse = A.attention(q[0], k[0], v[0], window)
     o, lse = torch.from_numpy(o).to(dtype)[None], torch.from_numpy(lse).float()[None]
     dev = [x.cuda() for x in (g, q, k, v, o, lse)]
-    grads = gdn2.attn_bwd(*dev, window=window)
+    grads = bwd(many, *dev, window=window)
     torch.cuda.synchronize()
     check_bwd(g[0], q[0], k[0], v[0], o[0], lse[0], {n: x[0] for n, x in grads.items()}, window)
-    again = gdn2.attn_bwd(*dev, window=window)
+    again = bwd(many, *dev, window=window)
     assert all(torch.equal(grads[n], again[n]) for n in grads)
 
 
@@ -232,24 +273,27 @@ PACKED = [  # dtype, query lengths, keys before them, H, G, d, window
 ]
 
 
+@MANY
 @pytest.mark.parametrize("dtype,lengths,past,H,G,d,window", PACKED)
-def test_packed_matches_oracle(dtype, lengths, past, H, G, d, window):
+def test_packed_matches_oracle(dtype, lengths, past, H, G, d, window, many):
     say("case: packed %s %s after %s H%d G%d d%d window %s" % (dtype, lengths, past, H, G, d, window))
     n = len(lengths)
     keys = [a + b for a, b in zip(lengths, past or [0] * n)]
     tail = 9  # tokens of no sequence
-    cu, cu_k = offsets(lengths), offsets(keys)
+    R = 2 + (8192 if d == 64 else 1024) // (n * G) if many else 1  # the sequences so many times
+    cu, cu_k = offsets(lengths * R), offsets(keys * R)
     q, _, _, g = case(dtype, sum(lengths) + tail, 1, H, G, d, 11)
     _, k, v, _ = case(dtype, 1, sum(keys) + tail, H, G, d, 12)
     q, k, v, g = (x[0] for x in (q, k, v, g))
     # what lies behind the last sequence is nobody's: it may be anything
     for x, end in ((q, sum(lengths)), (k, sum(keys)), (v, sum(keys)), (g, sum(lengths))):
         x[end:] = NAN
-    dq_, k_, v_, g_ = (x.cuda() for x in (q, k, v, g))
-    o, lse = torch.full(q.shape, 7.0, dtype=dtype, device="cuda"), torch.full(q.shape[:2], 7.0, device="cuda")
+    dq_, k_, v_, g_ = (torch.cat([times(R, x[:end].cuda()), x[end:].cuda()])
+                       for x, end in ((q, sum(lengths)), (k, sum(keys)), (v, sum(keys)), (g, sum(lengths))))
+    o, lse = torch.full(dq_.shape, 7.0, dtype=dtype, device="cuda"), torch.full(dq_.shape[:2], 7.0, device="cuda")
     kw = dict(cu_seqlens_k=None if past is None else cu_k.cuda(), window=window)
     gdn2.attn_fwd_varlen(dq_, k_, v_, cu.cuda(), o=o, lse=lse, **kw)
-    grads = {m: torch.full(x.shape, 7.0, dtype=dtype, device="cuda") for m, x in (("dq", q), ("dk", k), ("dv", v))}
+    grads = {m: torch.full(x.shape, 7.0, dtype=dtype, device="cuda") for m, x in (("dq", dq_), ("dk", k_), ("dv", v_))}
     gdn2.attn_bwd_varlen(g_, dq_, k_, v_, o, lse, cu.cuda(), grads=grads, **kw)
     torch.cuda.synchronize()
     for i in range(n):
@@ -260,8 +304,10 @@ def test_packed_matches_oracle(dtype, lengths, past, H, G, d, window):
             check_bwd(g[a:b], q[a:b], k[c:e], v[c:e], o[a:b], lse[a:b], dict(dq=grads["dq"][a:b], dk=grads["dk"][c:e], dv=grads["dv"][c:e]), window)
         elif c < e:
             assert not grads["dk"][c:e].any() and not grads["dv"][c:e].any()  # keys without queries
-    for x in (o[sum(lengths):], lse[sum(lengths):], grads["dq"][sum(lengths):], grads["dk"][sum(keys):], grads["dv"][sum(keys):]):
-        assert (x == 7.0).all()
+    for x, per in ((o, lengths), (lse, lengths), (grads["dq"], lengths), (grads["dk"], keys), (grads["dv"], keys)):
+        end = sum(per) * R
+        assert (x[end:] == 7.0).all()
+        first_of(R, x[:end])
 
 
 def test_packed_equals_whole():
@@ -321,18 +367,19 @@ def test_addresses_past_32_bits():
 
 # ---- values that are not finite -------------------------------------------------------------
 
+@MANY
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("bad", [NAN, INF, -INF])
 @pytest.mark.parametrize("T,window,at", [(200, None, 90), (200, 50, 90), (70, 7, 33), (300, 129, 128), (64, None, 0)])
-def test_bad_values_reach_no_query_that_does_not_see_them(dtype, bad, T, window, at):
+def test_bad_values_reach_no_query_that_does_not_see_them(dtype, bad, T, window, at, many):
     H, G, d = 2, 1, 64
     q, k, v, g = case(dtype, T, T, H, G, d, T + at)
     seen = A.sees(T, T, window)[:, at]  # the queries that see token `at`
     clean = [x.cuda() for x in (q, k, v)]
-    o, lse = gdn2.attn_fwd(*clean, window=window)
+    o, lse = fwd(many, *clean, window=window)
     dirty_v = v.clone()
     dirty_v[0, at, 0, 5] = bad
-    o2, lse2 = gdn2.attn_fwd(clean[0], clean[1], dirty_v.cuda(), window=window)
+    o2, lse2 = fwd(many, clean[0], clean[1], dirty_v.cuda(), window=window)
     assert torch.equal(lse, lse2)
     hit = torch.zeros(T, d, dtype=torch.bool)
     hit[:, 5] = torch.from_numpy(seen)
@@ -342,14 +389,14 @@ def test_bad_values_reach_no_query_that_does_not_see_them(dtype, bad, T, window,
     assert torch.equal(torch.nan_to_num(o2[~same], 1.0, 2.0, 3.0), torch.nan_to_num(want, 1.0, 2.0, 3.0))
     dirty_k = k.clone()
     dirty_k[0, at] = bad
-    o3, lse3 = gdn2.attn_fwd(clean[0], dirty_k.cuda(), clean[2], window=window)
+    o3, lse3 = fwd(many, clean[0], dirty_k.cuda(), clean[2], window=window)
     blind = torch.from_numpy(~seen).cuda()
     assert torch.equal(o[:, blind], o3[:, blind]) and torch.equal(lse[:, blind], lse3[:, blind])
     # gradients: an upstream gradient, a key and a value of one token
-    grads = gdn2.attn_bwd(g.cuda(), *clean, o, lse, window=window)
+    grads = bwd(many, g.cuda(), *clean, o, lse, window=window)
     dirty_g = g.clone()
     dirty_g[0, at, :, 7] = bad
-    bad_g = gdn2.attn_bwd(dirty_g.cuda(), *clean, o, lse, window=window)
+    bad_g = bwd(many, dirty_g.cuda(), *clean, o, lse, window=window)
     others = torch.arange(T, device="cuda") != at
     assert torch.equal(grads["dq"][:, others], bad_g["dq"][:, others])
     unseen = torch.from_numpy(~A.sees(T, T, window)[at]).cuda()  # keys that query `at` does not see
@@ -357,17 +404,17 @@ def test_bad_values_reach_no_query_that_does_not_see_them(dtype, bad, T, window,
         assert torch.equal(grads[n][:, unseen], bad_g[n][:, unseen]), n
     assert not torch.isfinite(bad_g["dv"][:, ~unseen][..., 7]).any()
     assert torch.equal(grads["dv"][..., :7], bad_g["dv"][..., :7])
-    ok, lk = gdn2.attn_fwd(clean[0], dirty_k.cuda(), clean[2], window=window)
-    bad_k = gdn2.attn_bwd(g.cuda(), clean[0], dirty_k.cuda(), clean[2], ok, lk, window=window)
+    ok, lk = fwd(many, clean[0], dirty_k.cuda(), clean[2], window=window)
+    bad_k = bwd(many, g.cuda(), clean[0], dirty_k.cuda(), clean[2], ok, lk, window=window)
     assert torch.equal(grads["dq"][:, blind], bad_k["dq"][:, blind])
     far = torch.from_numpy(~(A.sees(T, T, window)[seen].any(0))).cuda()  # keys that no query of those sees
     for n in ("dk", "dv"):
         assert torch.equal(grads[n][:, far], bad_k[n][:, far]), n
     dirty_q = q.clone()
     dirty_q[0, at] = bad
-    oq, lq = gdn2.attn_fwd(dirty_q.cuda(), *clean[1:], window=window)
+    oq, lq = fwd(many, dirty_q.cuda(), *clean[1:], window=window)
     assert torch.equal(o[:, others], oq[:, others])
-    bad_q = gdn2.attn_bwd(g.cuda(), dirty_q.cuda(), *clean[1:], oq, lq, window=window)
+    bad_q = bwd(many, g.cuda(), dirty_q.cuda(), *clean[1:], oq, lq, window=window)
     assert torch.equal(grads["dq"][:, others], bad_q["dq"][:, others])
     for n in ("dk", "dv"):
         assert torch.equal(grads[n][:, unseen], bad_q[n][:, unseen]), n
