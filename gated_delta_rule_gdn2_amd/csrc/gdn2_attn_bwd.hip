@@ -306,15 +306,28 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
         const Lds rq = opaque(row_base + tq), ro = opaque(row_base + tq + BYTES), rv = opaque(row_base + tv + wave * 32 * L::kRow);
         f32x16 s = zero16(), dp;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) mma(s, L::row_op(rq, 0, ks), k[ks]);
-#pragma unroll
         for (int c = 0; c < 4; ++c) {
             const f32x4 x = lds_get<f32x4>(ts + 128 + 32 * c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) dp[4 * c + e] = x[e];
         }
+        constexpr int C = sizeof(T) == 2 ? 2 : 1;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) mma(dp, L::row_op(ro, 0, ks), L::row_op(rv, 0, ks));
+        for (int k0 = 0; k0 < KS; k0 += C) {
+            Op<T> xq[C], xo[C], xv[C];
+#pragma unroll
+            for (int ks = 0; ks < C; ++ks) {
+                xq[ks] = L::row_op(rq, 0, k0 + ks);
+                xo[ks] = L::row_op(ro, 0, k0 + ks);
+                xv[ks] = L::row_op(rv, 0, k0 + ks);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int ks = 0; ks < C; ++ks) {
+                mma(s, xq[ks], k[k0 + ks]);
+                mma(dp, xo[ks], xv[ks]);
+            }
+        }
         float lse[16];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

@@ -264,14 +264,14 @@ __global__ __launch_bounds__(NW * 64, SW > 1 ? (kFwdLds<T, D, SW> > 80000 ? 1 : 
     }
 }
 
-// Joins parts: a workgroup a row, groups of its threads taking the row's parts in turn.
+// Joins parts: a workgroup a row, D / 4 threads a part; each takes every SUBth part, several loads at once.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(Parts p, T* __restrict__ o, float* __restrict__ lse, Owned owned) {
-    constexpr int SUB = 256 / (D / 2);
-    __shared__ float2 sum[SUB][D / 2];
+    constexpr int SUB = 256 / (D / 4);
+    __shared__ f32x4 sum[SUB][D / 4];
     __shared__ float total[SUB];
     const int64_t row = blockIdx.x;
-    const int c = threadIdx.x % (D / 2), sub = threadIdx.x / (D / 2), lane = threadIdx.x & 63;
+    const int c = threadIdx.x % (D / 4), sub = threadIdx.x / (D / 4), lane = threadIdx.x & 63;
     if (owned.cu) {  // a token of no sequence has no parts and stays as it was
         const int64_t token = row / owned.heads;
         bool found = false;
@@ -289,15 +289,16 @@ __global__ __launch_bounds__(256) void join_kernel(Parts p, T* __restrict__ o, f
     for (int i = lane; i < p.splits; i += 64) m = fmaxf(m, p.ml[i * p.rows + row].x);
 #pragma unroll
     for (int s = 32; s >= 1; s /= 2) m = fmaxf(m, __shfl_xor(m, s));
-    float2 x{0.f, 0.f};
+    f32x4 x{0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
+#pragma unroll 4
     for (int i = sub; i < p.splits; i += SUB) {
         const float2 ml = p.ml[i * p.rows + row];
-        if (ml.x == -__builtin_inff() && ml.y == 0.f) continue;  // a part that saw nothing
-        const float f = __builtin_amdgcn_exp2f(ml.x - m);
-        const float2 v = *reinterpret_cast<const float2*>(p.o + (i * p.rows + row) * D + 2 * c);
-        x.x += f * v.x;
-        x.y += f * v.y;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p.o + (i * p.rows + row) * D + 4 * c);
+        // a part that saw nothing is all zeros
+        const float f = ml.x == -__builtin_inff() && ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += f * v[e];
         l += f * ml.y;
     }
     sum[sub][c] = x;
@@ -306,13 +307,12 @@ __global__ __launch_bounds__(256) void join_kernel(Parts p, T* __restrict__ o, f
     if (sub == 0) {
 #pragma unroll
         for (int s = 1; s < SUB; ++s) {
-            x.x += sum[s][c].x;
-            x.y += sum[s][c].y;
+            x += sum[s][c];
             l += total[s];
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const float out[2] = {x.x * inv, x.y * inv};
-        store_vec_any<T, 2>(o + row * D + 2 * c, out);
+        const float out[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+        store_vec_any<T, 4>(o + row * D + 4 * c, out);
         if (lse && c == 0) lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
     }
 }

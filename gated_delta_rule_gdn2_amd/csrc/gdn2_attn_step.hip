@@ -195,13 +195,14 @@ __global__ __launch_bounds__((64 * kStepWaves<T, D>), 1) void step_kernel(StepPa
     }
 }
 
-// Parts of a sequence: as many as give the GPU two workgroups a CU, of a tile a wave and more.
+// Parts of a sequence: as many as the GPU runs at once (two workgroups a CU; a further few would have it to
+// themselves when the others are done), of whole turns of the waves, and no more of them than those turns need.
 int step_splits(const AttnStepArgs& a) {
     const int64_t share = a.H / a.G, groups = a.N * a.G * ((share + 31) / 32);
     const int waves = a.dtype_bf16 || a.d == 64 ? 4 : 2;
-    const int64_t seen = a.window > 0 && a.window < a.C ? a.window : a.C, most = (seen + kStepKeys * waves - 1) / (kStepKeys * waves);
-    const int64_t want = (2 * (int64_t)a.cus + groups - 1) / groups;
-    return (int)(want < most ? want : most);
+    const int64_t seen = a.window > 0 && a.window < a.C ? a.window : a.C, turns = (seen + kStepKeys * waves - 1) / (kStepKeys * waves);
+    const int64_t want = max((int64_t)1, 2 * (int64_t)a.cus / groups), each = (turns + want - 1) / want;
+    return (int)((turns + each - 1) / each);
 }
 
 template <typename T, int D>
