@@ -509,6 +509,7 @@ ROTARY = [  # dtype, lead, H, G, d, rot, interleaved, far
     (BF16, (300,), 3, 1, 128, 32, False, 1 << 30), (F32, (3, 40), 2, 2, 64, 32, True, 1 << 20), (F32, (1, 1300), 2, 1, 128, 128, False, 0),
     (F32, (9,), 1, 0, 6, 4, False, 100), (BF16, (9,), 3, 1, 10, 6, True, 100), (BF16, (5,), 2, 1, 64, 12, False, 7), (F32, (4,), 2, 1, 512, 512, False, 3),
     (BF16, (2500,), 40, 2, 128, 128, True, 0), (BF16, (1100,), 2, 1, 128, 126, False, 0),
+    (BF16, (33,), 3, 1, 96, 48, False, 9), (F32, (21,), 2, 2, 96, 48, True, 9), (BF16, (40,), 5, 1, 8, 8, True, 50), (F32, (3000,), 1, 0, 16, 8, False, 0),
 ]
 
 
