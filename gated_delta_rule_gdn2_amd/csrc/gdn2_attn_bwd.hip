@@ -216,10 +216,12 @@ __global__ __launch_bounds__(NW * 64, SW > 1 ? (kDqLds<T, D, SW> > 80000 ? 1 : 2
 
 // ---- dk and dv --------------------------------------------------------------------------------
 
-constexpr int kQueries = 32;  // queries in a tile
+// Queries in a tile: at 64 channels of bf16 two blocks of 32, which share the loop's own instructions (8 x 4096
+// tokens, 16 heads: 1033 us for all gradients, 1052 with one).
+template <typename T, int D, int SW> constexpr int kQueries = D * sizeof(T) == 128 && SW == 1 ? 64 : 32;
 // LDS of a tile: queries, d_o, and of each lse in base 2 and -delta; and of the whole workgroup
-template <typename T, int D> constexpr int kStage = 2 * kQueries * Tile<T, D>::kRow + 1024;
-template <typename T, int D, int NW, int SW> constexpr int kDkvLds = SW * 2 * kStage<T, D> + NW / SW * 32 * Tile<T, D>::kRow;
+template <typename T, int D, int SW> constexpr int kStage = 2 * kQueries<T, D, SW> * Tile<T, D>::kRow + 1024;
+template <typename T, int D, int NW, int SW> constexpr int kDkvLds = SW * 2 * kStage<T, D, SW> + NW / SW * 32 * Tile<T, D>::kRow;
 
 // A workgroup takes NW * 32 keys of one key head, a wave 32; the queries that see them come by in tiles, the
 // heads that share them one after the other.  S = Q K^T and dP = d_O V^T have queries in the rows, so that P and
@@ -231,7 +233,7 @@ template <typename T, int D, int NW, int SW, bool FIRST>
 __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* flag) {
     typedef Tile<T, D> L;
     static_assert(SW == 1 || SW == NW, "each wave its own keys, or all the same");
-    constexpr int KS = D / 16, DT = D / 32, BN = NW / SW * 32, BQ = kQueries, BYTES = BQ * L::kRow, STAGE = kStage<T, D>;
+    constexpr int KS = D / 16, DT = D / 32, BN = NW / SW * 32, BQ = kQueries<T, D, SW>, BYTES = BQ * L::kRow, STAGE = kStage<T, D, SW>;
     const int lane = threadIdx.x & 63, g = lane >> 5;
     const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = SW == 1 ? all_waves : 0, part = SW == 1 ? 0 : all_waves;
@@ -271,8 +273,15 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
         const Lds at = base + (part * 2 + buf) * STAGE;
         L::template stage<BQ, NW / SW>(at, a.q + token * p.q_stride + (int64_t)head * L::kRow, span(left, p.q_stride, L::kRow), p.q_stride, wave, lane);
         L::template stage<BQ, NW / SW>(at + BYTES, a.d_o + token * o_stride + (int64_t)head * L::kRow, span(left, o_stride, L::kRow), o_stride, wave, lane);
-        if (wave == 0)  // rows that are none repeat the last
-            load_far_words_to_lds(at + 2 * BYTES, (g ? a.no_delta : a.lse2) + (int64_t)head * a.tokens + token + min(lane & 31, left - 1));
+        if (wave == 0) {  // rows that are none repeat the last
+            const int64_t from = (int64_t)head * a.tokens + token;
+            if constexpr (BQ == 32) {
+                load_far_words_to_lds(at + 2 * BYTES, (g ? a.no_delta : a.lse2) + from + min(lane & 31, left - 1));
+            } else {
+                load_far_words_to_lds(at + 2 * BYTES, a.lse2 + from + min(lane, left - 1));
+                load_far_words_to_lds(at + 2 * BYTES + 256, a.no_delta + from + min(lane, left - 1));
+            }
+        }
     };
     // the workgroup's part of them
     const int all = t1 > t0 ? share * (t1 - t0) : 0, per = (all + (int)gridDim.y - 1) / (int)gridDim.y;
@@ -293,102 +302,108 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
     for (int n = n0; n < count; n += SW) {
         if (SW == 1) tile_barrier();
         else own_tile_wait();
-        const int64_t place = off + (int64_t)t * BQ;  // of the tile's first query
-        const int left = lq - t * BQ;                 // its queries
+        const int64_t place0 = off + (int64_t)t * BQ;  // of the tile's first query
+        const int left0 = lq - t * BQ;                 // its queries
+        const Lds tile = base + (part * 2 + ((n - n0) / SW & 1)) * STAGE;
         if (n + SW < count) {
             after(SW);
             stage(h, t, ((n - n0) / SW + 1) & 1);
         }
-        // no query of the tile sees a key of the wave's; or some query does not see some key, or is none
-        if (rows <= 0 || place + BQ - 1 < mine || place > (int64_t)mine + 30 + p.window) continue;
-        const bool cut = place < (int64_t)mine + 31 || place + BQ - 1 >= (int64_t)mine + p.window || left < BQ;
-        const Lds tq = base + (part * 2 + ((n - n0) / SW & 1)) * STAGE, ts = tq + 2 * BYTES + 16 * g;
-        const Lds rq = opaque(row_base + tq), ro = opaque(row_base + tq + BYTES), rv = opaque(row_base + tv + wave * 32 * L::kRow);
-        f32x16 s = zero16(), dp;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const f32x4 x = lds_get<f32x4>(ts + 128 + 32 * c);
+        for (int u = 0; u < BQ / 32; ++u) {
+            const int64_t place = place0 + 32 * u;
+            const int left = left0 - 32 * u;
+            // no query of the block sees a key of the wave's; or some query does not see some key, or is none
+            if (rows <= 0 || left <= 0 || place + 31 < mine || place > (int64_t)mine + 30 + p.window) continue;
+            const bool cut = place < (int64_t)mine + 31 || place + 31 >= (int64_t)mine + p.window || left < 32;
+            const Lds tq = tile + u * 32 * L::kRow, ts = tile + 2 * BYTES + u * 128 + 16 * g;
+            const Lds rq = opaque(row_base + tq), ro = opaque(row_base + tq + BYTES), rv = opaque(row_base + tv + wave * 32 * L::kRow);
+            f32x16 s = zero16(), dp;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dp[4 * c + e] = x[e];
-        }
-        constexpr int C = sizeof(T) == 2 ? 2 : 1;
+            for (int c = 0; c < 4; ++c) {
+                const f32x4 x = lds_get<f32x4>(ts + BQ * 4 + 32 * c);
 #pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += C) {
-            Op<T> xq[C], xo[C], xv[C];
-#pragma unroll
-            for (int ks = 0; ks < C; ++ks) {
-                xq[ks] = L::row_op(rq, 0, k0 + ks);
-                xo[ks] = L::row_op(ro, 0, k0 + ks);
-                xv[ks] = L::row_op(rv, 0, k0 + ks);
+                for (int e = 0; e < 4; ++e) dp[4 * c + e] = x[e];
             }
-            __builtin_amdgcn_sched_barrier(0);
+            constexpr int C = sizeof(T) == 2 ? 2 : 1;
 #pragma unroll
-            for (int ks = 0; ks < C; ++ks) {
-                mma(s, xq[ks], k[k0 + ks]);
-                mma(dp, xo[ks], xv[ks]);
-            }
-        }
-        float lse[16];
+            for (int k0 = 0; k0 < KS; k0 += C) {
+                Op<T> xq[C], xo[C], xv[C];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const f32x4 x = lds_get<f32x4>(ts + 32 * c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) lse[4 * c + e] = x[e];
-        }
-        Seen seen{0, BQ};  // the queries that see the lane's key
-        if (cut) {
-            const int64_t lo = (int64_t)mine + (lane & 31) - place, hi = min(lo + p.window - 1, (int64_t)left - 1);
-            seen = seen_between((int)min(max(lo, (int64_t)-1), (int64_t)BQ), (int)max((int64_t)-2, min(hi, (int64_t)BQ)));
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sum = watch(watch(watch(sum, s[i]), dp[i]), lse[i]);
-                s[i] = seen(acc_row(i, g)) ? s[i] : -__builtin_inff();
-            }
-            if (FIRST) again = again || __any(sum != 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale_log2, -lse[i]));
-            dp[i] *= s[i];
-        }
-        if (!FIRST && cut) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool yes = seen(acc_row(i, g));
-                s[i] = yes ? s[i] : 0.f;
-                dp[i] = yes ? dp[i] : 0.f;
-            }
-        }
-        Op<T> pr[BQ / 16], ds[BQ / 16];
-#pragma unroll
-        for (int c = 0; c < BQ / 16; ++c) {
-            pr[c] = op_of<T>(s, c);
-            ds[c] = op_of<T>(dp, c);
-        }
-        const Lds cq = opaque(col_base + tq), co = opaque(col_base + tq + BYTES);
-        if (!FIRST && cut) {
-            // a query that is not finite has made its dS a NaN where it sees the key, so its own product takes
-            // the finite part; d_o adds to dv what is not finite in it
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) {
-                const f32x16 add = special_sum<T, D, BQ>(co, dt, seen, g, false);
-#pragma unroll
-                for (int c = 0; c < BQ / 16; ++c) {
-                    mma(dv[dt], finite_part<T>(L::col_op(co, 16 * c, dt)), pr[c]);
-                    mma(dk[dt], finite_part<T>(L::col_op(cq, 16 * c, dt)), ds[c]);
+                for (int ks = 0; ks < C; ++ks) {
+                    xq[ks] = L::row_op(rq, 0, k0 + ks);
+                    xo[ks] = L::row_op(ro, 0, k0 + ks);
+                    xv[ks] = L::row_op(rv, 0, k0 + ks);
                 }
-                dv[dt] += add;
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int ks = 0; ks < C; ++ks) {
+                    mma(s, xq[ks], k[k0 + ks]);
+                    mma(dp, xo[ks], xv[ks]);
+                }
             }
-            continue;
+            float lse[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const f32x4 x = lds_get<f32x4>(ts + 32 * c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) lse[4 * c + e] = x[e];
+            }
+            Seen seen{0, 32};  // the queries that see the lane's key
+            if (cut) {
+                const int64_t lo = (int64_t)mine + (lane & 31) - place, hi = min(lo + p.window - 1, (int64_t)left - 1);
+                seen = seen_between((int)min(max(lo, (int64_t)-1), (int64_t)32), (int)max((int64_t)-2, min(hi, (int64_t)32)));
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sum = watch(watch(watch(sum, s[i]), dp[i]), lse[i]);
+                    s[i] = seen(acc_row(i, g)) ? s[i] : -__builtin_inff();
+                }
+                if (FIRST) again = again || __any(sum != 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], p.scale_log2, -lse[i]));
+                dp[i] *= s[i];
+            }
+            if (!FIRST && cut) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const bool yes = seen(acc_row(i, g));
+                    s[i] = yes ? s[i] : 0.f;
+                    dp[i] = yes ? dp[i] : 0.f;
+                }
+            }
+            Op<T> pr[2], ds[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                pr[c] = op_of<T>(s, c);
+                ds[c] = op_of<T>(dp, c);
+            }
+            const Lds cq = opaque(col_base + tq), co = opaque(col_base + tq + BYTES);
+            if (!FIRST && cut) {
+                // a query that is not finite has made its dS a NaN where it sees the key, so its own product takes
+                // the finite part; d_o adds to dv what is not finite in it
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    const f32x16 add = special_sum<T, D, 32>(co, dt, seen, g, false);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        mma(dv[dt], finite_part<T>(L::col_op(co, 16 * c, dt)), pr[c]);
+                        mma(dk[dt], finite_part<T>(L::col_op(cq, 16 * c, dt)), ds[c]);
+                    }
+                    dv[dt] += add;
+                }
+                continue;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    mma(dv[dt], L::col_op(co, 16 * c, dt), pr[c]);
+                    mma(dk[dt], L::col_op(cq, 16 * c, dt), ds[c]);
+                }
         }
-#pragma unroll
-        for (int c = 0; c < BQ / 16; ++c)
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) {
-                mma(dv[dt], L::col_op(co, 16 * c, dt), pr[c]);
-                mma(dk[dt], L::col_op(cq, 16 * c, dt), ds[c]);
-            }
     }
     if (FIRST && again) *flag = 1;
     lds_barrier();
@@ -483,8 +498,6 @@ hipError_t run_dkv(BwdParams x, int splits, hipStream_t stream) {
 // heads of 64 sharing 2, bf16, took 478 us in all with 64 workgroups, 180 us shared, 150 us in two parts (below);
 // 4 x 4096 tokens, 16 heads sharing 8: 593 and 559; 16 x 1000 tokens of 12 heads: 160 and 173.  Heads of 128 take
 // twice the LDS: 8192 tokens, 8 heads sharing 4, 859 and 781; 2 x 4096 tokens, 16 heads sharing 8, 605 and 743.
-// Packed sequences differ in length, and the longest one's loops end last: 16 of 4096 tokens and fewer, 12 heads
-// of 64, 253 and 243.
 // With fewer workgroups than the GPU runs at once the tiles of queries are taken in parts whose sums a further
 // launch joins: the same 4096 tokens of 4 heads sharing one, 143 us in one part, 82 in four.
 struct BwdForm {
@@ -497,7 +510,7 @@ BwdForm bwd_form(const Shape& p, int64_t d, bool is_bf16, int64_t cus) {
         return (p.cu_q ? b + p.n - 1 : b * p.n) * heads;
     };
     const int64_t wq = workgroups(p.tq, p.heads), wk = workgroups(p.tk, p.groups);
-    BwdForm f{wq <= 2 * cus, wk <= (d == 64 ? (p.cu_q ? 32 : 16) : is_bf16 ? 4 : 2) * cus, 1};
+    BwdForm f{wq <= 2 * cus, wk <= (d == 64 ? 16 : is_bf16 ? 4 : 2) * cus, 1};
     // tiles of queries that see a block of keys, and those that a part is worth
     const int64_t tiles = (min((int64_t)p.window + 32, p.tq) + 31) / 32 * (p.heads / p.groups), least = is_bf16 ? 16 : 4;
     if (f.share_k && wk > 0) f.splits = (int)max((int64_t)1, min(tiles / least, 2 * cus / wk));
