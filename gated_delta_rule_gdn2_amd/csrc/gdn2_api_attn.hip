@@ -101,8 +101,8 @@ gdn2_status_t attn_fwd(gdn2::AttnArgs a, gdn2_dtype_t dtype, void* workspace, si
     if (st != GDN2_OK) return st;
     if (b.o && !a.o) return GDN2_ERR_NULL;
     size_t need = 0;
+    a.cus = cus_or_default();
     if (workspace || workspace_bytes) {
-        a.cus = cus_or_default();
         need = b.tokens_q ? gdn2::attn_fwd_workspace_bytes(a) : 0;
         if (need == 0 || !workspace || workspace_bytes < need) return GDN2_ERR_WORKSPACE;
         if (!aligned_to(workspace, 16)) return GDN2_ERR_MISALIGNED;

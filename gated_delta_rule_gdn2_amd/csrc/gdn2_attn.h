@@ -459,12 +459,17 @@ struct Shape {
     int blocks;           // blocks of a head: of every sequence's, or of all packed ones
     unsigned all_groups;  // key heads of all sequences (packed: key heads)
     int slice_bits;       // a group's blocks are dealt out in 2^slice_bits slices, so that every XCD has as many
+    unsigned turn;        // slices of an XCD that take turns
 };
 
 // Workgroups go to the 8 XCDs in turn, each with an L2 of its own: the blocks of one group (a
 // sequence's key head; packed, a key head) stay on one XCD, or with fewer groups than XCDs are dealt
 // out in `slices`.  Within a slice the blocks with the most work come first, the heads of the group
-// side by side.
+// side by side.  `turn` slices of an XCD take turns, so that no heavy block starts late: as many as make kTurn
+// workgroups, and no more, because those that run at once share keys and values in L2.  Forward and backward
+// pass, us, one slice after the other, with 256 and with 8192 workgroups: 8 x 1024 tokens of 16 heads of 128, 63,
+// 50, 50 and 203, 172, 173; 32 x 4096 tokens, 2296, 2308, 3684 and 7347, 7089, 8926; the gradients of 16 packed
+// sequences of 20 to 4096 tokens, 12 heads of 64, 249 and 196 with 256.
 struct Work {
     Seq s;
     int block, head;  // head: of `per_group` in each group
@@ -472,11 +477,12 @@ struct Work {
 __device__ __forceinline__ bool find_work(const Shape& p, int rows, int per_group, bool last_first, bool keys, int lane, Work* w) {
     const unsigned x = blockIdx.x & 7, r = blockIdx.x >> 3;
     const unsigned per = (p.blocks + (1u << p.slice_bits) - 1) >> p.slice_bits, each = per * per_group;
-    const unsigned slice = r / each * 8 + x, group = slice >> p.slice_bits;
-    const unsigned in = r % each, nth = in / per_group;
+    const unsigned slices = (p.all_groups << p.slice_bits) >> 3, before = r / (each * p.turn) * p.turn;  // of an XCD
+    const unsigned width = min(slices - before, p.turn), rest = r % (each * p.turn) / (unsigned)per_group;
+    const unsigned slice = (before + rest % width) * 8 + x, group = slice >> p.slice_bits, nth = rest / width;
     const unsigned index = ((last_first && !p.cu_q ? per - 1 - nth : nth) << p.slice_bits) + (slice & ((1u << p.slice_bits) - 1));
     if (group >= p.all_groups || index >= (unsigned)p.blocks) return false;
-    w->head = (int)(group % (unsigned)p.groups) * per_group + in % per_group;
+    w->head = (int)(group % (unsigned)p.groups) * per_group + r % (unsigned)per_group;
     if (p.cu_q) {
         int64_t seq;
         int blocks;
@@ -494,6 +500,7 @@ __device__ __forceinline__ bool find_work(const Shape& p, int rows, int per_grou
 __device__ __forceinline__ Work uniform(const Work& w) {
     return Work{Seq{uniform(w.s.q0), uniform(w.s.k0), uniform(w.s.lq), uniform(w.s.lk)}, uniform(w.block), uniform(w.head)};
 }
+constexpr int64_t kTurn = 256;
 constexpr int64_t kMaxGrid = (int64_t)1 << 23;  // workgroups of up to 512 threads: a launch has less than 2^32
 // fills in how work is dealt out; workgroups of the launch (0: none), or -1 if they are too many
 inline int64_t deal(Shape* p, int64_t tokens, int rows, int per_group) {
@@ -505,8 +512,10 @@ inline int64_t deal(Shape* p, int64_t tokens, int rows, int per_group) {
     p->slice_bits = 0;
     while ((groups << p->slice_bits) % 8) ++p->slice_bits;
     const int64_t per = (blocks + ((int64_t)1 << p->slice_bits) - 1) >> p->slice_bits;
-    const int64_t grid = (groups << p->slice_bits) * per;
-    return grid < kMaxGrid && grid * per_group < kMaxGrid ? grid * per_group : -1;
+    const int64_t grid = (groups << p->slice_bits) * per, slices = (groups << p->slice_bits) / 8;
+    if (grid >= kMaxGrid) return -1;
+    p->turn = (unsigned)(grid > 0 ? min(slices, (kTurn + per * per_group - 1) / (per * per_group)) : 1);
+    return grid * per_group < kMaxGrid ? grid * per_group : -1;
 }
 
 struct Yes { static constexpr bool value = true; };

@@ -494,12 +494,12 @@ hipError_t run_dkv(BwdParams x, int splits, hipStream_t stream) {
 
 // How the backward pass is launched.  Workgroups whose waves share 32 queries or keys are four times as many,
 // with loops a fourth as long, but read the other side's tiles four times as often, and with more LDS each fewer
-// run at once.  dk and dv, whose loops go over the heads that share a key head too, gain most: 4096 tokens, 8
-// heads of 64 sharing 2, bf16, took 478 us in all with 64 workgroups, 180 us shared, 150 us in two parts (below);
-// 4 x 4096 tokens, 16 heads sharing 8: 593 and 559; 16 x 1000 tokens of 12 heads: 160 and 173.  Heads of 128 take
-// twice the LDS: 8192 tokens, 8 heads sharing 4, 859 and 781; 2 x 4096 tokens, 16 heads sharing 8, 605 and 743.
+// run at once.  dk and dv, whose loops go over the heads that share a key head too, gain most.  All gradients in
+// us, bf16, without and with shared keys: 4096 tokens of 8 heads of 64 sharing 2, 399 and 145 (124 with shared
+// queries as well); 2 x 4096 of 16 sharing 8, 300 and 277; 4 x 4096, 477 and 530.  Heads of 128 take twice the
+// LDS: 4096 tokens of 16 heads sharing 4, 668 and 389; 2 x 4096 of 16 sharing 8, 525 and 695.
 // With fewer workgroups than the GPU runs at once the tiles of queries are taken in parts whose sums a further
-// launch joins: the same 4096 tokens of 4 heads sharing one, 143 us in one part, 82 in four.
+// launch joins: 4096 tokens of 4 heads of 64 sharing one, 143 us in one part, 82 in four.
 struct BwdForm {
     bool share_q, share_k;
     int splits;  // parts that dk and dv are taken in
@@ -510,7 +510,8 @@ BwdForm bwd_form(const Shape& p, int64_t d, bool is_bf16, int64_t cus) {
         return (p.cu_q ? b + p.n - 1 : b * p.n) * heads;
     };
     const int64_t wq = workgroups(p.tq, p.heads), wk = workgroups(p.tk, p.groups);
-    BwdForm f{wq <= 2 * cus, wk <= (d == 64 ? 16 : is_bf16 ? 4 : 2) * cus, 1};
+    const int64_t seen = min((int64_t)p.window + 32, p.tk);  // keys that a block of queries sees
+    BwdForm f{wq <= (d == 64 && seen >= 2048 ? 4 : 2) * cus, wk <= (d == 64 ? 8 : is_bf16 ? 4 : 2) * cus, 1};
     // tiles of queries that see a block of keys, and those that a part is worth
     const int64_t tiles = (min((int64_t)p.window + 32, p.tq) + 31) / 32 * (p.heads / p.groups), least = is_bf16 ? 16 : 4;
     if (f.share_k && wk > 0) f.splits = (int)max((int64_t)1, min(tiles / least, 2 * cus / wk));

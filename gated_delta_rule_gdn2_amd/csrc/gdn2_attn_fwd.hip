@@ -328,11 +328,11 @@ hipError_t launch_join(const Parts& p, void* o, float* lse, int64_t d, bool bf16
 
 // How the forward pass is launched.  Workgroups whose waves share 32 queries are four times as many, and their
 // loops a fourth as long, but they read keys and values four times as often: they are taken while they fit the
-// GPU in two rounds (fp32 heads of 128, which two waves share: while they leave most of it idle).  bf16 in
-// us, shared against not: 14 and 24 at 1024 tokens of 4 heads of 64, 36 and 56 at 4096 of 8, 64 and 60 of 16;
-// heads of 128: 15 and 24, 96 and 84, 191 and 96.
+// GPU in about two rounds (fp32 heads of 128, which two waves share: while they leave most of it idle).  bf16 in
+// us, without and with: 4096 tokens of 4 heads of 64 sharing one, 39 and 24; of 8 sharing 2, 59 and 35; of 16
+// sharing 4, 60 and 63; heads of 128: 1024 tokens of 4 heads, 24 and 15; of 16, 25 and 22; 4096 of 8, 83 and 96.
 // With few workgroups and many keys a block's keys are also taken in parts, as many as fill the GPU, whose sums
-// a second launch joins: 4096 tokens of one head of 64 take 19 us in 4 parts, 23 in one.  (Sequences that
+// a second launch joins: 4096 tokens of one head of 64 take 18 us in 4 parts, 23 in one.  (Sequences that
 // are packed may be shorter than the longest: their parts are, too.)
 struct FwdForm {
     bool share;
