@@ -256,10 +256,10 @@ __device__ __forceinline__ void tile_barrier() {
     __syncthreads();
 }
 
-// The same for a wave's own loads and LDS.
+// The same for a wave's own loads and LDS; what it read there has arrived, too.
 __device__ __forceinline__ void own_tile_wait() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
     __builtin_amdgcn_wave_barrier();
     asm volatile("" ::: "memory");
 }
@@ -303,45 +303,18 @@ __device__ __forceinline__ float watch(float sum, float x) { return __builtin_fm
 
 // ---- values that are not finite -------------------------------------------------------------
 // A product over a tile's rows multiplies what a mask hides by zero, which an infinity or a NaN there
-// survives.  Tiles that a mask cuts are therefore searched.  Where something is found, a product with
-// the mask itself says which infinities and NaN each column sees, and the tile is cleared of them
-// before the product with the weights.
+// survives.  Kernels therefore take tiles as they are and look at what came of it; where something is not
+// finite, the workgroup starts again in a form in which, in tiles that a mask cuts, a product with the mask
+// itself says which infinities and NaN each column sees, and the tile's finite part meets the weights.
 
 __device__ __forceinline__ bool finite_bits(bf16 x) { return (__builtin_bit_cast(unsigned short, x) & 0x7f80u) != 0x7f80u; }
 __device__ __forceinline__ bool finite_bits(float x) { return (__builtin_bit_cast(unsigned, x) & 0x7f800000u) != 0x7f800000u; }
 
-// whether this thread's part of a tile of BYTES bytes holds a value that is not finite
-template <typename T, int BYTES, int NT>
-__device__ __forceinline__ bool any_special(Lds lds, int tid) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 two = 0;
-    uint32_t one = 0;
-#pragma unroll
-    for (int u = 0; u < BYTES / 16 / NT; ++u) {
-        const u32x4 x = lds_get<u32x4>(lds + (u * NT + tid) * 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // the largest exponent and mantissa
-            if constexpr (sizeof(T) == 2)
-                two = __builtin_elementwise_max(two, __builtin_bit_cast(u16x2, x[e] & 0x7fff7fffu));
-            else
-                one = __builtin_elementwise_max(one, x[e] & 0x7fffffffu);
-        }
-    }
-    return sizeof(T) == 2 ? two[0] >= 0x7f80u || two[1] >= 0x7f80u : one >= 0x7f800000u;
-}
 template <typename T> __device__ __forceinline__ Op<T> finite_part(Op<T> a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (!finite_bits((T)a.v[e])) a.v[e] = from_f32<T>(0.f);
     return a;
-}
-// the thread's part of the tile with zeros for what is not finite
-template <typename T, int BYTES, int NT>
-__device__ __forceinline__ void clear_special(Lds lds, int tid) {
-    for (int u = tid; u < BYTES / (int)sizeof(T); u += NT) {
-        GDN2_LDS T* x = (GDN2_LDS T*)(uintptr_t)(lds + u * (int)sizeof(T));
-        if (!finite_bits((T)*x)) *x = from_f32<T>(0.f);
-    }
 }
 // 1 for a NaN, 128 for an infinity, 16384 for a negative one: sums over up to 64 rows keep the three
 // counts apart, and are exact
@@ -386,12 +359,6 @@ __device__ __forceinline__ f32x16 special_sum(Lds base, int dt, Seen seen, int g
     for (int i = 0; i < 16; ++i) code[i] = nan && code[i] > 0.f ? __builtin_nanf("") : from_code(code[i]);
     return code;
 }
-// All columns of it, by a call of its own and through memory, so that the loop around it keeps its registers.
-template <typename T, int D, int ROWS>
-__device__ __attribute__((noinline)) void special_sums(f32x16* out, Lds base, Seen seen, int g, bool nan) {
-    for (int dt = 0; dt < D / 32; ++dt) out[dt] = special_sum<T, D, ROWS>(base, dt, seen, g, nan);
-}
-
 // ---- which workgroup does what --------------------------------------------------------------
 
 struct Seq {
@@ -517,9 +484,6 @@ inline int64_t deal(Shape* p, int64_t tokens, int rows, int per_group) {
     p->turn = (unsigned)(grid > 0 ? min(slices, (kTurn + per * per_group - 1) / (per * per_group)) : 1);
     return grid * per_group < kMaxGrid ? grid * per_group : -1;
 }
-
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
 
 // Rows whose keys were taken in parts: unnormalised sums o [splits][rows][d] in fp32, and of each row
 // and part the reference (base 2) and the sum (ml).  lse may be nullptr.

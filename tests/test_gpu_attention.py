@@ -268,6 +268,7 @@ PACKED = [  # dtype, query lengths, keys before them, H, G, d, window
     (BF16, [129, 257, 1], None, 2, 1, 128, 100),
     (BF16, [7, 65, 0, 128], [200, 0, 50, 31], 4, 1, 128, None),
     (BF16, [3, 1, 2], [700, 1500, 0], 2, 2, 64, 900),
+    (BF16, [300, 40, 1], None, 8, 1, 64, None), (BF16, [9, 190, 64], [70, 0, 3], 12, 2, 128, 150),
     (F32, [40, 0, 1, 100], None, 2, 1, 64, 30),
     (F32, [20, 66], [90, 3], 2, 1, 128, None),
 ]
@@ -342,6 +343,20 @@ def test_parts_of_the_keys_against_whole(dtype):
     assert (buf[:256] == 0x5a).all() and (buf[256 + need + 16:] == 0x5a).all()
     for x, y in ((o, lse), (o2, lse2)):
         check_fwd(q[0], k[0], v[0], x[0], y[0])
+
+
+@pytest.mark.parametrize("dtype,B,T,S,H,G,d", [(BF16, 1, 700, 700, 8, 1, 64), (F32, 2, 90, 130, 6, 2, 128), (BF16, 40, 65, 65, 2, 2, 128)])
+def test_gradients_keep_to_their_workspace(dtype, B, T, S, H, G, d):
+    """In a caller's workspace between guard bytes, which it need not clear: the same bits."""
+    q, k, v, g = (x.cuda() for x in case(dtype, T, S, H, G, d, 21, B))
+    o, lse = gdn2.attn_fwd(q, k, v)
+    want = gdn2.attn_bwd(g, q, k, v, o, lse)
+    need = gdn2.attn_bwd_workspace_bytes(B, T, S, H, G, d, dtype=dtype)
+    for fill in (0x5a, 0xff):
+        buf = torch.full((need + 512,), fill, dtype=torch.uint8, device="cuda")
+        got = gdn2.attn_bwd(g, q, k, v, o, lse, workspace=buf[256:256 + need + 16])
+        assert all(torch.equal(want[n], got[n]) for n in want)
+        assert (buf[:256] == fill).all() and (buf[256 + need + 16:] == fill).all()
 
 
 def test_addresses_past_32_bits():
