@@ -428,7 +428,14 @@ __device__ __forceinline__ bool dkv_block(const BwdParams& a, Lds base, int* fla
         else if (live) sums.template store<float>(parts + size, 1.f, part, g);
         return any;
     }
-    if (rows > 0 && !again) {
+    if (rows > 0 && !again && gridDim.y > 1) {
+        const int64_t size = a.keys * p.groups * D;
+        float* parts = a.parts + 2 * blockIdx.y * size + ((w.s.k0 + mine + (lane & 31)) * p.groups + kv) * D;
+        if ((lane & 31) < rows) {
+            store_column<float, D>(parts, dk, 1.f, g);
+            store_column<float, D>(parts + size, dv, 1.f, g);
+        }
+    } else if (rows > 0 && !again) {
         const int64_t at = ((w.s.k0 + mine) * p.groups + kv) * L::kRow, stride = (int64_t)p.groups * L::kRow;
         const Lds own = base + wave * 32 * L::kRow;
         store_rows<T, D>(own, (char*)a.dk + at, stride, rows, dk, p.scale, lane);
@@ -500,25 +507,31 @@ hipError_t run_dkv(BwdParams x, int splits, hipStream_t stream) {
 // with loops a fourth as long, but read the other side's tiles four times as often, and with more LDS each fewer
 // run at once.  dk and dv, whose loops go over the heads that share a key head too, gain most.  All gradients in
 // us, bf16, without and with shared keys: 4096 tokens of 8 heads of 64 sharing 2, 399 and 145 (124 with shared
-// queries as well); 2 x 4096 of 16 sharing 8, 300 and 277; 4 x 4096, 477 and 530.  Heads of 128 take twice the
-// LDS: 4096 tokens of 16 heads sharing 4, 668 and 389; 2 x 4096 of 16 sharing 8, 525 and 695.
-// With fewer workgroups than the GPU runs at once the tiles of queries are taken in parts whose sums a further
-// launch joins: 4096 tokens of 4 heads of 64 sharing one, 143 us in one part, 82 in four.
+// queries as well); 2 x 4096 of 16 sharing 8, 300 and 277; 4 x 4096, 477 and 530.
+// With fewer workgroups than the GPU runs at once the tiles of queries are also taken in parts whose sums a further
+// launch joins: 4096 tokens of 4 heads of 64 sharing one, 143 us in one part, 82 in four.  Heads of 128 take twice
+// the LDS, so that parts serve better than sharing but for few keys and short loops: 4096 tokens of 16 heads
+// sharing 4, 391 us with shared keys, 354 in 8 parts (716 in one); 3 x 700 of 6 sharing 3, 67 and 74.  Shared queries
+// need fewer workgroups yet where loops are short: the same of 64 channels, 38 us with, 32 without.
 struct BwdForm {
     bool share_q, share_k;
     int splits;  // parts that dk and dv are taken in
 };
 BwdForm bwd_form(const Shape& p, int64_t d, bool is_bf16, int64_t cus) {
-    auto workgroups = [&](int64_t tokens, int64_t heads) {
-        const int64_t b = (tokens + 31) / 32;
+    auto workgroups = [&](int64_t tokens, int64_t rows, int64_t heads) {
+        const int64_t b = (tokens + rows - 1) / rows;
         return (p.cu_q ? b + p.n - 1 : b * p.n) * heads;
     };
-    const int64_t wq = workgroups(p.tq, p.heads), wk = workgroups(p.tk, p.groups);
+    const int64_t wq = workgroups(p.tq, 32, p.heads), wk = workgroups(p.tk, 32, p.groups);
     const int64_t seen = min((int64_t)p.window + 32, p.tk);  // keys that a block of queries sees
-    BwdForm f{wq <= (d == 64 && seen >= 2048 ? 4 : 2) * cus, wk <= (d == 64 ? 8 : is_bf16 ? 4 : 2) * cus, 1};
-    // tiles of queries that see a block of keys, and those that a part is worth
-    const int64_t tiles = (min((int64_t)p.window + 32, p.tq) + 31) / 32 * (p.heads / p.groups), least = is_bf16 ? 16 : 4;
-    if (f.share_k && wk > 0) f.splits = (int)max((int64_t)1, min(tiles / least, 2 * cus / wk));
+    // tiles of queries that see a block of keys (in packed sequences up to four times as long as their mean)
+    const int64_t longest = p.cu_q ? min(p.tq, 4 * p.tq / p.n) : p.tq;
+    const int64_t tiles = (min((int64_t)p.window + 32, longest) + 31) / 32 * (p.heads / p.groups);
+    BwdForm f{wq <= (d == 64 && seen >= 2048 ? 4 : !is_bf16 || seen >= 1024 ? 2 : 1) * cus, d == 64 ? wk <= 8 * cus : wk < (is_bf16 ? cus : cus / 2) && tiles < 128, 1};
+    const int64_t least = !is_bf16 ? 4 : f.share_k ? 32 : 16;  // tiles that a part is worth
+    const int64_t w = f.share_k ? wk : workgroups(p.tk, 128, p.groups);
+    const int64_t want = w == 0 || (d == 64 && !f.share_k) ? 1 : f.share_k ? 2 * cus / w : (3 * cus + w - 1) / w;
+    f.splits = (int)max((int64_t)1, min(tiles / least, want));
     return f;
 }
 
@@ -527,7 +540,7 @@ hipError_t run_bwd(const BwdParams& b, const BwdForm& f, hipStream_t stream) {
     constexpr int SW = D * sizeof(T) > 256 ? 2 : 4;  // what LDS has room for
     const hipError_t e = f.share_q ? run_dq<T, D, SW, SW>(b, stream) : run_dq<T, D, 4, 1>(b, stream);
     if (e != hipSuccess) return e;
-    return f.share_k ? run_dkv<T, D, SW, SW>(b, f.splits, stream) : run_dkv<T, D, 4, 1>(b, 1, stream);
+    return f.share_k ? run_dkv<T, D, SW, SW>(b, f.splits, stream) : run_dkv<T, D, 4, 1>(b, f.splits, stream);
 }
 
 }  // namespace attn

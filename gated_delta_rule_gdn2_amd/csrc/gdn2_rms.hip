@@ -3,6 +3,7 @@
 //
 //   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd gamma
 //   8 bits (e4m3): scale = max|y| / 448 of a row (1 for a row of zeros), the output y / scale
+//   (max|y| at least 2^-110)
 // and with u = h rstd, v = dy gamma:
 //   dx = dh + rstd (v - u mean(u v)),  dgamma = sum over rows of dy u.
 //
@@ -19,6 +20,7 @@ namespace gdn2 {
 namespace norm {
 
 constexpr float kE4m3Max = 448.f;
+constexpr float kLeastTop = 0x1p-110f;  // below, the scale and its reciprocal would leave fp32's normal range
 
 // vectors of V values, stored as 8 bits each
 template <int LANES, int NV, int V, typename F>
@@ -87,6 +89,7 @@ __global__ __launch_bounds__(kThreads<LANES>) void rms_kernel(const T* __restric
             for (int i = 0; i < E; ++i) top = fmaxf(top, fabsf(v[i]));
             top = row_max<LANES>(top, scratch, 1);
             if (!(r == r)) top = r;  // a row of NaN has a scale that says so
+            if (top < kLeastTop && top > 0.f) top = kLeastTop;
             const float sc = top == 0.f ? 1.f : top * (1.f / kE4m3Max), to = top == 0.f ? 1.f : kE4m3Max / top;
             store_row_e4m3<LANES, NV, V>((uint8_t*)y + row * width, lane, width, [&](int i) { return v[i] * to; });
             if (lane == 0) scale[row] = sc;

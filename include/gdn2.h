@@ -700,7 +700,7 @@ gdn2_status_t gdn2_rms_norm(const void* x, const void* residual, const float* ga
 
 /* gdn2_rms_norm_fp8 -- the same with y in 8 bits (e4m3, [rows, width] bytes) and a scale for
  * each row (float32 [rows]): scale = max|y| / 448, or 1 for a row of zeros, and the byte is
- * the value nearest to y / scale. */
+ * the value nearest to y / scale.  (max|y| counts as 2^-110 if it is less and not zero.) */
 gdn2_status_t gdn2_rms_norm_fp8(const void* x, const void* residual, const float* gamma, void* y,
                                 float* scales, void* h, float* rstd, int64_t rows, int64_t width,
                                 float eps, gdn2_dtype_t dtype, gdn2_dtype_t residual_dtype, void* stream);

@@ -645,6 +645,20 @@ def test_rms_norm_gradients_match_oracle(dtype, hdtype, stream, rows, width):
         assert again["dx"] is dev[4] and torch.equal(again["dx"], out["dx"]) and torch.equal(again["dgamma"], out["dgamma"])
 
 
+@pytest.mark.parametrize("size", [2.0 ** -109, 2.0 ** -112, 2.0 ** -120, 2.0 ** -126])
+def test_rms_norm_fp8_of_tiny_rows(size):
+    """Rows so small that 448 over the largest value leaves fp32: zeros stay zeros, the others within a half step."""
+    x = torch.ones(3, 96)
+    x[1, ::2], x[2, 5:] = 0, 0
+    gamma = torch.full((96,), size)
+    y, scales, _, _ = gdn2.rms_norm_fp8(x.cuda(), gamma.cuda(), 1e-6)
+    ref = A.rms_norm(x, gamma, 1e-6)[0]
+    s, got = f64(scales)[:, None], f64(y.float()) * f64(scales)[:, None]
+    assert np.isfinite(got).all() and (s > 0).all()
+    bar = np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * s) + 64 * U * np.abs(ref)
+    assert (np.abs(got - ref) <= bar).all() and (got[ref == 0] == 0).all()
+
+
 def test_norm_of_no_rows_and_in_place():
     gamma = torch.rand(64, device="cuda")
     y, h, rstd = gdn2.rms_norm(torch.empty(0, 64, dtype=BF16, device="cuda"), gamma, residual=torch.empty(0, 64, device="cuda"))
