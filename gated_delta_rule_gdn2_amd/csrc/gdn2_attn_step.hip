@@ -8,8 +8,8 @@
 //
 // Bound by reading the caches once.  The query heads of a key head (up to 32 a workgroup) are the
 // columns of one product, so that a key is read once for all of them.  A workgroup takes a part of the
-// tokens; its waves take tiles of 32 of them in turn, each through LDS of its own and a tile ahead, so
-// no barrier stops the loads.  Every wave keeps a maximum, a sum and an output of its own; they are
+// tokens; its waves take tiles of 32 of them in turn, each through LDS of its own and ahead of their use,
+// so no barrier stops the loads.  Every wave keeps a maximum, a sum and an output of its own; they are
 // joined at the end, and parts of a sequence in a second launch.
 //
 // 256 sequences over 2048 tokens, 16 heads of 128 sharing 2, bf16: 78 us, 5.0 TB/s (a copy of 2 GiB: 4.9).  3
@@ -36,7 +36,7 @@ struct StepParams {
 };
 
 constexpr int kStepKeys = 32;
-template <typename T, int D> constexpr int kStepWaves = D * sizeof(T) > 256 ? 2 : 4;  // LDS of two tiles of both each
+constexpr int kStepWaves = 4;
 
 __device__ __forceinline__ void arrived(Op<bf16>& x) { asm volatile("" : "+v"(x.v)); }
 __device__ __forceinline__ void arrived(Op<float>& x) {
@@ -44,12 +44,28 @@ __device__ __forceinline__ void arrived(Op<float>& x) {
     for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(x.v[e]));
 }
 
+// all but a wave's last LEFT loads have arrived
+template <int LEFT> __device__ __forceinline__ void arrive() {
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (LEFT & 15) | (LEFT >> 4) << 14);
+    asm volatile("" ::: "memory");
+}
+// a wave has read what it asked LDS for
+__device__ __forceinline__ void have_read() {
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
 template <typename T, int D>
-__global__ __launch_bounds__((64 * kStepWaves<T, D>), 1) void step_kernel(StepParams a) {
+__global__ __launch_bounds__(64 * kStepWaves, 1) void step_kernel(StepParams a) {
     typedef Tile<T, D> L;
-    constexpr int NW = kStepWaves<T, D>, KS = D / 16, DT = D / 32, BYTES = kStepKeys * L::kRow, LOADS = BYTES / 1024;
+    constexpr int NW = kStepWaves, KS = D / 16, DT = D / 32, BYTES = kStepKeys * L::kRow, LOADS = BYTES / 1024;
     constexpr int ROW = D + 4;  // floats of a row of the join: rows 4 banks apart
-    constexpr int TILES = NW * 4 * BYTES, JOIN = NW * 32 * ROW * 4;
+    // In bf16 the next tile's keys and values are on their way while a tile is used.  In fp32, whose tiles are twice
+    // the bytes, the next keys' place is the keys', and they come while weights and values are multiplied; values
+    // come while scores are formed: either takes the matrix units longer than a load.  So four waves have room for
+    // heads of 128 (64 sequences over 4096 tokens, 16 heads sharing 2: 122 us; 189 with two waves, tiles ahead).
+    constexpr bool TWO = sizeof(T) == 2;
+    constexpr int TILES = NW * (TWO ? 4 : 2) * BYTES, JOIN = NW * 32 * ROW * 4;
     __shared__ __attribute__((aligned(1024))) char lds[TILES > JOIN ? TILES : JOIN];
     __shared__ float2 ml[NW][32];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
@@ -87,10 +103,10 @@ __global__ __launch_bounds__((64 * kStepWaves<T, D>), 1) void step_kernel(StepPa
     for (int dt = 0; dt < DT; ++dt) o[dt] = zero16();
     float m = -__builtin_inff(), l = 0.f;
 
-    const Lds mine = lds_of(lds) + wave * 4 * BYTES, row_base = L::row_base(lane), col_base = L::col_base(lane);
+    const Lds mine = lds_of(lds) + wave * (TWO ? 4 : 2) * BYTES, row_base = L::row_base(lane), col_base = L::col_base(lane);
     // Tile t's keys and values.  The newest token comes from the call: its slot is being written.  Rows
     // behind it repeat it, so that what the mask hides there is no value that another row does not have.
-    auto stage = [&](int64_t t, int buf) {
+    auto stage = [&](int64_t t, int buf, bool keys, bool values) {
         const Lds at = mine + buf * 2 * BYTES;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
@@ -99,12 +115,12 @@ __global__ __launch_bounds__((64 * kStepWaves<T, D>), 1) void step_kernel(StepPa
             int64_t slot = oldest + token;
             if (slot >= a.cache) slot -= a.cache;
             const bool last = token >= seen - 1;
-            load_far_to_lds(at + i * 1024, (last ? kin : kc + slot * row_bytes) + off);
-            load_far_to_lds(at + BYTES + i * 1024, (last ? vin : vc + slot * row_bytes) + off);
+            if (keys) load_far_to_lds(at + i * 1024, (last ? kin : kc + slot * row_bytes) + off);
+            if (values) load_far_to_lds(at + BYTES + i * 1024, (last ? vin : vc + slot * row_bytes) + off);
         }
     };
     int buf = 0;
-    if (t0 + wave < t1) stage(t0 + wave, 0);
+    if (t0 + wave < t1) stage(t0 + wave, 0, true, true);
     Op<T> q[KS];
     {
         const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(a.q + n * a.q_stride + head0 * L::kRow), 0, heads * L::kRow, 0x00020000);
@@ -115,18 +131,18 @@ __global__ __launch_bounds__((64 * kStepWaves<T, D>), 1) void step_kernel(StepPa
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) arrived(q[ks]);
     for (int64_t t = t0 + wave; t < t1; t += NW) {
-        if (t + NW < t1) {
-            stage(t + NW, buf ^ 1);
-            __builtin_amdgcn_s_waitcnt(0x0f70 | ((2 * LOADS) & 15) | ((2 * LOADS) >> 4) << 14);  // vmcnt: this tile's loads
-        } else {
-            __builtin_amdgcn_s_waitcnt(0x0f70);
-        }
-        asm volatile("" ::: "memory");
+        const bool more = t + NW < t1;
+        if (TWO && more) stage(t + NW, buf ^ 1, true, true);
+        if (TWO && more) arrive<2 * LOADS>();  // this tile's
+        else if (TWO) arrive<0>();
+        else arrive<LOADS>();                  // this tile's keys
         const Lds tk = mine + buf * 2 * BYTES;
         const Lds rb = opaque(row_base + tk), cb = opaque(col_base + tk + BYTES);
         f32x16 s = zero16();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) mma(s, L::row_op(rb, 0, ks), q[ks]);
+        if (!TWO) have_read();
+        if (!TWO && more) stage(t + NW, 0, true, false);
         const int64_t left = seen - t * kStepKeys;
         if (left < kStepKeys) {
 #pragma unroll
@@ -150,14 +166,15 @@ __global__ __launch_bounds__((64 * kStepWaves<T, D>), 1) void step_kernel(StepPa
             l += s[i];
         }
         const Op<T> pr[2] = {op_of<T>(s, 0), op_of<T>(s, 1)};
+        if (!TWO && more) arrive<LOADS>();  // its values
+        else if (!TWO) arrive<0>();
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) mma(o[dt], L::col_op(cb, 16 * ks, dt), pr[ks]);
-        // the tile has been read before the next loads into it are given out
-        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-        asm volatile("" ::: "memory");
-        buf ^= 1;
+        have_read();  // before the next loads into the place are given out
+        if (!TWO && more) stage(t + NW, 0, false, true);
+        if (TWO) buf ^= 1;
     }
     l += other_half(l, lane);
 
@@ -203,7 +220,7 @@ __global__ __launch_bounds__((64 * kStepWaves<T, D>), 1) void step_kernel(StepPa
 // themselves when the others are done), of whole turns of the waves, and no more of them than those turns need.
 int step_splits(const AttnStepArgs& a) {
     const int64_t share = a.H / a.G, groups = a.N * a.G * ((share + 31) / 32);
-    const int waves = a.dtype_bf16 || a.d == 64 ? 4 : 2;
+    const int waves = kStepWaves;
     const int64_t seen = a.window > 0 && a.window < a.C ? a.window : a.C, turns = (seen + kStepKeys * waves - 1) / (kStepKeys * waves);
     const int64_t want = max((int64_t)1, 2 * (int64_t)a.cus / groups), each = (turns + want - 1) / want;
     return (int)((turns + each - 1) / each);
@@ -212,7 +229,7 @@ int step_splits(const AttnStepArgs& a) {
 template <typename T, int D>
 hipError_t run_step(const StepParams& p, hipStream_t stream) {
     const int64_t share = p.heads / p.groups, grid = p.n * p.groups * ((share + 31) / 32) * p.parts.splits;
-    hipLaunchKernelGGL((step_kernel<T, D>), dim3((unsigned)grid), dim3(64 * kStepWaves<T, D>), 0, stream, p);
+    hipLaunchKernelGGL((step_kernel<T, D>), dim3((unsigned)grid), dim3(64 * kStepWaves), 0, stream, p);
     if (p.parts.splits > 1) return launch_join(p.parts, p.o, nullptr, D, sizeof(T) == 2, Owned{}, stream);
     return hipGetLastError();
 }
