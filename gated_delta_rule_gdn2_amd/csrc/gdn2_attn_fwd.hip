@@ -41,9 +41,9 @@ struct FwdParams {
 };
 
 // The work of one workgroup of NW waves.  SW of them share 32 queries: each takes every SWth tile of keys, with
-// tiles of its own in LDS, and their sums are joined at the end.  FIRST: returns whether some output of a wave is not finite, and leaves that
-// wave's outputs unwritten (`flag`: in LDS, zero).  A product multiplies what a query does not see by zero, which infinities
-// and NaN survive: the other form leaves out value by value what the mask hides.
+// tiles of its own in LDS, and their sums are joined at the end.  FIRST: returns whether some output of a wave is not finite, and leaves
+// that wave's outputs unwritten (`flag`: in LDS, zero).  A product multiplies what a query does not see by zero, which
+// infinities and NaN survive: the other form leaves out value by value what the mask hides.
 template <typename T, int D, int NW, int SW, bool FIRST>
 __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* flag) {
     typedef Tile<T, D> L;
