@@ -4,7 +4,7 @@
 //   query i of lq stands at p_i = lk - lq + i of its sequence's lk keys;
 //   o_i = sum_j e^(s_ij - m) v_j / l,  l = sum_j e^(s_ij - m),  lse_i = m + log l.
 //
-// One pass over the keys with the running maximum m and sum l.  A workgroup takes 32 queries a wave
+// One pass over the keys with the running maximum m and sum l.  A workgroup of 4 or 8 waves takes 32 queries a wave
 // of one head; tiles of keys and values go from memory to LDS directly, one tile ahead of the
 // products.  A wave forms S^T = K Q^T, so that a lane holds scores of one query (its column): the
 // maximum and the sum are reductions within a lane and with the lane 32 away, and the probabilities
@@ -13,7 +13,7 @@
 // unrounded, and o is rounded on the store.
 //
 // Heads of 128 in bf16: 8 x 4096 tokens, 16 heads sharing 8, window 2048, 435 to 450 us (920 TFLOP/s of the
-// scores that are seen); 32768 tokens of one sequence 3.95 ms (1110; a product of 16384^3 reaches 1378).  The
+// scores that are seen); 32768 tokens of one sequence 3.86 ms (1140; a product of 16384^3 reaches 1378).  The
 // matrix units are busy for 56% of the cycles, at a clock that their power brings down to 1.7 GHz; two waves a
 // SIMD, 256 registers each.  Heads of 64: 12648 packed tokens of 32 heads sharing 4, 163 us (760), 1040 vector
 // instructions' issue slots (32 exponentials take four each) of 1500 cycles a wave and tile of 64 keys; three
@@ -341,12 +341,17 @@ hipError_t launch_join(const Parts& p, void* o, float* lse, int64_t d, bool bf16
 // With few workgroups and many keys a block's keys are also taken in parts, as many as fill the GPU, whose sums
 // a second launch joins: 4096 tokens of one head of 64 take 18 us in 4 parts, 23 in one.  (Sequences that
 // are packed may be shorter than the longest: their parts are, too.)
+// Many long sequences without a window take heads of 128 in bf16 256 queries a workgroup, which reads keys and
+// values half as often: 32768 tokens of 16 heads, 3948 us at 128, 3827 at 256; 2 x 4096 of 16, 150 and 134.  With
+// a window the wider block sees more tiles than its waves use (8 x 4096, window 2048: 434 and 441), and short
+// sequences fill it badly (16 x 700: 51 and 58).
 struct FwdForm {
     bool share;
     int splits;
+    bool wide;
 };
 FwdForm fwd_form(Shape p, int64_t d, bool is_bf16, int64_t cus) {
-    if (deal(&p, p.tq, 128, p.heads / p.groups) <= 0) return {false, 1};
+    if (deal(&p, p.tq, 128, p.heads / p.groups) <= 0) return {false, 1, false};
     auto workgroups = [&](int64_t rows) {
         const int64_t b = (p.tq + rows - 1) / rows;
         return (p.cu_q ? b + p.n - 1 : b * p.n) * p.heads;
@@ -354,7 +359,8 @@ FwdForm fwd_form(Shape p, int64_t d, bool is_bf16, int64_t cus) {
     const bool share = workgroups(32) <= (d == 64 ? 4 * cus : is_bf16 ? 2 * cus : cus / 4);
     const int64_t w = workgroups(share ? 32 : 128), keys = min((int64_t)p.window + (share ? 32 : 128), p.tk);
     const int64_t least = is_bf16 ? 1024 : 256;  // keys of a part: below, the second launch costs more
-    return {share, w >= cus ? 1 : (int)max((int64_t)1, min(keys / least, 2 * cus / w))};
+    const bool wide = is_bf16 && d == 128 && !p.cu_q && p.window >= p.tk && p.tq >= 2048 && workgroups(256) >= 2 * cus;
+    return {share, w >= cus ? 1 : (int)max((int64_t)1, min(keys / least, 2 * cus / w)), wide};
 }
 
 template <typename T, int D, int NW, int SW>
@@ -368,9 +374,13 @@ hipError_t run_fwd(FwdParams f, hipStream_t stream) {
     return hipGetLastError();
 }
 template <typename T, int D>
-hipError_t choose_fwd(const FwdParams& f, bool share, hipStream_t stream) {
+hipError_t choose_fwd(const FwdParams& f, const FwdForm& form, hipStream_t stream) {
     constexpr int SW = D * sizeof(T) > 256 ? 2 : 4;
-    return share ? run_fwd<T, D, SW, SW>(f, stream) : run_fwd<T, D, 4, 1>(f, stream);
+    if (form.share) return run_fwd<T, D, SW, SW>(f, stream);
+    if constexpr (sizeof(T) == 2 && D == 128) {
+        if (form.wide) return run_fwd<T, D, 8, 1>(f, stream);
+    }
+    return run_fwd<T, D, 4, 1>(f, stream);
 }
 
 }  // namespace attn
@@ -416,9 +426,8 @@ hipError_t launch_attn_fwd(const AttnArgs& a, void* workspace) {
     const attn::FwdParams f{(const char*)a.q, (const char*)a.k, (const char*)a.v, a.o, a.lse,
                             attn::parts_in(workspace, rows, a.d, workspace ? form.splits : 1), p};
     const hipStream_t s = (hipStream_t)a.stream;
-    const bool share = form.share;
-    if (a.dtype_bf16) return a.d == 64 ? attn::choose_fwd<bf16, 64>(f, share, s) : attn::choose_fwd<bf16, 128>(f, share, s);
-    return a.d == 64 ? attn::choose_fwd<float, 64>(f, share, s) : attn::choose_fwd<float, 128>(f, share, s);
+    if (a.dtype_bf16) return a.d == 64 ? attn::choose_fwd<bf16, 64>(f, form, s) : attn::choose_fwd<bf16, 128>(f, form, s);
+    return a.d == 64 ? attn::choose_fwd<float, 64>(f, form, s) : attn::choose_fwd<float, 128>(f, form, s);
 }
 
 }  // namespace gdn2

@@ -359,6 +359,24 @@ def test_gradients_keep_to_their_workspace(dtype, B, T, S, H, G, d):
         assert (buf[:256] == fill).all() and (buf[256 + need + 16:] == fill).all()
 
 
+def test_many_long_sequences():
+    """Blocks of 256 queries: one sequence 64 times, also with values that are not finite."""
+    q, k, v, _ = case(BF16, 2100, 2130, 1, 1, 128, 31)
+    dev = [times(64, x.cuda()) for x in (q, k, v)]
+    o, lse = first_of(64, *gdn2.attn_fwd(*dev))
+    check_fwd(q[0], k[0], v[0], o[0], lse[0])
+    for at, bad in ((0, NAN), (1033, INF), (2129, -INF)):
+        dirty = v.clone()
+        dirty[0, at, 0, 7] = bad
+        o2, lse2 = first_of(64, *gdn2.attn_fwd(dev[0], dev[1], times(64, dirty.cuda())))
+        assert torch.equal(lse, lse2)
+        sees = torch.from_numpy(A.sees(2100, 2130, None)[:, at])
+        assert torch.equal(o[0, :, 0, :7], o2[0, :, 0, :7]) and torch.equal(o[0, :, 0, 8:], o2[0, :, 0, 8:])
+        assert torch.equal(o[0, ~sees, 0, 7], o2[0, ~sees, 0, 7])
+        got = o2[0, sees, 0, 7].float().cpu()
+        assert torch.isnan(got).all() if bad != bad else (got == bad).all()
+
+
 def test_addresses_past_32_bits():
     """Tokens two million elements apart: the last ones lie past 2^32 bytes."""
     T, stride = 1100, 1 << 21
