@@ -75,20 +75,23 @@ __device__ __forceinline__ u32x4 rsrc_words(const void* p, uint32_t bytes) {
 }
 // 16 bytes a lane from `off` behind the resource's base to LDS, lane after lane from `to` (uniform) on.
 // In assembly because the compiler takes every read of LDS for one of what such a load writes, and
-// waits for it; the waits are tile_barrier's.  The load has no result registers, and nothing else here
-// uses m0.
+// waits for it; the waits for what arrives are tile_barrier's.  The load has no result registers.  The compiler
+// puts no wait states into assembly either: a load reads m0 one state after its write at the earliest, and its
+// resource five states after a vector instruction (the readfirstlanes of rsrc_words, a spilled register's
+// return) has written a word of it.  The write of m0 and s_nop 3 are five.
 __device__ __forceinline__ void load_to_lds(Lds to, u32x4 r, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(uniform((int)to)), "v"(off), "s"(r) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(uniform((int)to)), "v"(off), "s"(r)
+                 : "memory", "m0");
 }
 
-// 16 bytes a lane from each lane's own address
+// 16 bytes a lane from each lane's own address (no scalar operand but m0)
 __device__ __forceinline__ void load_far_to_lds(Lds to, const void* from) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform((int)to)), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform((int)to)), "v"(from) : "memory", "m0");
 }
 
 // the same, 4 bytes a lane
 __device__ __forceinline__ void load_far_words_to_lds(Lds to, const void* from) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform((int)to)), "v"(from) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform((int)to)), "v"(from) : "memory", "m0");
 }
 
 // A tile of rows of D elements in LDS, filled by loads that go there directly; it begins at a multiple
