@@ -78,7 +78,10 @@ __device__ __forceinline__ u32x4 rsrc_words(const void* p, uint32_t bytes) {
 // waits for it; the waits for what arrives are tile_barrier's.  The load has no result registers.  The compiler
 // puts no wait states into assembly either: a load reads m0 one state after its write at the earliest, and its
 // resource five states after a vector instruction (the readfirstlanes of rsrc_words, a spilled register's
-// return) has written a word of it.  The write of m0 and s_nop 3 are five.
+// return) has written a word of it.  The write of m0 and s_nop 3 are five.  (m0 is a clobber, so that the compiler
+// takes no value of its own in it for kept; that it never allocates m0 anyway is what the warning would say.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(Lds to, u32x4 r, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(uniform((int)to)), "v"(off), "s"(r)
                  : "memory", "m0");
@@ -93,6 +96,7 @@ __device__ __forceinline__ void load_far_to_lds(Lds to, const void* from) {
 __device__ __forceinline__ void load_far_words_to_lds(Lds to, const void* from) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform((int)to)), "v"(from) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // A tile of rows of D elements in LDS, filled by loads that go there directly; it begins at a multiple
 // of 1024 bytes.  Rows lie one behind the other without padding (such a load writes 64 lanes' 16-byte
