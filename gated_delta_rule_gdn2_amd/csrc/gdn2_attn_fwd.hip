@@ -26,8 +26,8 @@ namespace attn {
 // keys in a tile
 template <typename T, int SW> constexpr int kKeys = sizeof(T) == 2 && SW == 1 ? 64 : 32;
 template <typename T, int D, int SW> constexpr int kFwdLds = SW * 2 * 2 * kKeys<T, SW> * Tile<T, D>::kRow;
-// Weights are formed against a reference near the row's largest score so far.  A row's sum over a tile
-// may grow up to this (in units of the reference's weight) before the reference follows.
+// Weights are formed against a reference near the row's largest score so far.  The sum over a lane's half of a
+// row's part of a tile may grow up to this (in units of the reference's weight) before the reference follows.
 constexpr float kSlack = 4096.f;
 
 struct FwdParams {
@@ -163,10 +163,12 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
         if (first_tile) follow(true);
         float sum = weights();
         // The reference is followed only where weights outgrow it (the exponents of fp32 and bf16 have room),
-        // or where there is none yet.  Each query goes by its own weights: what a neighbour does changes no bit.
+        // or where there is none yet.  Each query goes by its own two halves, and either calls the vote: what a
+        // neighbour does changes no bit.
         auto outgrown = [&](float x) { return x > kSlack || (m == -__builtin_inff() && x == x); };
         if (__any(!first_tile && outgrown(sum))) {
-            const bool need = outgrown(sum + other_half(sum, lane));
+            const float other = other_half(sum, lane);  // by all lanes
+            const bool need = outgrown(sum) || outgrown(other);
             scores(rb);
             if (cut) hide(seen);
             follow(need);
