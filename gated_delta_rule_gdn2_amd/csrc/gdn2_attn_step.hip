@@ -49,7 +49,7 @@ template <int LEFT> __device__ __forceinline__ void arrive() {
     __builtin_amdgcn_s_waitcnt(0x0f70 | (LEFT & 15) | (LEFT >> 4) << 14);
     asm volatile("" ::: "memory");
 }
-// a wave has read what it asked LDS for
+// a wave has read what it asked LDS for, and what it wrote there can be read
 __device__ __forceinline__ void have_read() {
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
     asm volatile("" ::: "memory");
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64 * kStepWaves, 1) void step_kernel(StepParams a) 
 
     const Lds mine = lds_of(lds) + wave * (TWO ? 4 : 2) * BYTES, row_base = L::row_base(lane), col_base = L::col_base(lane);
     // Tile t's keys and values.  The newest token comes from the call: its slot is being written.  Rows
-    // behind it repeat it, so that what the mask hides there is no value that another row does not have.
+    // behind it repeat it, until their values become zeros: weights of zero would make NaN of its infinities.
     auto stage = [&](int64_t t, int buf, bool keys, bool values) {
         const Lds at = mine + buf * 2 * BYTES;
 #pragma unroll
@@ -168,6 +168,13 @@ __global__ __launch_bounds__(64 * kStepWaves, 1) void step_kernel(StepParams a) 
         const Op<T> pr[2] = {op_of<T>(s, 0), op_of<T>(s, 1)};
         if (!TWO && more) arrive<LOADS>();  // its values
         else if (!TWO) arrive<0>();
+        if (left < kStepKeys) {  // the wave's last tile, all of which is there
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                if ((i * 64 + lane) / L::kUnits >= (int)left)
+                    *(GDN2_LDS u32x4*)(uintptr_t)(tk + BYTES + (i * 64 + lane) * 16) = u32x4{0, 0, 0, 0};
+            have_read();
+        }
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll

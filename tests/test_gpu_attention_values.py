@@ -1,10 +1,11 @@
-"""GPU tests of attention at values that seldom occur: scores that outgrow a reference.  Bars as derived in test_gpu_attention."""
+"""GPU tests of attention at values that seldom occur: scores that outgrow a reference, infinities in a
+step's own token.  Bars as derived in test_gpu_attention."""
 import pytest
 import torch
 
 import gated_delta_rule_gdn2_amd as gdn2
 from tests.parity_util import say
-from tests.test_gpu_attention import BF16, F32, MANY, check_fwd, fwd
+from tests.test_gpu_attention import BF16, F32, INF, MANY, NAN, check_fwd, fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,40 @@ def test_a_neighbours_scores_change_no_bit(dtype, d, many):
     check_fwd(loud[0], k[0], v[0], o2[0], lse2[0], None, 1.0)
     others = torch.arange(T) != 401
     assert torch.equal(o[0, others], o2[0, others]) and torch.equal(lse[0, others], lse2[0, others])
+
+
+# ---- infinities in a step's own token -------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+@pytest.mark.parametrize("C,window", [(200, None), (3000, None), (200, 33)])
+def test_step_with_values_that_are_not_finite(dtype, d, bad, C, window):
+    """The newest token's value, or an older one's, in one channel: that channel alone shows it, whether the
+    tokens seen fill their tiles of 32 or not."""
+    say("case: step, %s in a value, %s d%d C%d window %s" % (bad, dtype, d, C, window))
+    H, G = 4, 2
+    places = [0, 1, 30, 31, 32, 63, 100, 159, 199, 200, 2047, 2999, 3100]
+    n = len(places)
+    g = torch.Generator("cuda").manual_seed(C + d)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    q, k, v, kc, vc = r(n, H, d), r(n, G, d), r(n, G, d), r(n, C, G, d), r(n, C, G, d)
+    at = torch.tensor(places, device="cuda")
+    clean = gdn2.attn_step(q, k, v, kc.clone(), vc.clone(), at, window=window)
+    assert torch.isfinite(clean).all()
+    dirty = v.clone()
+    dirty[:, 1, 5] = bad
+    o = gdn2.attn_step(q, k, dirty, kc.clone(), vc.clone(), at, window=window)
+    hit = torch.zeros(n, H, d, dtype=torch.bool, device="cuda")
+    hit[:, H // G:, 5] = True
+    assert torch.equal(o[~hit], clean[~hit])
+    same = torch.isnan(o[hit]) if bad != bad else o[hit] == bad
+    assert same.all(), [places[i] for i in range(n) if not same.view(n, -1)[i].all()]
+    # an older token's: the one before the newest, where there is one that is seen
+    older = vc.clone()
+    for i, p in enumerate(places):
+        older[i, (p - 1) % C, 0, 7] = bad
+    o = gdn2.attn_step(q, k, v, kc.clone(), older, at, window=window)
+    hit = torch.zeros(n, H, d, dtype=torch.bool, device="cuda")
+    hit[[i for i, p in enumerate(places) if p > 0], :H // G, 7] = True
+    assert torch.equal(o[~hit], clean[~hit])
+    assert (torch.isnan(o[hit]) if bad != bad else o[hit] == bad).all()
