@@ -308,6 +308,9 @@ template <int D, int SW> struct WaveSums {
 // zero times x, added to `sum`: a NaN once anything was not finite
 __device__ __forceinline__ float watch(float sum, float x) { return __builtin_fmaf(x, 0.f, sum); }
 
+// a value's size as a number that grows with it: that of an infinity is larger than any, that of a NaN larger still
+__device__ __forceinline__ unsigned size_bits(float x) { return __builtin_bit_cast(unsigned, x) & 0x7fffffffu; }
+
 // ---- values that are not finite -------------------------------------------------------------
 // A product over a tile's rows multiplies what a mask hides by zero, which an infinity or a NaN there
 // survives.  Kernels therefore take tiles as they are and look at what came of it; where something is not

@@ -29,6 +29,10 @@ template <typename T, int D, int SW> constexpr int kFwdLds = SW * 2 * 2 * kKeys<
 // Weights are formed against a reference near the row's largest score so far.  The sum over a lane's half of a
 // row's part of a tile may grow up to this (in units of the reference's weight) before the reference follows.
 constexpr float kSlack = 4096.f;
+// So the sums of a row over its tiles, 2^26 at most, are up to 2^39 times a mean of values, and leave fp32 for values
+// near its end.  A row that comes to kLarge (or is not finite) is formed again with all its weights scaled by kDamp,
+// a power of two that changes no bit of what stays in fp32's range; below kLarge 2^11 waves and parts can be joined.
+constexpr float kLarge = 0x1p112f, kDamp = 0x1p-40f;
 
 struct FwdParams {
     const char* q;
@@ -41,11 +45,13 @@ struct FwdParams {
 };
 
 // The work of one workgroup of NW waves.  SW of them share 32 queries: each takes every SWth tile of keys, with
-// tiles of its own in LDS, and their sums are joined at the end.  FIRST: returns whether some output of a wave is not finite, and leaves
-// that wave's outputs unwritten (`flag`: in LDS, zero).  A product multiplies what a query does not see by zero, which
-// infinities and NaN survive: the other form leaves out value by value what the mask hides.
-template <typename T, int D, int NW, int SW, bool FIRST>
-__device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* flag) {
+// tiles of its own in LDS, and their sums are joined at the end.  Returns whether some output of a wave is not finite or
+// large, and leaves that wave's outputs unwritten (`flag`: in LDS, zero).  A product multiplies what a query does not
+// see by zero, which infinities and NaN survive: the form that is not FIRST leaves out value by value what the mask
+// hides.  It keeps in `large` (in LDS, zero) whose outputs are not finite or large, of each wave's 32 queries; `damped`,
+// it scales their weights, and writes all outputs as they are.
+template <typename T, int D, int NW, int SW, bool FIRST, typename Word>
+__device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, Word* flag, Word* large, bool damped) {
     typedef Tile<T, D> L;
     static_assert(SW == 1 || SW == NW, "each wave its own queries, or all the same");
     constexpr int BK = kKeys<T, SW>, KS = D / 16, DT = D / 32, BM = NW / SW * 32, BYTES = BK * L::kRow;
@@ -104,6 +110,7 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) o[dt] = zero16();
     float m = -__builtin_inff(), l = 0.f;  // the reference (base 2) and the lane's part of the sum
+    const bool damp = !FIRST && damped && (large[wave] >> (lane & 31) & 1);
 
     f32x16 s[BK / 32];
     auto scores = [&](Lds rb) {
@@ -175,6 +182,13 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
             sum = weights();
         }
         first_tile = false;
+        if (!FIRST) {
+            sum *= damp ? kDamp : 1.f;
+#pragma unroll
+            for (int h = 0; h < BK / 32; ++h)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[h][i] *= damp ? kDamp : 1.f;
+        }
         l += sum;
         Op<T> pr[BK / 16];
 #pragma unroll
@@ -196,14 +210,17 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
             for (int dt = 0; dt < DT; ++dt) mma(o[dt], L::col_op(cb, 16 * ks, dt), pr[ks]);
     }
     bool any = false;
-    if (FIRST) {
-        float sum = 0.f;
+    if (FIRST || !damped) {
+        unsigned top = 0;  // the largest size, as its bits: infinities and NaN are larger
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum = watch(sum, o[dt][i]);
-        const bool again = __any(sum != 0.f);
+            for (int i = 0; i < 16; ++i) top = max(top, size_bits(o[dt][i]));
+        const uint64_t whose = __ballot(top >= size_bits(kLarge));
+        const bool again = whose != 0;
         if (again) *flag = 1;
+        if (!FIRST && again && lane == 0)
+            __hip_atomic_fetch_or(large + wave, (unsigned)whose | (unsigned)(whose >> 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         lds_barrier();
         any = *flag != 0;
         if (SW == 1 ? again : any) return any;
@@ -215,6 +232,8 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
     const int64_t row0 = (w.s.q0 + mine) * p.heads + head, row = row0 + (int64_t)(lane & 31) * p.heads;
     const bool live = (lane & 31) < rows;
     const int64_t at = (int64_t)blockIdx.y * a.parts.rows + row;
+    auto log_sum = [&] { return l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(damp ? l / kDamp : l)) * kLn2; };
+    auto part_sum = [&] { return float2{m, damp ? -l : l}; };  // the sign says that the part's weights are scaled
     if constexpr (SW > 1) {
         typedef WaveSums<D, SW> Sums;
         static_assert(Sums::kBytes <= kFwdLds<T, D, SW> && SW * 256 <= kFwdLds<T, D, SW>, "room for the sums");
@@ -238,38 +257,46 @@ __device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, int* fla
         if (!live) return any;
         if (gridDim.y > 1) {
             sums.template store<float>(a.parts.o + at * D, 1.f, part, g);
-            if (g == 0 && part == 0) a.parts.ml[at] = float2{m, l};
+            if (g == 0 && part == 0) a.parts.ml[at] = part_sum();
             return any;
         }
         sums.template store<T>((T*)a.o + row * D, l == 0.f ? 0.f : 1.f / l, part, g);
-        if (a.lse && g == 0 && part == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        if (a.lse && g == 0 && part == 0) a.lse[row] = log_sum();
         return any;
     }
     if (gridDim.y > 1) {
         if (live) {
             store_column<float, D>(a.parts.o + at * D, o, 1.f, g);
-            if (g == 0) a.parts.ml[at] = float2{m, l};
+            if (g == 0) a.parts.ml[at] = part_sum();
         }
         return any;
     }
-    if (a.lse && live && g == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && live && g == 0) a.lse[row] = log_sum();
     store_rows<T, D>(base + wave * 32 * L::kRow, (char*)a.o + row0 * L::kRow, (int64_t)p.heads * L::kRow, rows, o, l == 0.f ? 0.f : 1.f / l, lane);
     return any;
 }
-// a call of its own, so that the kernel keeps its registers to the first form
+// a call of its own, so that the kernel keeps its registers to the first form; `outcome`: a flag, and `large`
 template <typename T, int D, int NW, int SW>
-__device__ __attribute__((noinline)) void fwd_again(FwdParams a, Lds base) {
-    fwd_block<T, D, NW, SW, false>(a, base, nullptr);
+__device__ __attribute__((noinline)) void fwd_again(FwdParams a, Lds base, GDN2_LDS unsigned* outcome) {
+    if (threadIdx.x < NW / SW) outcome[1 + threadIdx.x] = 0;
+#pragma unroll 1
+    for (int damped = 0; damped < 2; ++damped) {
+        if (threadIdx.x == 0) *outcome = 0;
+        __syncthreads();
+        if (!fwd_block<T, D, NW, SW, false>(a, base, outcome, outcome + 1, damped != 0)) break;
+        __syncthreads();
+    }
 }
 
 template <typename T, int D, int NW, int SW>
 __global__ __launch_bounds__(NW * 64, SW > 1 ? (kFwdLds<T, D, SW> > 80000 ? 1 : 2) : D == 64 ? 3 : 2) void fwd_kernel(FwdParams a) {
     __shared__ __attribute__((aligned(1024))) char lds[kFwdLds<T, D, SW>];
-    __shared__ int any_again;
+    __shared__ unsigned any_again;  // of its own: no call gets its address, or the offsets would be no scalar loads
+    __shared__ unsigned outcome[1 + NW / SW];
     if (threadIdx.x == 0) any_again = 0;
-    if (fwd_block<T, D, NW, SW, true>(a, lds_of(lds), &any_again)) {
+    if (fwd_block<T, D, NW, SW, true>(a, lds_of(lds), &any_again, (unsigned*)nullptr, false)) {
         __syncthreads();
-        fwd_again<T, D, NW, SW>(a, lds_of(lds));
+        fwd_again<T, D, NW, SW>(a, lds_of(lds), (GDN2_LDS unsigned*)outcome);
     }
 }
 
@@ -295,9 +322,15 @@ __global__ __launch_bounds__(256) void join_kernel(Parts p, T* __restrict__ o, f
         if (!found) return;
     }
     float m = -__builtin_inff();
-    for (int i = lane; i < p.splits; i += 64) m = fmaxf(m, p.ml[i * p.rows + row].x);
+    bool damped = false;  // some part's weights are scaled: the other parts' are, too
+    for (int i = lane; i < p.splits; i += 64) {
+        const float2 ml = p.ml[i * p.rows + row];
+        m = fmaxf(m, ml.x);
+        damped = damped || ml.y < 0.f;
+    }
 #pragma unroll
     for (int s = 32; s >= 1; s /= 2) m = fmaxf(m, __shfl_xor(m, s));
+    damped = __any(damped);
     f32x4 x{0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
 #pragma unroll 4
@@ -305,10 +338,11 @@ __global__ __launch_bounds__(256) void join_kernel(Parts p, T* __restrict__ o, f
         const float2 ml = p.ml[i * p.rows + row];
         const f32x4 v = *reinterpret_cast<const f32x4*>(p.o + (i * p.rows + row) * D + 4 * c);
         // a part that saw nothing is all zeros
-        const float f = ml.x == -__builtin_inff() && ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
+        const float f = (ml.x == -__builtin_inff() && ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - m)) *
+                        (damped && !(ml.y < 0.f) ? kDamp : 1.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += f * v[e];
-        l += f * ml.y;
+        l += f * fabsf(ml.y);
     }
     sum[sub][c] = x;
     if (c == 0) total[sub] = l;
@@ -322,7 +356,7 @@ __global__ __launch_bounds__(256) void join_kernel(Parts p, T* __restrict__ o, f
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float out[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
         store_vec_any<T, 4>(o + row * D + 4 * c, out);
-        if (lse && c == 0) lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        if (lse && c == 0) lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(damped ? l / kDamp : l)) * kLn2;
     }
 }
 

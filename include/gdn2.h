@@ -549,6 +549,9 @@ gdn2_status_t gdn2_layer_norm_bwd(const void* dy, const void* x, const float* ga
  * greater than S too: a query that sees no key (or none with a score above
  * minus infinity) has o = 0 and lse = -infinity.
  * A NaN or an infinity in k or v reaches no query that does not see it.
+ * Finite values below 2^127 in size give a finite o where the scores are finite.  (A
+ * query that sees values above 2^73 may take those below 2^-60 in its other channels
+ * for zero.)
  * scale > 0.  H is a multiple of G; strides are at least a token's elements,
  * below 2^22 and whole 16-byte units; H * d is below 2^22, T and S at most
  * 2^31 - 1025, B * T below 2^29, and B * G * ceil(T / 128) * (H / G) and
@@ -638,6 +641,7 @@ size_t gdn2_attn_bwd_varlen_workspace_bytes(int64_t N, int64_t total_T, int64_t 
  * The token sees the last min(p + 1, C) tokens, itself among them, with a
  * window > 0 at most `window` of them.  A position below 0 is no token: its output is zero and its
  * cache is left as it was.  Slots behind a sequence's last token are not read.
+ * Finite values below 2^127 over the number of tokens seen give a finite o.
  * Strides below 2^31, N * G * ceil(H / G / 32) below 2^23; otherwise as for
  * gdn2_attn_fwd.  With a workspace of gdn2_attn_step_workspace_bytes bytes (16-byte
  * aligned) a sequence's tokens are taken in parts; NULL and 0: whole.

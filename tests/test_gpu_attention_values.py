@@ -1,11 +1,13 @@
 """GPU tests of attention at values that seldom occur: scores that outgrow a reference, infinities in a
-step's own token.  Bars as derived in test_gpu_attention."""
+step's own token, values near fp32's end.  Bars as derived in test_gpu_attention."""
+import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_gdn2_amd as gdn2
+from oracle import attention as A
 from tests.parity_util import say
-from tests.test_gpu_attention import BF16, F32, INF, MANY, NAN, check_fwd, fwd
+from tests.test_gpu_attention import BF16, F32, INF, MANY, NAN, U, check_fwd, f64, fwd, half_step, pieces, within
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +81,53 @@ def test_step_with_values_that_are_not_finite(dtype, d, bad, C, window):
     hit[[i for i, p in enumerate(places) if p > 0], :H // G, 7] = True
     assert torch.equal(o[~hit], clean[~hit])
     assert (torch.isnan(o[hit]) if bad != bad else o[hit] == bad).all()
+
+
+# ---- values near the end of fp32 ------------------------------------------------------------
+
+def check(q, k, v, o, lse):
+    """check_fwd but for the channel of tiny values, which rows of large ones may lose."""
+    keep = [c for c in range(v.shape[-1]) if c != 5]
+    ro, rl = A.attention(q, k, v)
+    s, seen, off, top = pieces(q, k, None, None)
+    p = np.where(seen, np.exp(np.where(seen, s, 0.0) - rl.T[..., None]), 0.0)
+    n, r = seen.sum(-1, keepdims=True) + 8, half_step(q.dtype)
+    va = np.abs(np.repeat(f64(v), q.shape[1] // k.shape[1], 1))
+    spread = (p * (off + n * U)).sum(-1)
+    tol = np.einsum("hts,shd->thd", p * (off + r + n * U), va) + np.abs(ro) * spread.T[..., None] + r * np.abs(ro)
+    within("o", o[..., keep], ro[..., keep], tol[..., keep])
+    within("lse", lse, rl, spread.T + 8 * U * (1 + np.abs(rl) + top[..., 0].T))
+
+
+BIG = [  # T, S, H, G, d
+    (300, 300, 2, 1, 64), (300, 300, 2, 1, 128), (6, 3001, 4, 2, 64), (40, 5000, 1, 1, 128), (2100, 2130, 1, 1, 128)]
+
+
+@MANY
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,S,H,G,d", BIG)
+def test_finite_values_give_finite_outputs(dtype, T, S, H, G, d, many):
+    """Values up to 2^126 behind scores that grow along the keys, so that the reference stays behind: outputs
+    are means of values and stay below the largest.  Other channels keep their bits, and queries that see none of
+    the large values keep them in all, those of tiny values too."""
+    if many and S > 3001:
+        pytest.skip("the same form as the fewer")
+    say("case: large values %s T%d S%d d%d" % (dtype, T, S, d))
+    g = torch.Generator("cpu").manual_seed(S + d)
+    q, k, v = (torch.randn(1, n, h, d, generator=g) for n, h in ((T, H), (S, G), (S, G)))
+    q[..., 0], k[..., 0] = 1.0, torch.linspace(0, 40, S)[None, :, None]  # a weight grows by up to e^5 in all
+    v[..., 5] *= 2.0 ** -100
+    q, k, v = (x.to(dtype) for x in (q, k, v))
+    o, lse = fwd(many, q.cuda(), k.cuda(), v.cuda())
+    rest = [c for c in range(d) if c not in (3, 4, 5)]
+    for size, first in ((2.0 ** 105, 0), (2.0 ** 126, 0), (2.0 ** 126, S - 3 * T // 4)):
+        big = v.float().clone()
+        big[:, first:, :, 3] = size * torch.rand(1, S - first, G, generator=g)
+        big[:, first:, :, 4] = size
+        big = big.to(dtype)
+        o2, lse2 = fwd(many, q.cuda(), k.cuda(), big.cuda())
+        check(q[0], k[0], big[0], o2[0], lse2[0])
+        assert torch.equal(lse, lse2)
+        assert torch.equal(o[..., rest], o2[..., rest])
+        blind = max(0, first - (S - T))
+        assert torch.equal(o[:, :blind], o2[:, :blind])
