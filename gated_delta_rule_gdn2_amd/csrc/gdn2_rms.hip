@@ -46,11 +46,11 @@ __device__ __forceinline__ void store_row_e4m3(uint8_t* p, int lane, int width, 
     }
 }
 
-// T: x (and y, unless E4M3); R: the residual and the sum.  Both are walked in vectors of T's 16 bytes.
+// T: x (and y, unless E4M3); R: the residual and the sum, which may be one tensor.  Both are walked in vectors of T's 16 bytes.
 template <typename T, typename R, bool E4M3, int LANES, int NV>
-__global__ __launch_bounds__(kThreads<LANES>) void rms_kernel(const T* __restrict__ x, const R* __restrict__ residual,
+__global__ __launch_bounds__(kThreads<LANES>) void rms_kernel(const T* __restrict__ x, const R* residual,
                                                               const float* __restrict__ gamma, void* __restrict__ y,
-                                                              float* __restrict__ scale, R* __restrict__ h,
+                                                              float* __restrict__ scale, R* h,
                                                               float* __restrict__ rstd, int64_t rows, int width, float eps) {
     typedef Row<T, LANES, NV> RT;
     constexpr int V = RT::V, E = NV * V, RPB = kThreads<LANES> / LANES;
@@ -102,12 +102,12 @@ __global__ __launch_bounds__(kThreads<LANES>) void rms_kernel(const T* __restric
     }
 }
 
-// One pass over dy, h and dh: dx, and the workgroup's part of the sum over rows.
+// One pass over dy, h and dh: dx (which may be dh), and the workgroup's part of the sum over rows.
 template <typename T, typename R, int LANES, int NV>
 __global__ __launch_bounds__(kThreads<LANES>) void rms_bwd_kernel(const T* __restrict__ dy, const R* __restrict__ h,
                                                                   const float* __restrict__ gamma,
-                                                                  const float* __restrict__ rstd, const R* __restrict__ dh,
-                                                                  R* __restrict__ dx, float* __restrict__ parts,
+                                                                  const float* __restrict__ rstd, const R* dh,
+                                                                  R* dx, float* __restrict__ parts,
                                                                   float* __restrict__ dgamma, int64_t rows, int width) {
     typedef Row<T, LANES, NV> RT;
     constexpr int V = RT::V, E = NV * V, RPB = kThreads<LANES> / LANES;
