@@ -454,7 +454,7 @@ struct Work {
 __device__ __forceinline__ bool find_work(const Shape& p, int rows, int per_group, bool last_first, bool keys, int lane, Work* w) {
     const unsigned x = blockIdx.x & 7, r = blockIdx.x >> 3;
     const unsigned per = (p.blocks + (1u << p.slice_bits) - 1) >> p.slice_bits, each = per * per_group;
-    const unsigned slices = (p.all_groups << p.slice_bits) >> 3, before = r / (each * p.turn) * p.turn;  // of an XCD
+    const unsigned slices = ((p.all_groups << p.slice_bits) + 7) >> 3, before = r / (each * p.turn) * p.turn;  // of an XCD
     const unsigned width = min(slices - before, p.turn), rest = r % (each * p.turn) / (unsigned)per_group;
     const unsigned slice = (before + rest % width) * 8 + x, group = slice >> p.slice_bits, nth = rest / width;
     // A group's slices go round with its number: with fewer blocks than slices the last ones are empty, and would
@@ -481,21 +481,28 @@ __device__ __forceinline__ Work uniform(const Work& w) {
     return Work{Seq{uniform(w.s.q0), uniform(w.s.k0), uniform(w.s.lq), uniform(w.s.lk)}, uniform(w.block), uniform(w.head)};
 }
 constexpr int64_t kTurn = 256;
-constexpr int64_t kMaxGrid = (int64_t)1 << 23;  // workgroups of up to 512 threads: a launch has less than 2^32
-// fills in how work is dealt out; workgroups of the launch (0: none), or -1 if they are too many
+constexpr int64_t kMaxWork = (int64_t)1 << 23;  // blocks of all heads
+constexpr int64_t kMaxGrid = (int64_t)1 << 24;  // workgroups of 256 threads: a launch has less than 2^32
+// Fills in how work is dealt out; workgroups of the launch (0: none), or -1 if there is too much work.  Slices, and the
+// groups of the last round over the XCDs, that have no blocks make the launch larger than the work.  So many groups
+// of few blocks are cut into no more slices than they have blocks (1025 sequences of 60 tokens, 4 heads of 64 sharing
+// one: 53 us with 8 slices, 30 with one, the gradients 135 and 72), and slices are fewer where the launch would not fit.  Then it does: 8 blocks or more are less
+// than doubled by any slices, and 2^20 heads of fewer are 16 groups or more, which are less than doubled by none.
 inline int64_t deal(Shape* p, int64_t tokens, int rows, int per_group) {
     const int64_t blocks = p->cu_q ? tokens / rows + p->n : (tokens + rows - 1) / rows;
     const int64_t groups = p->cu_q ? p->groups : p->n * p->groups;
-    if (blocks >= kMaxGrid || groups >= kMaxGrid) return -1;
+    if (blocks == 0) return 0;
+    if (blocks >= kMaxWork || groups >= kMaxWork || blocks * groups >= kMaxWork || blocks * groups * per_group >= kMaxWork) return -1;
     p->blocks = (int)blocks;
     p->all_groups = (unsigned)groups;
+    auto per = [&] { return (blocks + ((int64_t)1 << p->slice_bits) - 1) >> p->slice_bits; };
+    auto slices = [&] { return ((groups << p->slice_bits) + 7) / 8; };  // of an XCD
+    auto grid = [&] { return slices() * 8 * per() * per_group; };
     p->slice_bits = 0;
-    while ((groups << p->slice_bits) % 8) ++p->slice_bits;
-    const int64_t per = (blocks + ((int64_t)1 << p->slice_bits) - 1) >> p->slice_bits;
-    const int64_t grid = (groups << p->slice_bits) * per, slices = (groups << p->slice_bits) / 8;
-    if (grid >= kMaxGrid) return -1;
-    p->turn = (unsigned)(grid > 0 ? min(slices, (kTurn + per * per_group - 1) / (per * per_group)) : 1);
-    return grid * per_group < kMaxGrid ? grid * per_group : -1;
+    while ((groups << p->slice_bits) % 8 && (groups < 64 || (2 << p->slice_bits) <= blocks)) ++p->slice_bits;
+    while (p->slice_bits > 0 && grid() >= kMaxGrid) --p->slice_bits;
+    p->turn = (unsigned)min(slices(), (kTurn + per() * per_group - 1) / (per() * per_group));
+    return grid() < kMaxGrid ? grid() : -1;
 }
 
 // Rows whose keys were taken in parts: unnormalised sums o [splits][rows][d] in fp32, and of each row

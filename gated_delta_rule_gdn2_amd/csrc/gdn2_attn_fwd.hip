@@ -395,7 +395,8 @@ FwdForm fwd_form(Shape p, int64_t d, bool is_bf16, int64_t cus) {
     const bool share = workgroups(32) <= (d == 64 ? 4 * cus : is_bf16 ? 2 * cus : cus / 4);
     const int64_t w = workgroups(share ? 32 : 128), keys = min((int64_t)p.window + (share ? 32 : 128), p.tk);
     const int64_t least = is_bf16 ? 1024 : 256;  // keys of a part: below, the second launch costs more
-    const bool wide = is_bf16 && d == 128 && !p.cu_q && p.window >= p.tk && p.tq >= 2048 && workgroups(256) >= 2 * cus;
+    bool wide = is_bf16 && d == 128 && !p.cu_q && p.window >= p.tk && p.tq >= 2048 && workgroups(256) >= 2 * cus;
+    if (wide) wide = deal(&p, p.tq, 256, p.heads / p.groups) < kMaxGrid / 2;  // of 512 threads
     return {share, w >= cus ? 1 : (int)max((int64_t)1, min(keys / least, 2 * cus / w)), wide};
 }
 

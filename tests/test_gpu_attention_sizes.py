@@ -1,0 +1,51 @@
+"""GPU tests of attention at counts of sequences and heads that do not divide into the XCDs."""
+import pytest
+import torch
+
+import gated_delta_rule_gdn2_amd as gdn2
+from tests.parity_util import say
+from tests.test_gpu_attention import BF16, F32, case, check_bwd, check_fwd, first_of, times
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    gdn2._load()
+
+
+@pytest.mark.parametrize("dtype,B,T,H,G,d", [
+    (BF16, 67, 130, 3, 1, 64), (BF16, 65, 300, 3, 3, 128), (BF16, 1025, 5, 1, 1, 64), (BF16, 333, 129, 6, 2, 128), (BF16, 21, 1100, 5, 5, 64),
+    (F32, 67, 130, 3, 1, 64), (F32, 129, 70, 3, 3, 128), (BF16, 9, 351, 16, 1, 128)])
+def test_counts_that_do_not_divide(dtype, B, T, H, G, d):
+    """One sequence B times: every copy has the same bits, and the first is right."""
+    say("case: copies %s B%d T%d H%d G%d d%d" % (dtype, B, T, H, G, d))
+    q, k, v, g = case(dtype, T, T, H, G, d, B + T)
+    dev = [times(B, x.cuda()) for x in (q, k, v)]
+    o, lse = gdn2.attn_fwd(*dev)
+    grads = gdn2.attn_bwd(times(B, g.cuda()), *dev, o, lse)
+    firsts = first_of(B, o, lse, *grads.values())
+    check_fwd(q[0], k[0], v[0], firsts[0][0], firsts[1][0])
+    check_bwd(g[0], q[0], k[0], v[0], firsts[0][0], firsts[1][0], dict(zip(grads, (x[0] for x in firsts[2:]))))
+
+
+def test_a_million_sequences_of_one_token():
+    """Each query sees its own key alone: o is its value, dv the sum over the heads' d_o, which three roundings
+    of a weight of one do not change in bf16."""
+    B, H, d = (1 << 20) + 1, 2, 64
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    g = torch.Generator("cuda").manual_seed(2)
+    q, k, v, d_o = (torch.randn(B, 1, h, d, generator=g, device="cuda", dtype=torch.float32).to(BF16) for h in (H, 1, 1, H))
+    o, lse = gdn2.attn_fwd(q, k, v)
+    assert torch.equal(o, v.expand_as(o))
+    scores = (q.float() * k.float()).sum(-1) / 8
+    assert ((lse - scores).abs() <= 1e-5 * (1 + scores.abs())).all()  # 64 products' roundings and the logarithm's
+    grads = gdn2.attn_bwd(d_o, q, k, v, o, lse)
+    want = (d_o[:, :, :1].float() + d_o[:, :, 1:].float()).to(BF16)
+    assert torch.equal(grads["dv"], want)
+    cu = torch.arange(257, dtype=torch.int64, device="cuda")
+    part, _ = gdn2.attn_fwd_varlen(q[:256, 0], k[:256, 0], v[:256, 0], cu)
+    assert torch.equal(part, o[:256, 0])
