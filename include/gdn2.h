@@ -670,12 +670,15 @@ size_t gdn2_attn_step_workspace_bytes(int64_t N, int64_t H, int64_t G, int64_t d
  *   freq       [rot / 2]       float32  radians a position
  *   positions  [tokens]        int64    or NULL: token n is at n mod T
  *
- * Angles are formed in 64 bits, so far positions are exact.  q_out may be q and
+ * Angles are formed and reduced in 64 bits: off by 2^-51 of themselves, which stays
+ * below fp32's own 2^-24 of a turn for angles up to 2^29 radians.  q_out may be q and
  * k_out k, with the same strides (in place; the channels from rot on are then not
  * touched); outputs may be parts of one wider tensor, but share no byte with
  * anything else.  rot is even, from 2 to d; d from 2 to 512; (H + G) d below 2^22;
  * strides at least a token's elements and below 2^31; tensors need the alignment
- * of their elements only.  scale > 0.
+ * of their elements only.  scale > 0.  A launch has less than 2^32 threads: up to
+ * 2^25 - 8 tokens are always taken, up to 2^27 - 8 where (H + G) d <= 192, and where
+ * more would not fit they are refused (GDN2_ERR_SHAPE).
  */
 gdn2_status_t gdn2_rotary(const void* q, const void* k, const float* freq, const int64_t* positions,
                           void* q_out, void* k_out, int64_t tokens, int64_t T, int64_t H, int64_t G,

@@ -1,10 +1,12 @@
 """Which sizes attention takes, on both sides of its documented bounds, without a GPU: the gradients' workspace
 is more than zero bytes for sizes that are taken, and calls that are not are refused before any launch."""
+import ctypes
+
 import pytest
 
 import gated_delta_rule_gdn2_amd as gdn2
 from tests.test_abi_cpu import ERR_SHAPE, Fake
-from tests.test_attention_cpu import bwd, bwd_packed, fwd, fwd_packed, lib  # noqa: F401  (lib is a fixture)
+from tests.test_attention_cpu import bwd, bwd_packed, fwd, fwd_packed, lib, rot  # noqa: F401  (lib is a fixture)
 
 LIMIT = 1 << 23  # blocks of 128 tokens of all heads
 
@@ -41,3 +43,12 @@ def test_sizes_behind_the_bounds_are_refused(lib):
     for kw in (dict(N=LIMIT), dict(N=LIMIT // 2, H=2), dict(N=LIMIT - 1, T=128)):
         assert fwd_packed(lib, f, **{"H": 1, **kw}) == ERR_SHAPE, kw
     assert bwd_packed(lib, f, N=LIMIT // 2) == ERR_SHAPE
+
+
+def test_more_tokens_than_rotary_takes_are_refused(lib):
+    f = Fake()
+    far = dict(q=ctypes.c_void_p(1 << 45), qo=ctypes.c_void_p(1 << 46))  # never read
+    one = dict(far, H=1, G=0, d=2, n=2, qs=2, ks=0, qos=2, kos=0, k=None, ko=None, pos=None)
+    for kw in (dict(one, tokens=1 << 27), dict(one, tokens=(1 << 31) - 1025), dict(one, tokens=1 << 27, d=192, qs=192, qos=192),
+               dict(one, tokens=1 << 25, H=1024, d=64, qs=65536, qos=65536)):
+        assert rot(lib, f, **kw) == ERR_SHAPE, kw

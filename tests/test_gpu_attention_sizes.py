@@ -3,8 +3,9 @@ import pytest
 import torch
 
 import gated_delta_rule_gdn2_amd as gdn2
+from oracle import attention as A
 from tests.parity_util import say
-from tests.test_gpu_attention import BF16, F32, case, check_bwd, check_fwd, first_of, times
+from tests.test_gpu_attention import BF16, F32, U, case, check_bwd, check_fwd, f64, first_of, rotary_bar, times, within
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +50,21 @@ def test_a_million_sequences_of_one_token():
     cu = torch.arange(257, dtype=torch.int64, device="cuda")
     part, _ = gdn2.attn_fwd_varlen(q[:256, 0], k[:256, 0], v[:256, 0], cu)
     assert torch.equal(part, o[:256, 0])
+
+
+@pytest.mark.parametrize("tokens,H,d", [((1 << 27) - 8, 1, 2), ((1 << 25) - 8, 7, 32)])
+def test_rotary_of_the_most_tokens(tokens, H, d):
+    """The first and the last tokens: angles of 2^27 radians are off by 2^-51 of themselves, 2^-24."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB")
+    g = torch.Generator("cuda").manual_seed(3)
+    q = torch.empty(tokens, H, d, device="cuda")
+    for at in (slice(0, 500), slice(tokens - 500, tokens)):
+        q[at] = torch.randn(500, H, d, generator=g, device="cuda")
+    freq = gdn2.rotary_frequencies(2)
+    out, _ = gdn2.rotary(q, None, freq.cuda())
+    for at in (slice(0, 500), slice(tokens - 500, tokens)):
+        x = q[at].cpu()
+        ref = A.rotary(x, freq, range(tokens)[at])
+        pair = abs(f64(x))[..., :2].sum(-1, keepdims=True)
+        within("q", out[at], ref, rotary_bar(x, freq, False) + U * pair)
