@@ -235,9 +235,11 @@ def attn_step(q, k, v, k_cache, v_cache, positions, *, window=None, scale=None, 
 def rotary_frequencies(rot, base=10000.0, *, factor=1.0, length=None, low=1.0, high=32.0, device=None):
     """The table that rotary takes: fp32 [rot / 2], base^(-2 i / rot) radians a position, formed in 64
     bits.  For contexts ``factor`` times as long as those a model has learned: without ``length`` every
-    frequency is divided by ``factor``; with ``length``, the context learned, only those that make fewer
-    than ``low`` turns in it, those of more than ``high`` turns stay, and between them the share that is
-    divided falls linearly."""
+    frequency is divided by ``factor`` (position interpolation); with ``length``, the context learned, only
+    those that make fewer than ``low`` turns in it, those of more than ``high`` turns stay, and between them
+    the share that is divided falls linearly with the turns: interpolation by parts as in Peng et al., "YaRN:
+    Efficient Context Window Extension of Large Language Models" (arXiv:2309.00071, section 3.2), whose alpha
+    and beta are the defaults of ``low`` and ``high``."""
     if rot < 2 or rot % 2:
         raise ValueError("rot must be even and at least 2")
     if not factor > 0 or (length is not None and not (length > 0 and high > low)):
@@ -332,7 +334,7 @@ def rms_norm(x, gamma, eps=1e-6, *, residual=None, y=None, h=None, stats=True):
 
 def rms_norm_fp8(x, gamma, eps=1e-6, *, residual=None, y=None, scales=None, h=None, stats=True):
     """rms_norm with its output in 8 bits (float8_e4m3fn) and a scale for each row: y * scales[..., None]
-    stands for the norm's output, scales being the row's largest value / 448.  Returns (y, scales, h, rstd)."""
+    stands for the norm's output, scales being the row's largest size / 448.  Returns (y, scales, h, rstd)."""
     code, dev, width, px, pg = _norm_in("rms_norm_fp8", x, gamma)
     pr, rcode, h = _residual(x, residual, h, dev)
     y = _out("y", y, x.shape, torch.float8_e4m3fn, dev)

@@ -11,9 +11,10 @@
 // dq for each block of keys would move more bytes than that takes).  Sums are fp32; with bf16 inputs P and dS
 // are rounded to bf16 once, as the matrix unit's operands, and gradients on the store.
 //
-// At 8 x 4096 tokens, 16 heads of 128 sharing 8, window 2048, bf16: dq 590 to 630 us, dk and dv 740 to 770,
-// matrix units busy for 52% and 56% of the cycles at 1.66 GHz (1040 TFLOP/s of the 7 products).  Heads of 64 are
-// bound by vector issue, three waves a SIMD (8 x 4096 tokens of 16 heads: 1000 us in all).
+// At 8 x 4096 tokens, 16 heads of 128 sharing 8, window 2048, bf16: dq 590 to 640 us, dk and dv 740 to 820,
+// matrix units busy for 50 to 56% of the cycles at 1.5 to 1.8 GHz (980 to 1050 TFLOP/s of the 7 products).  Heads of
+// 64 are bound by vector issue, three waves a SIMD (8 x 4096 tokens of 16 heads: 1000 us in all).  fp32: 2 x 4096
+// tokens, 16 heads of 128 sharing 4, 5.0 ms (96 TFLOP/s of the 7 products), of 64 2.16 ms (111).
 //
 // A product multiplies what a query does not see by zero, which infinities and NaN survive.  A wave that meets
 // a value that is not finite in a tile that the mask cuts gives up, and its workgroup starts again in a form

@@ -12,12 +12,15 @@
 // inputs a probability is rounded to bf16 once (the matrix unit's operand), the sum l takes it
 // unrounded, and o is rounded on the store.
 //
-// Heads of 128 in bf16: 8 x 4096 tokens, 16 heads sharing 8, window 2048, 435 to 450 us (920 TFLOP/s of the
-// scores that are seen); 32768 tokens of one sequence 3.86 ms (1140; a product of 16384^3 reaches 1378).  The
-// matrix units are busy for 56% of the cycles, at a clock that their power brings down to 1.7 GHz; two waves a
-// SIMD, 256 registers each.  Heads of 64: 12648 packed tokens of 32 heads sharing 4, 163 us (760), 1040 vector
-// instructions' issue slots (32 exponentials take four each) of 1500 cycles a wave and tile of 64 keys; three
-// waves a SIMD (two took 184 us, four spill: 171).
+// Heads of 128 in bf16, on several cards of one kind: 32768 tokens of one sequence, 16 heads sharing 2, 3.76 to 3.97
+// ms (1110 to 1170 TFLOP/s; a product of 16384^3 reaches 1350 to 1380): the matrix units are busy for 52 to 56% of
+// the cycles, at a clock that their power brings down to 1.7 to 1.9 GHz.  8 x 4096 tokens, 16 heads sharing 8,
+// window 2048, 439 to 470 us (880 to 940 of the scores that are seen): loops of 33 tiles, for which the matrix units
+// are busy for 44 to 46% at 1.8 to 1.9 GHz, keys and values are read four times over (1040 MB, 2.3 TB/s) and a
+// quarter of the waves' cycles wait.  Two waves a SIMD, 256 registers each.  Heads of 64: 12648 packed tokens of 32
+// heads sharing 4, 164 to 171 us (725 to 760), 1040 vector instructions' issue slots (32 exponentials take four each)
+// of 1500 cycles a wave and tile of 64 keys; three waves a SIMD (two took 184 us, four spill: 171).  fp32: 2 x 4096
+// tokens, 16 heads of 128 sharing 4, 1037 us (133 TFLOP/s; a product of 8192^3 reaches 153); of 64, 587 us (117).
 #include "gdn2_attn.h"
 
 namespace gdn2 {

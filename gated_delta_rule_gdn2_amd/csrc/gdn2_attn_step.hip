@@ -12,9 +12,9 @@
 // so no barrier stops the loads.  Every wave keeps a maximum, a sum and an output of its own; they are
 // joined at the end, and parts of a sequence in a second launch.
 //
-// 256 sequences over 2048 tokens, 16 heads of 128 sharing 2, bf16: 78 us, 5.0 TB/s (a copy of 2 GiB: 4.9).  3
-// sequences over 16384: 16 us and 4 for the join, of which 10 are the bytes at that rate; 128 workgroups a
-// sequence with their loads in flight at once.
+// 256 sequences over 2048 tokens, 16 heads of 128 sharing 2, bf16: 79 us, 5.0 TB/s (a copy of 2 GiB: 4.9).  3
+// sequences over 16384: 16 to 17 us and 4 for the join, of which 10 are the bytes at that rate: 384 workgroups, of
+// which a CU has room for one, so that half of them wait for the first.
 #include "gdn2_attn.h"
 
 namespace gdn2 {
@@ -223,8 +223,8 @@ __global__ __launch_bounds__(64 * kStepWaves, 1) void step_kernel(StepParams a) 
     }
 }
 
-// Parts of a sequence: as many as the GPU runs at once (two workgroups a CU; a further few would have it to
-// themselves when the others are done), of whole turns of the waves, and no more of them than those turns need.
+// Parts of a sequence: up to two workgroups a CU, of whole turns of the waves, and no more of them than those turns
+// need.  (LDS has room for two at once at 64 channels and for one at 128.)
 int step_splits(const AttnStepArgs& a) {
     const int64_t share = a.H / a.G, groups = a.N * a.G * ((share + 31) / 32);
     const int waves = kStepWaves;

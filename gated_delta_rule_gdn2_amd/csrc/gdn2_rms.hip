@@ -2,7 +2,7 @@
 // bits, and its gradients.
 //
 //   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd gamma
-//   8 bits (e4m3): scale = max|y| / 448 of a row (1 for a row of zeros), the output y / scale
+//   8 bits (e4m3): scale = max|y| / 448 of a row (1 for a row of zeros), the output y (448 / max|y|)
 //   (max|y| at least 2^-110)
 // and with u = h rstd, v = dy gamma:
 //   dx = dh + rstd (v - u mean(u v)),  dgamma = sum over rows of dy u.

@@ -698,8 +698,9 @@ gdn2_status_t gdn2_rotary(const void* q, const void* k, const float* freq, const
  *                                            pointer as residual
  *   rstd      [rows]         float32         out, for the backward pass; NULL to skip
  *
- * y and rstd are formed from the sum before it is rounded to h.  width may be any
- * value from 1 to 16384, rows any from 0 on.  eps >= 0.
+ * y and rstd are formed from the sum before it is rounded to h, the sum of squares in
+ * fp32: sizes below 2^63 / sqrt(width) are in its range.  width may be any value from
+ * 1 to 16384, rows any from 0 on.  eps >= 0.
  */
 gdn2_status_t gdn2_rms_norm(const void* x, const void* residual, const float* gamma, void* y, void* h,
                             float* rstd, int64_t rows, int64_t width, float eps, gdn2_dtype_t dtype,
@@ -707,7 +708,9 @@ gdn2_status_t gdn2_rms_norm(const void* x, const void* residual, const float* ga
 
 /* gdn2_rms_norm_fp8 -- the same with y in 8 bits (e4m3, [rows, width] bytes) and a scale for
  * each row (float32 [rows]): scale = max|y| / 448, or 1 for a row of zeros, and the byte is
- * the value nearest to y / scale.  (max|y| counts as 2^-110 if it is less and not zero.) */
+ * the value nearest to y (448 / max|y|), y and both products rounded to fp32: where y / scale
+ * is within 2^-22 of itself of the middle of two values it may be either.  (max|y| counts as
+ * 2^-110 if it is less and not zero.) */
 gdn2_status_t gdn2_rms_norm_fp8(const void* x, const void* residual, const float* gamma, void* y,
                                 float* scales, void* h, float* rstd, int64_t rows, int64_t width,
                                 float eps, gdn2_dtype_t dtype, gdn2_dtype_t residual_dtype, void* stream);
