@@ -77,7 +77,7 @@ __global__ __launch_bounds__(64 * kStepWaves, 1) void step_kernel(StepParams a) 
     const int heads = min((int)share - (int)hb * 32, 32);     // of the workgroup
     const int64_t head0 = (int64_t)kv * share + hb * 32;      // the first of them
     const int64_t pos = a.positions[n];
-    const int64_t seen = pos < 0 ? 0 : min(min(pos + 1, a.window), a.cache);  // tokens, the newest last
+    const int64_t seen = pos < 0 ? 0 : min(pos, min(a.window, a.cache) - 1) + 1;  // tokens, the newest last
     const int64_t newest = seen > 0 ? pos % a.cache : 0;      // its slot
     int64_t oldest = newest - seen + 1;
     if (oldest < 0) oldest += a.cache;

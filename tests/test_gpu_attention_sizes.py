@@ -52,6 +52,23 @@ def test_a_million_sequences_of_one_token():
     assert torch.equal(part, o[:256, 0])
 
 
+@pytest.mark.parametrize("window", [None, 20, (1 << 63) - 1])
+def test_step_at_the_last_position(window):
+    """Position 2^63 - 1 and the ones before it see as many tokens as any other."""
+    C, H, G, d = 50, 2, 1, 64
+    last = (1 << 63) - 1
+    places = [last, last - 1, last - 25, 3]
+    g = torch.Generator("cpu").manual_seed(8)
+    q, k, v, kc, vc = (torch.randn(s, generator=g).to(BF16) for s in ((4, H, d), (4, G, d), (4, G, d), (4, C, G, d), (4, C, G, d)))
+    k2, v2 = kc.cuda(), vc.cuda()
+    o = gdn2.attn_step(q.cuda(), k.cuda(), v.cuda(), k2, v2, torch.tensor(places, device="cuda"), window=window)
+    for i, p in enumerate(places):
+        kc[i, p % C], vc[i, p % C] = k[i], v[i]
+        tokens = [t % C for t in range(max(0, p + 1 - min(C, window or C)), p + 1)]
+        check_fwd(q[i:i + 1], kc[i, tokens], vc[i, tokens], o[i:i + 1], None)
+    assert torch.equal(k2.cpu(), kc) and torch.equal(v2.cpu(), vc)
+
+
 @pytest.mark.parametrize("tokens,H,d", [((1 << 27) - 8, 1, 2), ((1 << 25) - 8, 7, 32)])
 def test_rotary_of_the_most_tokens(tokens, H, d):
     """The first and the last tokens: angles of 2^27 radians are off by 2^-51 of themselves, 2^-24."""
