@@ -483,11 +483,12 @@ __device__ __forceinline__ Work uniform(const Work& w) {
 constexpr int64_t kTurn = 256;
 constexpr int64_t kMaxWork = (int64_t)1 << 23;  // blocks of all heads
 constexpr int64_t kMaxGrid = (int64_t)1 << 24;  // workgroups of 256 threads: a launch has less than 2^32
-// Fills in how work is dealt out; workgroups of the launch (0: none), or -1 if there is too much work.  Slices, and the
-// groups of the last round over the XCDs, that have no blocks make the launch larger than the work.  So many groups
-// of few blocks are cut into no more slices than they have blocks (1025 sequences of 60 tokens, 4 heads of 64 sharing
-// one: 53 us with 8 slices, 30 with one, the gradients 135 and 72), and slices are fewer where the launch would not fit.  Then it does: 8 blocks or more are less
-// than doubled by any slices, and 2^20 heads of fewer are 16 groups or more, which are less than doubled by none.
+// Fills in how work is dealt out; workgroups of the launch (0: none), or -1 if there is too much work.  Slices without
+// a block, and groups that are missing to a multiple of the XCDs, make the launch larger than the work.  So many
+// groups of few blocks are cut into no more slices than they have blocks (1025 sequences of 60 tokens, 4 heads of 64
+// sharing one: 53 us with 8 slices, 30 with one, the gradients 135 and 72), and slices are fewer where the launch
+// would not fit.  Then it does: 8 blocks or more are less than doubled by any slices, and 2^20 heads of fewer are 16
+// groups or more, which are less than doubled without.
 inline int64_t deal(Shape* p, int64_t tokens, int rows, int per_group) {
     const int64_t blocks = p->cu_q ? tokens / rows + p->n : (tokens + rows - 1) / rows;
     const int64_t groups = p->cu_q ? p->groups : p->n * p->groups;

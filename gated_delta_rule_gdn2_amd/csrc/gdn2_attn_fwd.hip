@@ -53,8 +53,8 @@ struct FwdParams {
 // see by zero, which infinities and NaN survive: the form that is not FIRST leaves out value by value what the mask
 // hides.  It keeps in `large` (in LDS, zero) whose outputs are not finite or large, of each wave's 32 queries; `damped`,
 // it scales their weights, and writes all outputs as they are.
-template <typename T, int D, int NW, int SW, bool FIRST, typename Word>
-__device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, Word* flag, Word* large, bool damped) {
+template <typename T, int D, int NW, int SW, bool FIRST>
+__device__ __forceinline__ bool fwd_block(const FwdParams& a, Lds base, GDN2_LDS unsigned* flag, GDN2_LDS unsigned* large, bool damped) {
     typedef Tile<T, D> L;
     static_assert(SW == 1 || SW == NW, "each wave its own queries, or all the same");
     constexpr int BK = kKeys<T, SW>, KS = D / 16, DT = D / 32, BM = NW / SW * 32, BYTES = BK * L::kRow;
@@ -294,12 +294,12 @@ __device__ __attribute__((noinline)) void fwd_again(FwdParams a, Lds base, GDN2_
 template <typename T, int D, int NW, int SW>
 __global__ __launch_bounds__(NW * 64, SW > 1 ? (kFwdLds<T, D, SW> > 80000 ? 1 : 2) : D == 64 ? 3 : 2) void fwd_kernel(FwdParams a) {
     __shared__ __attribute__((aligned(1024))) char lds[kFwdLds<T, D, SW>];
-    __shared__ unsigned any_again;  // of its own: no call gets its address, or the offsets would be no scalar loads
-    __shared__ unsigned outcome[1 + NW / SW];
-    if (threadIdx.x == 0) any_again = 0;
-    if (fwd_block<T, D, NW, SW, true>(a, lds_of(lds), &any_again, (unsigned*)nullptr, false)) {
+    __shared__ unsigned words[1 + NW / SW];
+    GDN2_LDS unsigned* outcome = (GDN2_LDS unsigned*)words;
+    if (threadIdx.x == 0) *outcome = 0;
+    if (fwd_block<T, D, NW, SW, true>(a, lds_of(lds), outcome, nullptr, false)) {
         __syncthreads();
-        fwd_again<T, D, NW, SW>(a, lds_of(lds), (GDN2_LDS unsigned*)outcome);
+        fwd_again<T, D, NW, SW>(a, lds_of(lds), outcome);
     }
 }
 
